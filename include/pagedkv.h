@@ -41,6 +41,10 @@
  *     the offending access is skipped or redirected to block 0, the result is
  *     undefined, and a PKV_DEV_* flag is raised in a per-device status word
  *     read by pkv_device_status().
+ *   - Strides given as int64_t count elements.  Accumulated attention weights
+ *     are fp32 [num_seqs, num_kv_heads, >= the contexts] with weights_stride
+ *     elements between rows: weights[s][h][t] belongs to position t of batch
+ *     row s, whatever blocks the position lives in.
  *   - The kernels never spin on another block or another launch.  Apart from
  *     the wait for the previous kernel on the stream described above, the
  *     only waits are on their own copies into shared memory, each bounded in
@@ -79,6 +83,7 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1 } pkv_dtype_t;
 #define PKV_DEV_BAD_CONTEXT_LEN 2u  /* context_lens[s] < 0 or > max_context_len or > table row */
 #define PKV_DEV_BAD_SLOT 4u         /* slot_mapping[t] >= num_blocks * block_size */
 #define PKV_DEV_WAIT_TIMEOUT 8u     /* a bounded wait inside a kernel gave up (never expected) */
+#define PKV_DEV_BAD_KEEP 16u        /* keep[i] < i or not a position of the sequence */
 
 /* Human-readable name of a status code (static string). */
 const char* pkv_status_string(pkv_status_t status);
@@ -367,6 +372,150 @@ pkv_status_t pkv_block_copy(
     void* k_cache, void* v_cache, const int64_t* src_dst_pairs, int num_pairs,
     int num_blocks, size_t block_bytes, pkv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A cache smaller than the history.
+ *
+ * [P3] "Eviction and reuse can move costs elsewhere": a sequence that outgrows
+ * its share of the pool drops cached positions.  The calls below keep it
+ * going: rotary positions applied as new rows are appended (a token's position
+ * then no longer has to be its index in the cache), attention that also
+ * accumulates how much weight each cached position received, the choice of
+ * the positions to keep, and the move of their rows to the front, after which
+ * pkv_alloc_shrink_seqs returns the blocks behind them to the pool.
+ * ---------------------------------------------------------------------- */
+
+/* Rotary positions with append, in one launch.
+ *
+ * For each token t with pos = positions[t] >= 0, each pair i < rot_dim / 2 of
+ * every head row of q and k is turned by the angle a = pos * inv_freq[i]:
+ *   first'  = attn_factor * (first cos a - second sin a)
+ *   second' = attn_factor * (first sin a + second cos a)
+ * with (first, second) the elements (2i, 2i + 1) if interleaved, else
+ * (i, i + rot_dim / 2); elements from rot_dim on are copied.  The angle is
+ * formed in 64 bits, the products in fp32, and each result is rounded once to
+ * dtype.  q goes to q_out; k and v (v unturned) go to slot slot_mapping[t], as
+ * pkv_kv_append.  A token with a negative position is padding: nothing is
+ * written for it.  A negative slot skips k and v only.  A slot at or beyond
+ * num_blocks * block_size does so too and flags PKV_DEV_BAD_SLOT.
+ *
+ *   q_out, q      [num_tokens, num_q_heads, head_dim] dtype, tokens *_stride
+ *                 elements apart (a multiple of 8, at least a token's row, so
+ *                 that slices of a joint projection need no copy); q_out may
+ *                 be q with the same stride, and must not overlap it otherwise
+ *   k, v          [num_tokens, num_kv_heads, head_dim] likewise
+ *   positions     int32 [num_tokens]
+ *   inv_freq      double [rot_dim / 2], radians per position, scaled for long
+ *                 contexts as the model wants
+ *   rot_dim       even, 2 .. head_dim
+ *   slot_mapping  int64 [num_tokens], distinct where not negative
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (head_dim or block_size not
+ * built, 65,536 heads or more), PKV_ERR_CUDA. */
+pkv_status_t pkv_rope_kv_append(
+    void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+    const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+    const int32_t* positions, const double* inv_freq, int rot_dim, int interleaved,
+    float attn_factor, void* k_cache, void* v_cache, const int64_t* slot_mapping,
+    int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, pkv_dtype_t dtype, pkv_stream_t stream);
+
+/* Decode attention that accumulates attention weights: pkv_paged_attn_decode,
+ * and for every KV head h and position t < context_lens[s]
+ *   weights[s][h][t] = decay * weights[s][h][t] + sum_g p_g(t)
+ * over the softmax weights p_g of the query heads g that read h (fp32; decay 0
+ * overwrites without reading).  Positions at or beyond context_lens[s] keep
+ * their values.  Runs the tensor-core kernel: groups of at most 32 query
+ * heads, partition_size 0 or a multiple of 128 (PKV_ERR_UNSUPPORTED
+ * otherwise; pkv_paged_attn_prefill_weights takes larger groups, one query per
+ * sequence), whatever pkv_set_decode_path says.
+ *   weights_stride  >= max_context_len
+ *   workspace       pkv_decode_weights_workspace_size(...) bytes, which is
+ *                   never 0: the step's logits are kept there
+ * Everything else as pkv_paged_attn_decode. */
+pkv_status_t pkv_paged_attn_decode_weights(
+    void* out, float* weights, int64_t weights_stride, float decay,
+    const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len,
+    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, pkv_dtype_t dtype,
+    int partition_size, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream);
+
+/* (size_t)-1 for invalid arguments or sizes the call does not support. */
+size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int max_context_len, int partition_size);
+
+/* Chunked-prompt attention that accumulates attention weights:
+ * pkv_paged_attn_prefill, and for every sequence with L_s > 0 queries, every
+ * KV head h and position t < context_lens[s]
+ *   weights[s][h][t] = decay * weights[s][h][t] + sum_j sum_g p_{j,g}(t)
+ * over the last min(window, L_s) queries j (window 0: all of them) and the
+ * query heads g that read h.  The sums run in a fixed order (the same bits on
+ * every call).  A sequence without queries keeps its weights.
+ *   weights_stride  >= max_context_len
+ *   workspace       pkv_prefill_weights_workspace_size(...) bytes
+ * Everything else as pkv_paged_attn_prefill. */
+pkv_status_t pkv_paged_attn_prefill_weights(
+    void* out, float* weights, int64_t weights_stride, float decay, int window,
+    const void* q, int total_queries, const int32_t* query_start, int max_query_len,
+    const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len,
+    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, pkv_dtype_t dtype,
+    void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* (size_t)-1 for invalid arguments. */
+size_t pkv_prefill_weights_workspace_size(int total_queries, int num_q_heads);
+
+/* The positions to keep, per sequence and KV head.
+ *
+ * With n = context_lens[s]: if n <= budget, keep[s][h] = 0 .. n - 1.  Otherwise
+ * the first `sinks` positions, the last `recent` ones, and of the others the
+ * budget - sinks - recent with the largest weights (of equal weights the
+ * lowest positions; NaN ranks below everything), in ascending order.  Entries
+ * past min(n, budget) are -1.  new_lens[s] = min(n, budget) if new_lens is not
+ * NULL (another array than context_lens).
+ *
+ *   keep          int32 [num_seqs, num_kv_heads, budget]
+ *   weights       fp32, weights_stride >= max_context_len
+ *   sinks, recent >= 0 with sinks + recent <= budget */
+pkv_status_t pkv_kv_evict_select(
+    int32_t* keep, int32_t* new_lens, const float* weights, int64_t weights_stride,
+    const int32_t* context_lens, int max_context_len, int num_seqs, int num_kv_heads,
+    int budget, int recent, int sinks, pkv_stream_t stream);
+
+/* Move the kept rows of every sequence and KV head to its front.
+ *
+ * For i < min(context_lens[s], budget): position i of (s, h) receives the K
+ * and V rows of position keep[s][h][i], read through src_tables and written
+ * through dst_tables (a byte copy: bit-exact), and weights[s][h][i] receives
+ * weights[s][h][keep[s][h][i]]; the weights of the positions from there to
+ * context_lens[s] become 0.  keep has to ascend strictly.  An entry below its
+ * index or outside the sequence is skipped and flags PKV_DEV_BAD_KEEP.
+ *
+ * dst_tables may be src_tables (rows move in place), or name another block
+ * where a source block is shared ([P3] "Shared prefixes need ownership
+ * rules"): pkv_alloc_shrink_seqs gives every shared block of the kept part a
+ * fresh one.  A destination block must belong to one sequence, and must not be
+ * a source block of another sequence or of another place of the same one.
+ *
+ *   src_tables    int32 [num_seqs, max_blocks_per_seq], the blocks of
+ *                 context_lens[s] positions
+ *   dst_tables    int32 [num_seqs, dst_blocks_per_seq], dst_blocks_per_seq *
+ *                 block_size >= min(budget, the longest context)
+ *   keep          int32 [num_seqs, num_kv_heads, budget]
+ *   context_lens  the lengths before the eviction, each at most
+ *                 max_context_len
+ *   weights       fp32 or NULL, weights_stride >= max_context_len */
+pkv_status_t pkv_kv_compact(
+    void* k_cache, void* v_cache, float* weights, int64_t weights_stride,
+    const int32_t* src_tables, int max_blocks_per_seq,
+    const int32_t* dst_tables, int dst_blocks_per_seq,
+    const int32_t* keep, int budget, const int32_t* context_lens, int max_context_len,
+    int num_seqs, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+    pkv_dtype_t dtype, pkv_stream_t stream);
+
 /* Read (and optionally clear) the status word of the current device.
  * Synchronises `stream` first so that flags from work already enqueued on it
  * are visible.  flags may be NULL when only clearing. */
@@ -440,6 +589,16 @@ pkv_status_t pkv_alloc_append_slots(pkv_allocator* a, const int64_t* seq_ids, in
                                     int64_t* slots, int64_t* cow_pairs, int* num_pairs);
 /* Drop a sequence (finish or cancel); blocks reaching count 0 are freed. */
 pkv_status_t pkv_alloc_free_seq(pkv_allocator* a, int64_t seq_id);
+/* Shorten sequences to new_lens[i] <= their length, after an eviction.  The
+ * blocks behind the new length are dropped, and a sequence that gets shorter
+ * receives a fresh block in the place of every kept block that was shared when
+ * the call began (another owner keeps that one; pkv_kv_compact writes every
+ * row of the fresh block, so no pair to copy results).  All fresh blocks are
+ * taken before any is freed, so a block the batch reads from never becomes one
+ * it writes to.  All or nothing; a sequence id may appear once per batch
+ * (PKV_ERR_INVALID_ARG otherwise). */
+pkv_status_t pkv_alloc_shrink_seqs(pkv_allocator* a, const int64_t* seq_ids, int n,
+                                   const int64_t* new_lens);
 /* Host int32 rows [n, max_blocks] of physical ids, padded with -1. */
 pkv_status_t pkv_alloc_block_table(pkv_allocator* a, const int64_t* seq_ids, int n,
                                    int32_t* out, int max_blocks);

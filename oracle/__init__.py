@@ -24,10 +24,12 @@ Modules:
 * :mod:`oracle.attention` — paged single-query decode attention and paged
   multi-query (chunked prompt) attention in fp64.
 * :mod:`oracle.cache_ops` — the slot scatter (append) and block copy.
+* :mod:`oracle.evict` — rotary positions, accumulated attention weights, the
+  choice of the positions to keep and the compaction of a cache to them.
 * :mod:`oracle.allocator` — a pure-Python refcounted block allocator model.
 
-Every function here is pinned by ``tests/test_oracle_pins.py`` and
-``tests/test_oracle_allocator.py`` to facts and invariants that do not come
+Every function here is pinned by ``tests/test_oracle_pins.py``,
+``tests/test_oracle_evict.py`` and ``tests/test_oracle_allocator.py`` to facts and invariants that do not come
 from the oracle itself; no function is "parity unpinned".
 """
 
@@ -39,4 +41,6 @@ from .facts import (  # noqa: F401
 from .attention import (  # noqa: F401
     paged_decode_attention, paged_prefill_attention, gather_sequence_kv)
 from .cache_ops import kv_append, block_copy  # noqa: F401
+from .evict import (  # noqa: F401
+    rope, attention_weights, evict_select, compact, compact_weights)
 from .allocator import OracleAllocator, OracleOutOfBlocks  # noqa: F401

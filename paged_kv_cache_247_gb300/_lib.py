@@ -24,6 +24,7 @@ STATUS = {
 }
 PKV_F16, PKV_BF16 = 0, 1
 DEV_BAD_BLOCK_ID, DEV_BAD_CONTEXT_LEN, DEV_BAD_SLOT, DEV_WAIT_TIMEOUT = 1, 2, 4, 8
+DEV_BAD_KEEP = 16
 
 
 class AllocStats(ctypes.Structure):
@@ -63,6 +64,26 @@ SIGNATURES = {
     "pkv_kv_append": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                               c_int, c_int, c_int, c_int, c_void_p]),
     "pkv_block_copy": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_size_t, c_void_p]),
+    "pkv_rope_kv_append": (c_int, [
+        c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+        c_void_p, c_int, c_int, c_float, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+        c_int, c_int, c_int, c_void_p]),
+    "pkv_paged_attn_decode_weights": (c_int, [
+        c_void_p, c_void_p, c_int64, c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+        c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_int, c_int,
+        c_void_p, c_size_t, c_void_p]),
+    "pkv_decode_weights_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "pkv_paged_attn_prefill_weights": (c_int, [
+        c_void_p, c_void_p, c_int64, c_float, c_int, c_void_p, c_int, c_void_p, c_int, c_void_p,
+        c_void_p, c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+        c_float, c_int, c_void_p, c_size_t, c_void_p]),
+    "pkv_prefill_weights_workspace_size": (c_size_t, [c_int, c_int]),
+    "pkv_kv_evict_select": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int,
+        c_void_p]),
+    "pkv_kv_compact": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
+        c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),
     "pkv_device_status": (c_int, [P_u32, c_int, c_void_p]),
     "pkv_debug_wait_timeout": (c_int, [c_void_p]),
     "pkv_alloc_create": (c_int, [c_int, c_int, ctypes.POINTER(c_void_p)]),
@@ -74,6 +95,7 @@ SIGNATURES = {
     # costs half as much per call as building typed pointers
     "pkv_alloc_append_slots": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, P_int]),
     "pkv_alloc_free_seq": (c_int, [c_void_p, c_int64]),
+    "pkv_alloc_shrink_seqs": (c_int, [c_void_p, c_void_p, c_int, c_void_p]),
     "pkv_alloc_block_table": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int]),
     "pkv_alloc_seq_slots": (c_int, [c_void_p, c_int64, c_int, c_int, c_void_p]),
     "pkv_alloc_seq_info": (c_int, [c_void_p, c_int64, P_int, P_int]),

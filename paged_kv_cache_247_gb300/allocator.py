@@ -70,6 +70,16 @@ class BlockAllocator:
     def free_seq(self, seq_id):
         self._check(self._lib.pkv_alloc_free_seq(self._h, seq_id), "free_seq")
 
+    def shrink_seqs(self, seq_ids, new_lens):
+        """Shorten sequences after an eviction (see pkv_alloc_shrink_seqs);
+        read their source tables before and their new ones after this call."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        lens = np.ascontiguousarray(new_lens, dtype=np.int64)
+        if ids.ndim != 1 or lens.shape != ids.shape:
+            raise ValueError("new_lens must have one entry per sequence")
+        self._check(self._lib.pkv_alloc_shrink_seqs(self._h, _addr(ids), len(ids), _addr(lens)),
+                    "shrink_seqs")
+
     def block_table(self, seq_ids, max_blocks):
         ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
         out = np.empty((len(ids), max_blocks), dtype=np.int32)

@@ -17,6 +17,8 @@
 #include <algorithm>
 #include <new>
 #include <unordered_map>
+#include <unordered_set>
+#include <utility>
 #include <vector>
 
 #include "pagedkv.h"
@@ -188,6 +190,50 @@ pkv_status_t pkv_alloc_free_seq(pkv_allocator* a, int64_t seq_id) {
   const std::vector<int32_t>& t = it->second.table;
   for (auto b = t.rbegin(); b != t.rend(); ++b) a->release(*b);
   a->seqs.erase(it);
+  return PKV_OK;
+}
+
+pkv_status_t pkv_alloc_shrink_seqs(pkv_allocator* a, const int64_t* seq_ids, int n,
+                                   const int64_t* new_lens) {
+  if (!a || n < 0 || (n > 0 && (!seq_ids || !new_lens))) return PKV_ERR_INVALID_ARG;
+  // Check everything, then take every fresh block, then release: a block that
+  // one sequence of the batch gives up is not handed to another one of it.
+  // Everything that may run out of host memory comes before the first change.
+  std::vector<std::pair<pkv_allocator::Seq*, size_t>> fresh;  // (sequence, logical block)
+  std::vector<int32_t> given_up;                              // one owner less each
+  try {
+    std::unordered_set<int64_t> seen;
+    for (int i = 0; i < n; ++i) {
+      auto it = a->seqs.find(seq_ids[i]);
+      if (it == a->seqs.end()) return PKV_ERR_UNKNOWN_SEQ;
+      pkv_allocator::Seq& s = it->second;
+      if (new_lens[i] < 0 || new_lens[i] > s.length || !seen.insert(seq_ids[i]).second)
+        return PKV_ERR_INVALID_ARG;
+      if (new_lens[i] == s.length) continue;
+      const size_t kept = static_cast<size_t>(a->blocks_for(new_lens[i], a->block_size));
+      for (size_t b = 0; b < kept; ++b)
+        if (a->refcount[s.table[b]] > 1) fresh.emplace_back(&s, b);
+    }
+    given_up.reserve(fresh.size());
+  } catch (const std::bad_alloc&) {
+    return PKV_ERR_OUT_OF_BLOCKS;
+  }
+  if (fresh.size() > a->free_list.size()) return PKV_ERR_OUT_OF_BLOCKS;
+  for (const auto& f : fresh) {
+    given_up.push_back(f.first->table[f.second]);
+    f.first->table[f.second] = a->take();
+    ++a->cow_copies;
+  }
+  for (int i = 0; i < n; ++i) {
+    pkv_allocator::Seq& s = a->seqs.find(seq_ids[i])->second;
+    const size_t kept = static_cast<size_t>(a->blocks_for(new_lens[i], a->block_size));
+    while (s.table.size() > kept) {
+      a->release(s.table.back());
+      s.table.pop_back();
+    }
+    s.length = new_lens[i];
+  }
+  for (int32_t b : given_up) a->release(b);
   return PKV_OK;
 }
 

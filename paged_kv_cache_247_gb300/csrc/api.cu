@@ -317,6 +317,46 @@ size_t pkv_decode_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads
 
 namespace {
 
+// Accumulated attention weights of an attention call.
+struct WeightsArgs {
+  float* weights;
+  int64_t stride;
+  float decay;
+  int window;
+  void* workspace;
+  size_t workspace_bytes;
+};
+
+// Contexts the calls with 32-bit position arithmetic beyond a tile take.
+constexpr int kMaxPositions = 1 << 30;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+pkv_status_t check_weights(const WeightsArgs& w, int max_context_len) {
+  if (!w.weights || !aligned4(w.weights) || w.stride < max_context_len || !isfinite(w.decay))
+    return PKV_ERR_INVALID_ARG;
+  return max_context_len > kMaxPositions ? PKV_ERR_UNSUPPORTED : PKV_OK;
+}
+
+// Workspace of the decode call with weights: the partials when the context is
+// split, every partition's maximum and sum, and the step's logits, rows
+// 16-byte aligned.
+struct DecodeWeightsLayout {
+  size_t m, x, floats;  // offsets of ws_m and ws_x, and the whole, in floats
+  long long x_stride;
+};
+
+DecodeWeightsLayout decode_weights_layout(int num_seqs, int num_q_heads, int head_dim,
+                                          int max_context_len, long long parts) {
+  DecodeWeightsLayout l{};
+  const size_t pairs = (size_t)num_seqs * num_q_heads, rows = pairs * parts;
+  l.x_stride = ((long long)max_context_len + 3) / 4 * 4;
+  l.m = parts > 1 ? rows * head_dim : 0;
+  l.x = (l.m + 2 * rows + 3) / 4 * 4;
+  l.floats = l.x + pairs * l.x_stride;
+  return l;
+}
+
 // Shared body of the paged decode calls.  k_new/v_new (both or neither) are
 // the step's new-token rows [num_seqs, num_kv_heads, head_dim] for the fused
 // append.
@@ -326,7 +366,8 @@ pkv_status_t paged_decode_impl(void* out, const void* q, const void* k_new, cons
                                int max_context_len, int num_seqs, int num_q_heads,
                                int num_kv_heads, int head_dim, int block_size, int num_blocks,
                                float scale, pkv_dtype_t dtype, int partition_size,
-                               void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+                               void* workspace, size_t workspace_bytes, pkv_stream_t stream,
+                               const WeightsArgs* wa = nullptr) {
   if (!decode_shape_ok(num_seqs, num_q_heads, num_kv_heads, max_context_len))
     return PKV_ERR_INVALID_ARG;
   if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
@@ -348,8 +389,15 @@ pkv_status_t paged_decode_impl(void* out, const void* q, const void* k_new, cons
 
   const int group = num_q_heads / num_kv_heads;
   const int gt = pkv::decode_heads_per_cta(group);
-  const DecodePlan plan = decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                      max_context_len, partition_size);
+  DecodePlan plan = decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                                partition_size);
+  if (wa) {
+    const pkv_status_t st = check_weights(*wa, max_context_len);
+    if (st != PKV_OK) return st;
+    plan = {true, partition_size ? partition_size
+                                 : tc_partition(num_seqs, num_kv_heads, max_context_len)};
+    if (!pkv::decode_tc_supported(head_dim, group, plan.partition)) return PKV_ERR_UNSUPPORTED;
+  }
   const int head_chunks = plan.tc ? 1 : (group + gt - 1) / gt;
   const int part = plan.partition;
   const long long parts = num_parts_for(max_context_len, part);
@@ -381,7 +429,22 @@ pkv_status_t paged_decode_impl(void* out, const void* q, const void* k_new, cons
   p.partition_size = part;
   p.num_parts = (int)parts;
   p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax is evaluated with exp2
-  if (parts > 1) {
+  if (wa) {
+    const DecodeWeightsLayout l =
+        decode_weights_layout(num_seqs, num_q_heads, head_dim, max_context_len, parts);
+    if (!workspace || workspace_bytes < l.floats * sizeof(float))
+      return PKV_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+    float* ws = static_cast<float*>(workspace);
+    p.ws_o = ws;
+    p.ws_m = ws + l.m;
+    p.ws_l = p.ws_m + (size_t)num_seqs * num_q_heads * parts;
+    p.ws_x = ws + l.x;
+    p.x_stride = l.x_stride;
+    p.weights = wa->weights;
+    p.weights_stride = wa->stride;
+    p.decay = wa->decay;
+  } else if (parts > 1) {
     const size_t need = (size_t)num_seqs * num_q_heads * parts * (head_dim + 2) * sizeof(float);
     if (!workspace || workspace_bytes < need) return PKV_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
@@ -407,6 +470,8 @@ pkv_status_t paged_decode_impl(void* out, const void* q, const void* k_new, cons
     err = pkv::launch_paged_decode_tc(p, dtype, head_dim, ctas,
                                       reinterpret_cast<cudaStream_t>(stream), &unsupported);
     if (unsupported) return PKV_ERR_UNSUPPORTED;
+    if (wa && err == cudaSuccess && max_context_len > 0)
+      err = pkv::launch_decode_weights(p, reinterpret_cast<cudaStream_t>(stream));
   } else {
     err = pkv::launch_paged_decode(p, dtype, head_dim, gt,
                                    reinterpret_cast<cudaStream_t>(stream));
@@ -447,6 +512,32 @@ pkv_status_t pkv_paged_attn_decode_append(void* out, const void* q, const void* 
                            max_blocks_per_seq, context_lens, max_context_len, num_seqs,
                            num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                            dtype, partition_size, workspace, workspace_bytes, stream);
+}
+
+size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int max_context_len, int partition_size) {
+  if (!decode_shape_ok(num_seqs, num_q_heads, num_kv_heads, max_context_len)) return (size_t)-1;
+  if (partition_size < 0 || max_context_len > kMaxPositions) return (size_t)-1;
+  const int part = partition_size ? partition_size
+                                  : tc_partition(num_seqs, num_kv_heads, max_context_len);
+  if (!pkv::decode_tc_supported(head_dim, num_q_heads / num_kv_heads, part)) return (size_t)-1;
+  return decode_weights_layout(num_seqs, num_q_heads, head_dim, max_context_len,
+                               num_parts_for(max_context_len, part)).floats * sizeof(float);
+}
+
+pkv_status_t pkv_paged_attn_decode_weights(
+    void* out, float* weights, int64_t weights_stride, float decay, const void* q,
+    const void* k_cache, const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    pkv_dtype_t dtype, int partition_size, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream) {
+  const WeightsArgs wa{weights, weights_stride, decay, 0, workspace, workspace_bytes};
+  return paged_decode_impl(out, q, nullptr, nullptr, const_cast<void*>(k_cache),
+                           const_cast<void*>(v_cache), block_tables, max_blocks_per_seq,
+                           context_lens, max_context_len, num_seqs, num_q_heads, num_kv_heads,
+                           head_dim, block_size, num_blocks, scale, dtype, partition_size,
+                           workspace, workspace_bytes, stream, &wa);
 }
 
 pkv_status_t pkv_contiguous_attn_decode(void* out, const void* q, const void* k_cache,
@@ -516,14 +607,17 @@ pkv_status_t pkv_contiguous_attn_decode(void* out, const void* q, const void* k_
   return PKV_OK;
 }
 
-pkv_status_t pkv_paged_attn_prefill(void* out, const void* q, int total_queries,
-                                    const int32_t* query_start, int max_query_len,
-                                    const void* k_cache, const void* v_cache,
-                                    const int32_t* block_tables, int max_blocks_per_seq,
-                                    const int32_t* context_lens, int max_context_len,
-                                    int num_seqs, int num_q_heads, int num_kv_heads,
-                                    int head_dim, int block_size, int num_blocks, float scale,
-                                    pkv_dtype_t dtype, pkv_stream_t stream) {
+namespace {
+
+// Shared body of the prompt-chunk calls.
+pkv_status_t paged_prefill_impl(void* out, const void* q, int total_queries,
+                                const int32_t* query_start, int max_query_len,
+                                const void* k_cache, const void* v_cache,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* context_lens, int max_context_len, int num_seqs,
+                                int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                int num_blocks, float scale, pkv_dtype_t dtype,
+                                pkv_stream_t stream, const WeightsArgs* wa = nullptr) {
   if (!decode_shape_ok(num_seqs, num_q_heads, num_kv_heads, max_context_len))
     return PKV_ERR_INVALID_ARG;
   if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
@@ -545,6 +639,20 @@ pkv_status_t pkv_paged_attn_prefill(void* out, const void* q, int total_queries,
   if ((long long)num_blocks * num_kv_heads * block_size > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
 
   pkv::PrefillArgs a{};
+  if (wa) {
+    const pkv_status_t st = check_weights(*wa, max_context_len);
+    if (st != PKV_OK) return st;
+    if (wa->window < 0) return PKV_ERR_INVALID_ARG;
+    if (!wa->workspace ||
+        wa->workspace_bytes < pkv_prefill_weights_workspace_size(total_queries, num_q_heads))
+      return PKV_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(wa->workspace)) return PKV_ERR_INVALID_ARG;
+    a.lse = static_cast<float*>(wa->workspace);
+    a.weights = wa->weights;
+    a.weights_stride = wa->stride;
+    a.window = wa->window;
+    a.decay = wa->decay;
+  }
   a.out = out;
   a.q = q;
   a.total_queries = total_queries;
@@ -569,9 +677,186 @@ pkv_status_t pkv_paged_attn_prefill(void* out, const void* q, int total_queries,
   a.sm_count = sm_count() > 0 ? sm_count() : kAssumedSms;
   bool unsupported = false;
   err = pkv::launch_paged_prefill(a, reinterpret_cast<cudaStream_t>(stream), &unsupported);
+  if (wa && err == cudaSuccess && !unsupported)
+    err = pkv::launch_prefill_weights(a, reinterpret_cast<cudaStream_t>(stream), &unsupported);
   if (unsupported) return PKV_ERR_UNSUPPORTED;
   if (err != cudaSuccess) return cuda_fail(err);
   return PKV_OK;
+}
+
+}  // namespace
+
+pkv_status_t pkv_paged_attn_prefill(void* out, const void* q, int total_queries,
+                                    const int32_t* query_start, int max_query_len,
+                                    const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, int max_blocks_per_seq,
+                                    const int32_t* context_lens, int max_context_len,
+                                    int num_seqs, int num_q_heads, int num_kv_heads,
+                                    int head_dim, int block_size, int num_blocks, float scale,
+                                    pkv_dtype_t dtype, pkv_stream_t stream) {
+  return paged_prefill_impl(out, q, total_queries, query_start, max_query_len, k_cache, v_cache,
+                            block_tables, max_blocks_per_seq, context_lens, max_context_len,
+                            num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                            scale, dtype, stream);
+}
+
+size_t pkv_prefill_weights_workspace_size(int total_queries, int num_q_heads) {
+  if (total_queries < 0 || num_q_heads <= 0) return (size_t)-1;
+  return (size_t)total_queries * num_q_heads * sizeof(float);
+}
+
+pkv_status_t pkv_paged_attn_prefill_weights(
+    void* out, float* weights, int64_t weights_stride, float decay, int window, const void* q,
+    int total_queries, const int32_t* query_start, int max_query_len, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    pkv_dtype_t dtype, void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  const WeightsArgs wa{weights, weights_stride, decay, window, workspace, workspace_bytes};
+  return paged_prefill_impl(out, q, total_queries, query_start, max_query_len, k_cache, v_cache,
+                            block_tables, max_blocks_per_seq, context_lens, max_context_len,
+                            num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                            scale, dtype, stream, &wa);
+}
+
+pkv_status_t pkv_rope_kv_append(void* q_out, int64_t q_out_stride, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const int32_t* positions,
+                                const double* inv_freq, int rot_dim, int interleaved,
+                                float attn_factor, void* k_cache, void* v_cache,
+                                const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                                int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                pkv_dtype_t dtype, pkv_stream_t stream) {
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (!isfinite(attn_factor)) return PKV_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (!supported_block_size(block_size)) return PKV_ERR_UNSUPPORTED;
+  if (num_q_heads > 65535 || num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2) return PKV_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PKV_OK;
+  if (!q_out || !q || !k || !v || !positions || !inv_freq || !k_cache || !v_cache || !slot_mapping)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(positions))
+    return PKV_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(inv_freq) | reinterpret_cast<uintptr_t>(slot_mapping)) & 7u)
+    return PKV_ERR_INVALID_ARG;
+  if ((q_out_stride | q_stride | k_stride | v_stride) % 8) return PKV_ERR_INVALID_ARG;
+  const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+  if (q_out_stride < q_row || q_stride < q_row || k_stride < kv_row || v_stride < kv_row)
+    return PKV_ERR_INVALID_ARG;
+  if (q_out == q && q_out_stride != q_stride) return PKV_ERR_INVALID_ARG;
+  pkv::RopeParams p{};
+  p.q_out = q_out;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out_stride = q_out_stride;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.slot_mapping = slot_mapping;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.num_slots = (long long)num_blocks * block_size;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.head_dim = head_dim;
+  p.block_size = block_size;
+  p.rot_dim = rot_dim;
+  p.interleaved = interleaved != 0;
+  p.factor = attn_factor;
+  cudaError_t err = status_word(&p.status);
+  if (err != cudaSuccess) return cuda_fail(err);
+  err = pkv::launch_rope_kv_append(p, num_tokens, dtype, reinterpret_cast<cudaStream_t>(stream));
+  return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
+}
+
+pkv_status_t pkv_kv_evict_select(int32_t* keep, int32_t* new_lens, const float* weights,
+                                 int64_t weights_stride, const int32_t* context_lens,
+                                 int max_context_len, int num_seqs, int num_kv_heads, int budget,
+                                 int recent, int sinks, pkv_stream_t stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || max_context_len < 0 || budget <= 0 || recent < 0 ||
+      sinks < 0 || (int64_t)recent + sinks > budget || weights_stride < max_context_len)
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs > 65535 || num_kv_heads > 65535 || max_context_len > kMaxPositions ||
+      budget > kMaxPositions)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PKV_OK;
+  if (!keep || !weights || !context_lens) return PKV_ERR_INVALID_ARG;
+  if (new_lens == context_lens) return PKV_ERR_INVALID_ARG;  // other heads still read it
+  if (!aligned4(keep) || !aligned4(new_lens) || !aligned4(weights) || !aligned4(context_lens))
+    return PKV_ERR_INVALID_ARG;
+  pkv::SelectParams p{};
+  p.keep = keep;
+  p.new_lens = new_lens;
+  p.weights = weights;
+  p.context_lens = context_lens;
+  p.weights_stride = weights_stride;
+  p.num_kv_heads = num_kv_heads;
+  p.max_context_len = max_context_len;
+  p.budget = budget;
+  p.recent = recent;
+  p.sinks = sinks;
+  cudaError_t err = status_word(&p.status);
+  if (err != cudaSuccess) return cuda_fail(err);
+  err = pkv::launch_kv_evict_select(p, num_seqs, reinterpret_cast<cudaStream_t>(stream));
+  return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
+}
+
+pkv_status_t pkv_kv_compact(void* k_cache, void* v_cache, float* weights, int64_t weights_stride,
+                            const int32_t* src_tables, int max_blocks_per_seq,
+                            const int32_t* dst_tables, int dst_blocks_per_seq,
+                            const int32_t* keep, int budget, const int32_t* context_lens,
+                            int max_context_len, int num_seqs, int num_kv_heads, int head_dim,
+                            int block_size, int num_blocks, pkv_dtype_t dtype,
+                            pkv_stream_t stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || max_context_len < 0 || budget <= 0 || num_blocks <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (!supported_block_size(block_size)) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535 || max_context_len > kMaxPositions ||
+      budget > kMaxPositions)
+    return PKV_ERR_UNSUPPORTED;
+  if (max_blocks_per_seq <= 0 || dst_blocks_per_seq <= 0 ||
+      (long long)max_blocks_per_seq * block_size < max_context_len ||
+      (long long)dst_blocks_per_seq * block_size < std::min(budget, max_context_len))
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !src_tables || !dst_tables || !keep || !context_lens)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(src_tables) ||
+      !aligned4(dst_tables) || !aligned4(keep) || !aligned4(context_lens))
+    return PKV_ERR_INVALID_ARG;
+  if (weights && (!aligned4(weights) || weights_stride < max_context_len))
+    return PKV_ERR_INVALID_ARG;
+  pkv::CompactParams p{};
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.weights = weights;
+  p.src_tables = src_tables;
+  p.dst_tables = dst_tables;
+  p.keep = keep;
+  p.context_lens = context_lens;
+  p.weights_stride = weights_stride;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.dst_blocks_per_seq = dst_blocks_per_seq;
+  p.max_len = max_context_len;
+  p.budget = budget;
+  p.num_kv_heads = num_kv_heads;
+  p.head_dim = head_dim;
+  p.block_size = block_size;
+  p.log2_block = log2_int(block_size);
+  p.num_blocks = num_blocks;
+  cudaError_t err = status_word(&p.status);
+  if (err != cudaSuccess) return cuda_fail(err);
+  err = pkv::launch_kv_compact(p, num_seqs, reinterpret_cast<cudaStream_t>(stream));
+  return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
 }
 
 pkv_status_t pkv_kv_append(const void* k, const void* v, void* k_cache, void* v_cache,

@@ -171,7 +171,9 @@ __device__ __forceinline__ bool group_any(int kg, bool v) {
 
 __device__ __forceinline__ void group_sync(int kg) { named_barrier_sync(1 + kg, 128); }
 
-template <typename T, int NH, int D>
+// kWeights: the logits and every item's (m, l) are kept for the accumulated
+// attention weights.
+template <typename T, int NH, int D, bool kWeights>
 __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
     paged_decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap,
@@ -483,6 +485,13 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
           x[g] *= qs;  // base-2 logit
           exceed |= valid && hb + g < G && x[g] > mref[g] + 8.f;
         }
+        if constexpr (kWeights) {
+          float* xr = p.ws_x + ((size_t)it.s * p.num_q_heads + h0 + hb) * p.x_stride +
+                      it.t_begin + i * kKeys + t;
+#pragma unroll
+          for (int g = 0; g < NHW; ++g)
+            if (valid && hb + g < G) xr[(size_t)g * p.x_stride] = x[g];
+        }
         if (group_any(kg, exceed)) {
           // Some key exceeds its head's running max by more than 8: the tile
           // maxima per head, then the heads whose maximum moves.
@@ -611,11 +620,13 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
             for (int g = 0; g < NHW; ++g)
               if (hb + g < G) dst[(size_t)g * D] = static_cast<T>(o[g] * inv[g]);
           } else {
-            const size_t r0 = row0 * p.num_parts + it.part;
-            float* dst = p.ws_o + r0 * D + d;
+            float* dst = p.ws_o + (row0 * p.num_parts + it.part) * D + d;
 #pragma unroll
             for (int g = 0; g < NHW; ++g)
               if (hb + g < G) dst[(size_t)g * p.num_parts * D] = o[g] * inv[g];
+          }
+          if (kWeights || it.nparts_seq > 1) {
+            const size_t r0 = row0 * p.num_parts + it.part;
             // Thread g writes head g's maximum and sum (one thread writing
             // them all took longer than the whole tile).
             float mg = 0.f, lg = 0.f;
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&o_free[ob]);
-        if (ok && mine && it.nparts_seq > 1) {
+        if (ok && mine && (kWeights || it.nparts_seq > 1)) {
           p.ws_m[r] = m;
           p.ws_l[r] = l;
         }
@@ -694,7 +705,7 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
   }
 }
 
-template <typename T, int NH, int D>
+template <typename T, int NH, int D, bool kWeights>
 cudaError_t launch_tc_typed(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                             const CUtensorMap& qm, int sms, cudaStream_t stream) {
   using L = TcShape<NH, D>;
@@ -703,28 +714,35 @@ cudaError_t launch_tc_typed(const DecodeParams& p, const CUtensorMap& km, const 
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    err = cudaFuncSetAttribute(paged_decode_tc_kernel<T, NH, D>,
+    err = cudaFuncSetAttribute(paged_decode_tc_kernel<T, NH, D, kWeights>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
     if (err != cudaSuccess) return err;
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
   const long long items = (long long)p.num_parts * p.num_kv_heads * p.num_seqs;
   const int grid = (int)(items < sms ? items : sms);
-  err = launch_overlapped(paged_decode_tc_kernel<T, NH, D>, dim3(grid), dim3(L::kThreads),
+  err = launch_overlapped(paged_decode_tc_kernel<T, NH, D, kWeights>, dim3(grid), dim3(L::kThreads),
                           L::kBytes, stream, p, km, vm, qm, (int)items);
   if (err != cudaSuccess || p.num_parts <= 1) return err;
   return launch_decode_reduce(p, std::is_same<T, __nv_bfloat16>::value ? PKV_BF16 : PKV_F16, D,
                               stream);
 }
 
+template <typename T, int NH, int D>
+cudaError_t launch_tc_heads(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+                            const CUtensorMap& qm, int sms, cudaStream_t stream) {
+  return p.ws_x ? launch_tc_typed<T, NH, D, true>(p, km, vm, qm, sms, stream)
+                : launch_tc_typed<T, NH, D, false>(p, km, vm, qm, sms, stream);
+}
+
 template <typename T, int D>
 cudaError_t launch_tc_group(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                             const CUtensorMap& qm, int sms, cudaStream_t stream) {
   static_assert(kMaxTcGroup == 32, "instantiations cover groups up to 32");
-  if (p.group <= 4) return launch_tc_typed<T, 4, D>(p, km, vm, qm, sms, stream);
-  if (p.group <= 8) return launch_tc_typed<T, 8, D>(p, km, vm, qm, sms, stream);
-  if (p.group <= 16) return launch_tc_typed<T, 16, D>(p, km, vm, qm, sms, stream);
-  return launch_tc_typed<T, 32, D>(p, km, vm, qm, sms, stream);
+  if (p.group <= 4) return launch_tc_heads<T, 4, D>(p, km, vm, qm, sms, stream);
+  if (p.group <= 8) return launch_tc_heads<T, 8, D>(p, km, vm, qm, sms, stream);
+  if (p.group <= 16) return launch_tc_heads<T, 16, D>(p, km, vm, qm, sms, stream);
+  return launch_tc_heads<T, 32, D>(p, km, vm, qm, sms, stream);
 }
 
 }  // namespace

@@ -35,6 +35,13 @@ struct DecodeParams {
   int partition_size;  // tokens per CTA (multiple of 32)
   int num_parts;       // ceil(max_context_len / partition_size), >= 1
   float qscale;        // scale * log2(e): logits are kept in base-2 units
+  // Accumulated attention weights (ws_x == nullptr: none; tensor-core kernel
+  // only).  ws_m and ws_l are then written for unsplit contexts too.
+  float* ws_x;             // base-2 logits [S, Hq, x_stride]
+  long long x_stride;
+  float* weights;          // [S, Hkv, weights_stride]
+  long long weights_stride;
+  float decay;
 };
 
 // Query heads one CTA processes for a group size (1, 2 or 4).
@@ -96,11 +103,111 @@ struct PrefillArgs {
   int dtype;
   unsigned int* status;
   int sm_count;  // SMs of the device (sizes the launch order's groups)
+  float* lse;    // base-2 log-sum of each row [total_queries, Hq] (nullptr: not wanted)
+  float* weights;  // accumulated attention weights [S, Hkv, weights_stride]
+  long long weights_stride;
+  int window;      // last queries of a chunk that count (0: all)
+  float decay;
 };
 
 // unsupported is set when the tensor maps of q or of the caches cannot be
 // encoded, or the work needs more CTAs than a 1-D grid holds.
 cudaError_t launch_paged_prefill(const PrefillArgs& a, cudaStream_t stream, bool* unsupported);
+
+// Accumulated attention weights of a decode step from ws_x, ws_m and ws_l.
+cudaError_t launch_decode_weights(const DecodeParams& p, cudaStream_t stream);
+
+struct PrefillWeightsParams {
+  const float* lse;
+  float* weights;
+  long long weights_stride;
+  float decay;
+  int window;
+  const int32_t* query_start;
+  const int32_t* context_lens;
+  const int32_t* block_tables;
+  unsigned int* status;
+  int max_blocks_per_seq;
+  int max_context_len;
+  int num_q_heads;
+  int num_kv_heads;
+  int group;
+  int group_pow2;
+  int block_size;
+  int num_blocks;
+  int total_queries;
+  float qscale;
+  int key_tiles;
+};
+
+// Accumulated attention weights of a prompt chunk, after launch_paged_prefill
+// with a.lse set.
+cudaError_t launch_prefill_weights(const PrefillArgs& a, cudaStream_t stream, bool* unsupported);
+
+// Rotary positions with append.  Strides are in elements, between tokens.
+struct RopeParams {
+  void* q_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_out_stride, q_stride, k_stride, v_stride;
+  const int32_t* positions;
+  const double* inv_freq;  // [rot_dim / 2]
+  const int64_t* slot_mapping;
+  void* k_cache;
+  void* v_cache;
+  unsigned int* status;
+  long long num_slots;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  int block_size;
+  int rot_dim;
+  int interleaved;
+  float factor;
+};
+
+cudaError_t launch_rope_kv_append(const RopeParams& p, int num_tokens, int dtype,
+                                  cudaStream_t stream);
+
+struct SelectParams {
+  int32_t* keep;           // [S, Hkv, budget]
+  int32_t* new_lens;       // [S] or nullptr
+  const float* weights;    // [S, Hkv, weights_stride]
+  const int32_t* context_lens;
+  unsigned int* status;
+  long long weights_stride;
+  int num_kv_heads;
+  int max_context_len;
+  int budget;
+  int recent;
+  int sinks;
+};
+
+cudaError_t launch_kv_evict_select(const SelectParams& p, int num_seqs, cudaStream_t stream);
+
+struct CompactParams {
+  void* k_cache;
+  void* v_cache;
+  float* weights;          // [S, Hkv, weights_stride] or nullptr
+  const int32_t* src_tables;
+  const int32_t* dst_tables;
+  const int32_t* keep;     // [S, Hkv, budget]
+  const int32_t* context_lens;
+  unsigned int* status;
+  long long weights_stride;
+  int max_blocks_per_seq;  // row strides of the two tables
+  int dst_blocks_per_seq;
+  int max_len;             // positions the source table and the weights rows hold
+  int budget;
+  int num_kv_heads;
+  int head_dim;
+  int block_size;
+  int log2_block;
+  int num_blocks;
+};
+
+cudaError_t launch_kv_compact(const CompactParams& p, int num_seqs, cudaStream_t stream);
 
 // kv_append indexes (token, 16-byte chunk) pairs with 32 bits: a call may move
 // at most this many chunks of K (and as many of V), 32 GiB each.

@@ -120,6 +120,7 @@ struct PrefillParams {
   int q_tiles;          // CTAs per (sequence, KV head)
   int pairs_per_group;  // (sequence, KV head) pairs whose items are launched together
   int total_queries;    // rows of q and out
+  float* lse;           // kLse: base-2 log-sum of each row [total_queries, Hq]
   int prefetch_stride;  // work items between a CTA and the one likely to follow it on its SM
 };
 
@@ -142,7 +143,8 @@ __device__ __forceinline__ uint32_t tile_chunk_offset(int r, int c) {
 
 // ---- the kernel -----------------------------------------------------------
 
-template <typename T, int D>
+// kLse: each row's log-sum is written for the accumulated attention weights.
+template <typename T, int D, bool kLse>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
     paged_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap,
@@ -562,6 +564,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (nt > 0 && ok && mbar_wait_warp(&pv_done[t], (nt - 1) & 1, p.status)) {
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      if constexpr (kLse) {
+        if (row_valid) p.lse[(size_t)(q0 + jq) * p.num_q_heads + kvh * G + g] = m_run + log2f(l_run);
+      }
       T* orow = static_cast<T*>(p.out) + row_elem;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -594,8 +599,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 
 // ---- host side ------------------------------------------------------------
 
-template <typename T, int D>
-cudaError_t launch_prefill_typed(const PrefillParams& p, const CUtensorMap& qm,
+template <typename T, int D, bool kLse>
+cudaError_t launch_prefill_lse(const PrefillParams& p, const CUtensorMap& qm,
                                  const CUtensorMap& km, const CUtensorMap& vm, int q_tiles,
                                  int num_seqs, cudaStream_t stream) {
   using L = PrefillSmem<D>;
@@ -604,14 +609,22 @@ cudaError_t launch_prefill_typed(const PrefillParams& p, const CUtensorMap& qm,
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    err = cudaFuncSetAttribute(paged_prefill_kernel<T, D>,
+    err = cudaFuncSetAttribute(paged_prefill_kernel<T, D, kLse>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
     if (err != cudaSuccess) return err;
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
   const dim3 grid((unsigned)((long long)q_tiles * p.num_kv_heads * num_seqs));
-  paged_prefill_kernel<T, D><<<grid, kPrefillThreads, L::kBytes, stream>>>(p, qm, km, vm);
+  paged_prefill_kernel<T, D, kLse><<<grid, kPrefillThreads, L::kBytes, stream>>>(p, qm, km, vm);
   return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_prefill_typed(const PrefillParams& p, const CUtensorMap& qm,
+                                 const CUtensorMap& km, const CUtensorMap& vm, int q_tiles,
+                                 int num_seqs, cudaStream_t stream) {
+  return p.lse ? launch_prefill_lse<T, D, true>(p, qm, km, vm, q_tiles, num_seqs, stream)
+               : launch_prefill_lse<T, D, false>(p, qm, km, vm, q_tiles, num_seqs, stream);
 }
 
 }  // namespace
@@ -659,6 +672,7 @@ cudaError_t launch_paged_prefill(const PrefillArgs& a, cudaStream_t stream, bool
   p.num_seqs = a.num_seqs;
   p.q_tiles = q_tiles;
   p.total_queries = a.total_queries;
+  p.lse = a.lse;
   p.prefetch_stride = std::max(1, a.sm_count);
   // About one wave of CTAs (one per SM) per group; the count only shapes
   // the order, not the result.

@@ -174,6 +174,112 @@ def paged_attn_prefill(out, q, query_start, k_cache, v_cache, block_tables, cont
     return out
 
 
+def _same_device(first, *rest):
+    """The tensors' common device (None entries are skipped)."""
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on one device")
+    return first.device
+
+
+def _attn_shapes(q, out, k_cache, v_cache, weights):
+    _cuda(q, "q", ndim=3)
+    dtype = q.dtype
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("q must be float16 or bfloat16")
+    _cuda(out, "out", dtype, 3)
+    _cuda(k_cache, "k_cache", dtype, 4)
+    _cuda(v_cache, "v_cache", dtype, 4)
+    if v_cache.shape != k_cache.shape or k_cache.shape[3] != q.shape[2] or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, out and the caches")
+
+
+def _weights(weights, num_seqs, num_kv_heads, max_context_len):
+    _cuda(weights, "weights", torch.float32, 3)
+    if (weights.shape[:2] != (num_seqs, num_kv_heads) or weights.shape[2] < max_context_len):
+        raise ValueError("weights must be [num_seqs, num_kv_heads, >= max_context_len]")
+
+
+def decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                                  partition_size=0):
+    """Bytes of scratch :func:`paged_attn_decode_weights` needs."""
+    n = _lib.load().pkv_decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                      head_dim, max_context_len, partition_size)
+    if n == _SIZE_T_MAX:
+        raise ValueError("invalid decode sizes")
+    return n
+
+
+def paged_attn_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens,
+                              scale, max_context_len, decay=1.0, partition_size=0,
+                              workspace=None):
+    """:func:`paged_attn_decode` that also accumulates attention weights:
+    ``weights`` (fp32 [S, Hkv, >= max_context_len]) becomes ``decay * weights``
+    plus each held position's softmax weight, summed over the query heads of
+    the KV head's group.  Groups of at most 32 query heads.  Writes ``out``
+    and returns it."""
+    _attn_shapes(q, out, k_cache, v_cache, weights)
+    _cuda(block_tables, "block_tables", torch.int32, 2)
+    _cuda(context_lens, "context_lens", torch.int32, 1)
+    S, Hq, D = q.shape
+    NB, Hkv, B, _ = k_cache.shape
+    _weights(weights, S, Hkv, max_context_len)
+    if block_tables.shape[0] != S or context_lens.shape[0] != S:
+        raise ValueError("block_tables / context_lens must have one row per sequence")
+    dev = _same_device(q, out, weights, k_cache, v_cache, block_tables, context_lens, workspace)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = torch.empty(
+                decode_weights_workspace_size(S, Hq, Hkv, D, max_context_len, partition_size),
+                dtype=torch.uint8, device=dev)
+        _cuda(workspace, "workspace")
+        st = _lib.load().pkv_paged_attn_decode_weights(
+            out.data_ptr(), weights.data_ptr(), weights.stride(1), float(decay), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), S, Hq, Hkv, D,
+            B, NB, float(scale), _DTYPE_CODE[q.dtype], int(partition_size), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(dev))
+    _lib.check(st, "pkv_paged_attn_decode_weights")
+    return out
+
+
+def paged_attn_prefill_weights(out, weights, q, query_start, k_cache, v_cache, block_tables,
+                               context_lens, scale, max_context_len, max_query_len, window=0,
+                               decay=1.0, workspace=None):
+    """:func:`paged_attn_prefill` that also accumulates attention weights:
+    ``weights`` (fp32 [S, Hkv, >= max_context_len]) becomes ``decay * weights``
+    plus each position's softmax weights, summed over the last ``window``
+    queries of its sequence's chunk (0: all) and the query heads of the KV
+    head's group.  ``workspace``: uint8, 4 bytes per query row and head.
+    Writes ``out`` and returns it."""
+    _attn_shapes(q, out, k_cache, v_cache, weights)
+    _cuda(block_tables, "block_tables", torch.int32, 2)
+    _cuda(context_lens, "context_lens", torch.int32, 1)
+    _cuda(query_start, "query_start", torch.int32, 1)
+    T, Hq, D = q.shape
+    NB, Hkv, B, _ = k_cache.shape
+    S = context_lens.shape[0]
+    _weights(weights, S, Hkv, max_context_len)
+    if block_tables.shape[0] != S or query_start.shape[0] != S + 1:
+        raise ValueError("block_tables / query_start must match context_lens")
+    dev = _same_device(q, out, weights, query_start, k_cache, v_cache, block_tables,
+                       context_lens, workspace)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = torch.empty(_lib.load().pkv_prefill_weights_workspace_size(T, Hq),
+                                    dtype=torch.uint8, device=dev)
+        _cuda(workspace, "workspace")
+        st = _lib.load().pkv_paged_attn_prefill_weights(
+            out.data_ptr(), weights.data_ptr(), weights.stride(1), float(decay), int(window),
+            q.data_ptr(), T, query_start.data_ptr(), int(max_query_len), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), int(max_context_len), S, Hq, Hkv, D, B, NB, float(scale),
+            _DTYPE_CODE[q.dtype], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(dev))
+    _lib.check(st, "pkv_paged_attn_prefill_weights")
+    return out
+
+
 def contiguous_attn_decode(out, q, k_cache, v_cache, context_lens, scale, partition_size=0,
                            workspace=None):
     """Decode over a contiguous cache ``[S, Hkv, capacity, D]`` (no block
@@ -230,6 +336,171 @@ def kv_append(k, v, k_cache, v_cache, slot_mapping):
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         slot_mapping.data_ptr(), T, Hkv, D, B, NB, _DTYPE_CODE[dtype], _stream_handle(k.device))
     _lib.check(st, "pkv_kv_append")
+
+
+def _token_rows(t, name, dtype):
+    """Element stride between the tokens of a [T, H, D] tensor whose token rows
+    are dense (a slice of a joint projection, say)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions")
+    T, H, D = t.shape
+    if T > 0 and H > 0 and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name} must have dense token rows")
+    # (a dimension of one entry may carry any stride)
+    return t.stride(0) if T > 1 else H * D
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=None,
+                     low=1.0, high=32.0, device="cuda"):
+    """Frequencies ``base ** (-2i / rot_dim)`` in radians per position for
+    :func:`rope_kv_append` (float64 [rot_dim / 2]), scaled for contexts
+    ``factor`` times as long as the model was trained on:
+
+    * ``None``: unscaled;
+    * ``"linear"``: every frequency divided by ``factor`` (positions are
+      interpolated);
+    * ``"base"``: the base raised by ``factor ** (rot_dim / (rot_dim - 2))``,
+      which leaves the highest frequency and divides the lowest by ``factor``;
+    * ``"bands"``: frequencies that turn at least ``high`` times over
+      ``original_len`` positions are kept, those that turn at most ``low``
+      times are divided by ``factor``, and between them the two are mixed
+      linearly in the number of turns.
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    i = np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError("scaling the base needs rot_dim of at least 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = base ** -i
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "bands":
+        if original_len is None or original_len <= 0 or not high > low:
+            raise ValueError("bands need original_len above 0 and high above low")
+        turns = original_len * freq / (2 * np.pi)
+        kept = np.clip((turns - low) / (high - low), 0.0, 1.0)
+        freq = freq * kept + freq / factor * (1.0 - kept)
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.from_numpy(freq).to(device)
+
+
+def rope_kv_append(q_out, q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping,
+                   interleaved=False, attn_factor=1.0):
+    """Rotary positions with append: ``q`` ([T, Hq, D]) turned into ``q_out``
+    (which may be ``q``), ``k`` turned and ``v`` ([T, Hkv, D]) written into
+    slot ``slot_mapping[t]`` (int64) of the caches.  ``positions`` (int32 [T]):
+    negative = padding, nothing is written; a negative slot skips k and v
+    only.  ``inv_freq``: float64 [rot_dim / 2] (:func:`rope_frequencies`);
+    dimensions from rot_dim on pass through.  Pairs are neighbours if
+    ``interleaved``, else rot_dim / 2 apart.  q, k, v and q_out may be slices
+    of wider token rows.  Returns ``q_out``."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE_CODE:
+        raise ValueError("q must be float16 or bfloat16")
+    dtype = q.dtype
+    strides = [_token_rows(t, n, dtype) for t, n in
+               ((q_out, "q_out"), (q, "q"), (k, "k"), (v, "v"))]
+    _cuda(k_cache, "k_cache", dtype, 4)
+    _cuda(v_cache, "v_cache", dtype, 4)
+    _cuda(positions, "positions", torch.int32, 1)
+    _cuda(inv_freq, "inv_freq", torch.float64, 1)
+    _cuda(slot_mapping, "slot_mapping", torch.int64, 1)
+    T, Hq, D = q.shape
+    NB, Hkv, B, D2 = k_cache.shape
+    if (q_out.shape != q.shape or k.shape != (T, Hkv, D) or v.shape != k.shape or D2 != D
+            or v_cache.shape != k_cache.shape):
+        raise ValueError("shape mismatch between q, q_out, the new rows and the caches")
+    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("positions / slot_mapping must have one entry per token")
+    dev = _same_device(q, q_out, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping)
+    with torch.cuda.device(dev):
+        st = _lib.load().pkv_rope_kv_append(
+            q_out.data_ptr(), strides[0], q.data_ptr(), strides[1], k.data_ptr(), strides[2],
+            v.data_ptr(), strides[3], positions.data_ptr(), inv_freq.data_ptr(),
+            2 * inv_freq.shape[0], 1 if interleaved else 0, float(attn_factor),
+            k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv, D, B, NB,
+            _DTYPE_CODE[dtype], _stream_handle(dev))
+    _lib.check(st, "pkv_rope_kv_append")
+    return q_out
+
+
+def kv_evict_select(keep, weights, context_lens, max_context_len, recent=0, sinks=0,
+                    new_lens=None):
+    """The positions each sequence and KV head keeps when it holds more than
+    ``keep.shape[2]`` (``keep``: int32 [S, Hkv, budget], written): the first
+    ``sinks``, the last ``recent`` and, of the others, those with the largest
+    ``weights`` (fp32 [S, Hkv, >= max_context_len]; equal weights: the lowest
+    positions), ascending, -1 past the end.  ``new_lens`` (int32 [S], not
+    ``context_lens`` itself) receives the lengths after the eviction.  Returns
+    ``keep``."""
+    _cuda(keep, "keep", torch.int32, 3)
+    S, Hkv, budget = keep.shape
+    _weights(weights, S, Hkv, max_context_len)
+    _cuda(context_lens, "context_lens", torch.int32, 1)
+    if new_lens is not None:
+        _cuda(new_lens, "new_lens", torch.int32, 1)
+    if context_lens.shape[0] != S or (new_lens is not None and new_lens.shape[0] != S):
+        raise ValueError("context_lens / new_lens must have one entry per sequence")
+    dev = _same_device(keep, weights, context_lens, new_lens)
+    with torch.cuda.device(dev):
+        st = _lib.load().pkv_kv_evict_select(
+            keep.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
+            weights.data_ptr(), weights.stride(1), context_lens.data_ptr(), int(max_context_len),
+            S, Hkv, budget, int(recent), int(sinks), _stream_handle(dev))
+    _lib.check(st, "pkv_kv_evict_select")
+    return keep
+
+
+def kv_compact(k_cache, v_cache, block_tables, keep, context_lens, weights=None,
+               dst_tables=None, max_context_len=None):
+    """Move the kept rows to each sequence's front: position i of (sequence s,
+    KV head h) receives the K and V rows (and the weight) of position
+    ``keep[s][h][i]``; the weights behind them become 0.  Rows move in place
+    unless ``dst_tables`` names other blocks (``BlockAllocator.shrink_seqs``
+    does for shared ones).  ``context_lens``: the lengths before the eviction,
+    each at most ``max_context_len`` (default: what the tables and weights
+    hold)."""
+    _cuda(k_cache, "k_cache", ndim=4)
+    dtype = k_cache.dtype
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("the caches must be float16 or bfloat16")
+    _cuda(v_cache, "v_cache", dtype, 4)
+    _cuda(block_tables, "block_tables", torch.int32, 2)
+    _cuda(keep, "keep", torch.int32, 3)
+    _cuda(context_lens, "context_lens", torch.int32, 1)
+    if dst_tables is None:
+        dst_tables = block_tables
+    _cuda(dst_tables, "dst_tables", torch.int32, 2)
+    NB, Hkv, B, D = k_cache.shape
+    S, H2, budget = keep.shape
+    if v_cache.shape != k_cache.shape or H2 != Hkv:
+        raise ValueError("shape mismatch between keep and the caches")
+    if block_tables.shape[0] != S or dst_tables.shape[0] != S or context_lens.shape[0] != S:
+        raise ValueError("tables / context_lens must have one row per sequence")
+    if max_context_len is None:
+        max_context_len = block_tables.shape[1] * B
+        if weights is not None:
+            max_context_len = min(max_context_len, weights.shape[-1])
+    if weights is not None:
+        _weights(weights, S, Hkv, max_context_len)
+    dev = _same_device(k_cache, v_cache, block_tables, keep, context_lens, weights, dst_tables)
+    with torch.cuda.device(dev):
+        st = _lib.load().pkv_kv_compact(
+            k_cache.data_ptr(), v_cache.data_ptr(),
+            None if weights is None else weights.data_ptr(),
+            0 if weights is None else weights.stride(1), block_tables.data_ptr(),
+            block_tables.shape[1], dst_tables.data_ptr(), dst_tables.shape[1], keep.data_ptr(),
+            budget, context_lens.data_ptr(), int(max_context_len), S, Hkv, D, B, NB,
+            _DTYPE_CODE[dtype], _stream_handle(dev))
+    _lib.check(st, "pkv_kv_compact")
 
 
 def check_copy_pairs(pairs, num_blocks):
