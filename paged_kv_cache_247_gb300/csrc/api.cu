@@ -804,7 +804,7 @@ pkv_status_t pkv_kv_evict_select(int32_t* keep, int32_t* new_lens, const float* 
   p.sinks = sinks;
   cudaError_t err = status_word(&p.status);
   if (err != cudaSuccess) return cuda_fail(err);
-  err = pkv::launch_kv_evict_select(p, num_seqs, reinterpret_cast<cudaStream_t>(stream));
+  err = pkv::launch_kv_evict_select(p, num_seqs, device_sms(), reinterpret_cast<cudaStream_t>(stream));
   return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
 }
 

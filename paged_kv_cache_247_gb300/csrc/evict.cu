@@ -8,6 +8,10 @@
 
 #include <math_constants.h>
 
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "overlap.cuh"
@@ -15,129 +19,290 @@
 namespace pkv {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr unsigned kFull = 0xffffffffu;
 
 // ---- choice ----------------------------------------------------------------
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelPer = 4;  // elements per thread and tile of the output pass
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelPerSm = 4;    // CTAs per SM the register budget is sized for
+constexpr int kSelBins = 2048;
+constexpr int kSelCoarse = 64;  // bins per coarse count: two per lane of one warp
+constexpr int kSelMaxCluster = 16;
+// Keys a CTA holds in shared memory; a longer share of a row is read again
+// from global memory in every pass.
+constexpr int kSelMaxKeys = 48 * 1024;
 
 // Order-preserving key of a weight: larger weight, larger key; -0 as +0; NaN
 // below everything.
 __device__ __forceinline__ uint32_t weight_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
-  if (x != x) return 0u;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t k = u ^ (uint32_t)((int32_t)u >> 31 | 0x80000000);
+  return x != x ? 0u : k;
 }
 
-// Exclusive prefix sum over the CTA's threads; *total gets the sum.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
+// Inclusive prefix sum over a warp.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t y = __shfl_up_sync(kFull, x, d);
     if (lane >= d) x += y;
   }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  uint32_t w = warp_sums[lane];  // 32 warps
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t y = __shfl_up_sync(kFull, w, d);
-    if (lane >= d) w += y;
-  }
-  const uint32_t before = warp > 0 ? __shfl_sync(kFull, w, warp - 1) : 0u;
-  *total = __shfl_sync(kFull, w, 31);
-  __syncthreads();
-  return before + x - v;
+  return x;
 }
 
-// One CTA per (sequence, KV head).  The r-th largest of the m candidates is
-// found by a radix selection over the keys, 8 bits a pass, and the kept
-// positions are written in ascending order by a prefix sum.
-__global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const SelectParams p) {
+// A cluster of CTAs per (sequence, KV head), each with an equal share of the
+// row's candidates [sinks, n - recent), in order.
+//
+// The r-th largest key is found by radix selection in three passes (11, 11 and
+// 10 bits, from the top).  Each CTA counts the digits of its keys in shared
+// memory and sums them by 64; one warp per CTA adds up the cluster's 32 coarse
+// counts, then the 64 bins of the coarse one that holds the wanted rank (all
+// CTAs find the same digit; distributed shared memory carries 96 words per CTA
+// and pass).  The keys stay in shared memory, so the row is read from HBM once.
+// Then each warp marks the kept keys of its contiguous part, one bit mask per
+// 32 keys, and after a prefix sum over warps and CTAs writes their positions:
+// ascending, and of the keys that equal the threshold the lowest positions.
+template <bool kCached>
+__global__ void __launch_bounds__(kSelThreads, kSelPerSm)
+    kv_evict_select_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ __align__(16) uint32_t hist[2 * kSelBins];
+  __shared__ uint32_t coarse[2][kSelBins / kSelCoarse];  // (passes alternate, as in hist)
+  __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+  __shared__ uint32_t s_digit, s_need, s_count, cta_gt, cta_eq;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 2 * kSelBins / 4; i += kSelThreads)
+    reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
   grid_dep_wait();
   grid_dep_launch_dependents();
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t warp_sums[32];
-  __shared__ uint32_t s_digit, s_need;
-  const int h = blockIdx.x, s = blockIdx.y;
-  const int tid = threadIdx.x;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int C = p.cluster, rank = C > 1 ? (int)cluster.block_rank() : 0;
+  const int h = blockIdx.x / C, s = blockIdx.y;
   int n = p.context_lens[s];
   if (n < 0 || n > p.max_context_len) {
-    if (tid == 0 && h == 0) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+    if (tid == 0 && h == 0 && rank == 0) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
     n = n < 0 ? 0 : p.max_context_len;
   }
   const size_t row = (size_t)s * p.num_kv_heads + h;
   int32_t* keep = p.keep + row * p.budget;
-  if (h == 0 && tid == 0 && p.new_lens) p.new_lens[s] = min(n, p.budget);
-  if (n <= p.budget) {
-    for (int i = tid; i < p.budget; i += kSelThreads) keep[i] = i < n ? i : -1;
+  if (h == 0 && rank == 0 && tid == 0 && p.new_lens) p.new_lens[s] = min(n, p.budget);
+  const int gtid = rank * kSelThreads + tid, gthreads = C * kSelThreads;
+  if (n <= p.budget) {  // the same in every CTA of the cluster
+    for (int i = gtid; i < p.budget; i += gthreads) keep[i] = i < n ? i : -1;
     return;
   }
   const int lo = p.sinks, hi = n - p.recent;
   const uint32_t r = p.budget - p.sinks - p.recent;
-  for (int i = tid; i < lo; i += kSelThreads) keep[i] = i;
-  for (int i = tid; i < p.recent; i += kSelThreads) keep[p.budget - p.recent + i] = hi + i;
+  for (int i = gtid; i < lo; i += gthreads) keep[i] = i;
+  for (int i = gtid; i < p.recent; i += gthreads) keep[p.budget - p.recent + i] = hi + i;
   if (r == 0) return;
-  const float* w = p.weights + row * p.weights_stride;
 
-  uint32_t prefix = 0, need = r;  // the need-th largest among keys that share the prefix
+  // This CTA's share [c0, c0 + m) of the candidates.
+  const int share = ((hi - lo + C - 1) / C + 31) / 32 * 32;
+  const int c0 = lo + min(rank * share, hi - lo);
+  const int m = min(share, hi - c0);
+  const float* w = p.weights + row * p.weights_stride + c0;
+  __syncthreads();  // the cleared histograms
+
+  // The need-th largest among the keys that share the prefix.  Once exactly
+  // that many do, all of them are kept: every key from the prefix on.
+  uint32_t prefix = 0, need = r;
+  bool whole = false;
 #pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int i = lo + tid; i < hi; i += kSelThreads) {
-      const uint32_t k = weight_key(w[i]);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[(k >> shift) & 255u], 1u);
+  for (int pass = 0; pass < 3 && !whole; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    const uint32_t span = pass == 0 ? 0xffffffffu : (pass == 1 ? 0x1fffffu : 0x3ffu);
+    uint32_t* hb = hist + (pass & 1) * kSelBins;
+    // The digit of a key that has the prefix: k ^ prefix has zeros above it.
+    auto count = [&](uint32_t k) {
+      const uint32_t d = k ^ prefix;
+      if (d <= span) atomicAdd(&hb[d >> shift], 1u);
+    };
+    if (pass == 0 || !kCached) {
+      // Four loads per thread are issued before any is used.
+      int i0 = 0;
+      for (; i0 + 4 * kSelThreads <= m; i0 += 4 * kSelThreads) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = w[i0 + j * kSelThreads + tid];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t k = weight_key(x[j]);
+          if (kCached) keys[i0 + j * kSelThreads + tid] = k;
+          count(k);
+        }
+      }
+      for (int i = i0 + tid; i < m; i += kSelThreads) {
+        const uint32_t k = weight_key(w[i]);
+        if (kCached) keys[i] = k;
+        count(k);
+      }
+    } else {
+      const int m4 = m & ~3;
+      for (int i = 4 * tid; i < m4; i += 4 * kSelThreads) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+        count(k.x);
+        count(k.y);
+        count(k.z);
+        count(k.w);
+      }
+      if (tid < m - m4) count(keys[m4 + tid]);
     }
     __syncthreads();
-    // thread d holds bin 255 - d: the prefix sum runs from the largest keys
-    const uint32_t c = tid < 256 ? hist[255 - tid] : 0u;
-    uint32_t total;
-    const uint32_t before = block_scan(c, warp_sums, &total);
-    if (tid < 256 && before < need && need <= before + c) {
-      s_digit = 255 - tid;
-      s_need = need - before;
+    // coarse counts: 16 threads with 4 bins each
+    for (int i = tid; i < kSelBins / 4; i += kSelThreads) {
+      const uint4 b = reinterpret_cast<const uint4*>(hb)[i];
+      uint32_t sum = (b.x + b.y) + (b.z + b.w);
+#pragma unroll
+      for (int d = 1; d < kSelCoarse / 4; d <<= 1) sum += __shfl_xor_sync(kFull, sum, d);
+      if (i % (kSelCoarse / 4) == 0) coarse[pass & 1][i / (kSelCoarse / 4)] = sum;
     }
+    if (C > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+    if (warp == 0) {
+      // Lane l holds coarse count 31 - l, then bins 2 (31 - l) + 1 and
+      // 2 (31 - l) of the one found: prefix sums run from the largest digit.
+      // (The loads from all CTAs are in flight together: one after another
+      // they took 1.6 us with 16 CTAs.)
+      uint32_t c = coarse[pass & 1][31 - lane];
+      if (C > 1) {
+        uint32_t x[kSelMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kSelMaxCluster; ++q)
+          x[q] = q < C && q != rank ? cluster.map_shared_rank(coarse[pass & 1], q)[31 - lane] : 0u;
+#pragma unroll
+        for (int q = 0; q < kSelMaxCluster; ++q) c += x[q];
+      }
+      uint32_t incl = warp_scan(c);
+      const int hit = __ffs(__ballot_sync(kFull, incl >= need)) - 1;
+      const uint32_t rest = need - __shfl_sync(kFull, incl - c, hit);  // wanted within the 64 bins
+      const int bin = (31 - hit) * kSelCoarse + 2 * (31 - lane);
+      uint32_t b1 = hb[bin + 1], b0 = hb[bin];
+      if (C > 1) {
+        uint2 x[kSelMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kSelMaxCluster; ++q)
+          x[q] = q < C && q != rank
+                     ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hb, q) + bin)
+                     : make_uint2(0, 0);
+#pragma unroll
+        for (int q = 0; q < kSelMaxCluster; ++q) {
+          b0 += x[q].x;
+          b1 += x[q].y;
+        }
+      }
+      incl = warp_scan(b1 + b0);
+      const uint32_t before = incl - b1 - b0;
+      if (before < rest && rest <= incl) {
+        const bool upper = rest <= before + b1;
+        s_digit = upper ? bin + 1 : bin;
+        s_need = upper ? rest - before : rest - before - b1;
+        s_count = upper ? b1 : b0;
+      }
+    }
+    // The first pass's histogram is counted in again by the third: every CTA
+    // is done reading it, having arrived at the second pass's barrier.
+    if (pass == 1)
+      for (int i = tid; i < kSelBins / 4; i += kSelThreads)
+        reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     prefix |= s_digit << shift;
     need = s_need;
-    __syncthreads();
+    whole = s_count == need;
   }
-  // Kept: every key above prefix, and the first `need` that equal it.
-  uint32_t out = lo, ties = 0;
-  for (int i0 = lo; i0 < hi; i0 += kSelThreads * kSelPer) {
-    uint32_t k[kSelPer];
-    uint32_t mine = 0;  // keys above in the low half, equal ones in the high half
-#pragma unroll
-    for (int j = 0; j < kSelPer; ++j) {
-      const int i = i0 + tid * kSelPer + j;
-      k[j] = i < hi ? weight_key(w[i]) : 0u;
-      if (i < hi) mine += k[j] > prefix ? 1u : (k[j] == prefix ? 65536u : 0u);
+
+  // Each warp marks the kept keys of a contiguous part of the share, in whole
+  // 32-key groups, 32 groups at a time: lane g holds the mask of group g.
+  const int part = ((m + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int w0 = min(warp * part, m), w1 = min(w0 + part, m);
+  auto masks = [&](int base, uint32_t least) {  // of keys of at least this value
+    uint32_t mine = 0;
+    const int groups = min(32, (w1 - base + 31) / 32);
+#pragma unroll 4
+    for (int g = 0; g < groups; ++g) {
+      const int i = base + 32 * g + lane;
+      const uint32_t k = i >= w1 ? 0u : (kCached ? keys[i] : weight_key(w[i]));
+      const uint32_t a = __ballot_sync(kFull, k >= least);
+      if (lane == g) mine = a;
     }
-    uint32_t total;
-    const uint32_t before = block_scan(mine, warp_sums, &total);
-    uint32_t above = before & 0xffffu, equal = ties + (before >> 16);
-#pragma unroll
-    for (int j = 0; j < kSelPer; ++j) {
-      const int i = i0 + tid * kSelPer + j;
-      if (i >= hi) break;
-      const bool eq = k[j] == prefix;
-      if (k[j] > prefix || (eq && equal < need)) {
-        // ties placed before this tile are part of `out` already
-        const uint32_t placed = min(equal, need) - min(ties, need);
-        keep[out + above + placed] = i;
-      }
-      above += k[j] > prefix;
-      equal += eq;
-    }
-    const uint32_t tile_ties = total >> 16;
-    out += (total & 0xffffu) + min(ties + tile_ties, need) - min(ties, need);
-    ties += tile_ties;
+    // (a key past the part's end reads as 0, which `least` may be)
+    const int left = w1 - base - 32 * lane;
+    return left >= 32 ? mine : (left > 0 ? mine & ((1u << left) - 1u) : 0u);
+  };
+  // Two thresholds only where some, but not all, of the keys that equal the
+  // prefix are kept (then it is a whole key; NaN's 0 has none below it).
+  uint32_t gt = 0, eq = 0;
+  auto count_kept = [&](int base, uint32_t& gm, uint32_t& em) {
+    const uint32_t ge = masks(base, prefix);
+    gm = whole ? ge : (prefix == 0xffffffffu ? 0u : masks(base, prefix + 1));
+    em = ge & ~gm;
+  };
+  uint32_t gm = 0, em = 0;
+  for (int base = w0; base < w1; base += 1024) {
+    count_kept(base, gm, em);
+    gt += __popc(gm);
+    eq += __popc(em);
   }
+  gt = __reduce_add_sync(kFull, gt);
+  eq = __reduce_add_sync(kFull, eq);
+  if (lane == 0) {
+    warp_gt[warp] = gt;
+    warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  const uint32_t sg = warp_scan(lane < kSelWarps ? warp_gt[lane] : 0u);
+  const uint32_t se = warp_scan(lane < kSelWarps ? warp_eq[lane] : 0u);
+  uint32_t above = warp > 0 ? __shfl_sync(kFull, sg, warp - 1) : 0u;
+  uint32_t equal = warp > 0 ? __shfl_sync(kFull, se, warp - 1) : 0u;
+  if (C > 1) {
+    const uint32_t tg = __shfl_sync(kFull, sg, 31), te = __shfl_sync(kFull, se, 31);
+    if (tid == 0) {
+      cta_gt = tg;
+      cta_eq = te;
+    }
+    cluster.sync();
+    uint32_t g = 0, e = 0;
+    if (lane < rank) {
+      g = *cluster.map_shared_rank(&cta_gt, lane);
+      e = *cluster.map_shared_rank(&cta_eq, lane);
+    }
+    above += __reduce_add_sync(kFull, g);
+    equal += __reduce_add_sync(kFull, e);
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  int32_t* to = keep + lo;
+  uint32_t at = above + min(equal, need);  // kept so far
+  for (int base = w0; base < w1; base += 1024) {
+    if (part > 1024) count_kept(base, gm, em);
+    if (!whole) {
+      // The group's ties before the need-th: the lowest bits of its mask.
+      const uint32_t ties = __popc(em);
+      const uint32_t eb = equal + warp_scan(ties) - ties;
+      uint32_t take = eb < need ? em : 0u;
+      for (uint32_t extra = eb < need ? max(ties, need - eb) - (need - eb) : 0u; extra > 0; --extra)
+        take &= ~(0x80000000u >> __clz(take));
+      gm |= take;
+      equal += __reduce_add_sync(kFull, ties);
+    }
+    const uint32_t kept = __popc(gm);
+    const uint32_t incl = warp_scan(kept);
+    const uint32_t first = at + incl - kept;
+    const int groups = min(32, (w1 - base + 31) / 32);
+#pragma unroll 4
+    for (int g = 0; g < groups; ++g) {
+      const uint32_t k = __shfl_sync(kFull, gm, g);
+      const uint32_t f = __shfl_sync(kFull, first, g);
+      if (k >> lane & 1u) to[f + __popc(k & below)] = c0 + base + 32 * g + lane;
+    }
+    at += __shfl_sync(kFull, incl, 31);
+  }
+  if (C > 1) cluster.sync();  // no CTA leaves while another may read its counts
 }
 
 // ---- compaction ------------------------------------------------------------
@@ -229,9 +394,52 @@ __global__ void __launch_bounds__(kCmpThreads) kv_compact_kernel(const CompactPa
 
 }  // namespace
 
-cudaError_t launch_kv_evict_select(const SelectParams& p, int num_seqs, cudaStream_t stream) {
-  return launch_overlapped(kv_evict_select_kernel, dim3(p.num_kv_heads, num_seqs),
-                           dim3(kSelThreads), 0, stream, p);
+cudaError_t launch_kv_evict_select(SelectParams p, int num_seqs, int sm_count,
+                                   cudaStream_t stream) {
+  // CTAs per row: as many as keep the whole launch within one wave, each with
+  // 1,024 keys or more.  (8 rows of 131,072: 95 us on one CTA each with 1,024
+  // threads, 33 us on 8, 17 us on 16.)
+  const long long rows = (long long)num_seqs * p.num_kv_heads;
+  int cluster = 1;
+  while (cluster < kSelMaxCluster && rows * cluster * 2 <= (long long)kSelPerSm * sm_count &&
+         p.max_context_len / (cluster * 2) >= 1024)
+    cluster *= 2;
+  p.cluster = cluster;
+  const int share = (std::max(1, (p.max_context_len + cluster - 1) / cluster) + 31) / 32 * 32;
+  const bool cached = share <= kSelMaxKeys;
+  const size_t smem = cached ? (size_t)share * 4 : 0;
+
+  auto kernel = cached ? kv_evict_select_kernel<true> : kv_evict_select_kernel<false>;
+  static unsigned long long configured = 0;  // bit per device ordinal (< 64)
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    err = cudaFuncSetAttribute(kv_evict_select_kernel<true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4);
+    for (auto k : {kv_evict_select_kernel<true>, kv_evict_select_kernel<false>})
+      if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.num_kv_heads * cluster, num_seqs);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t last = cudaGetLastError();  // clears the error, as after <<<>>>
+  return err != cudaSuccess ? err : last;
 }
 
 cudaError_t launch_kv_compact(const CompactParams& p, int num_seqs, cudaStream_t stream) {

@@ -182,9 +182,11 @@ struct SelectParams {
   int budget;
   int recent;
   int sinks;
+  int cluster;             // CTAs per row (set by the launch)
 };
 
-cudaError_t launch_kv_evict_select(const SelectParams& p, int num_seqs, cudaStream_t stream);
+cudaError_t launch_kv_evict_select(SelectParams p, int num_seqs, int sm_count,
+                                   cudaStream_t stream);
 
 struct CompactParams {
   void* k_cache;

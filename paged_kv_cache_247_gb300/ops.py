@@ -20,7 +20,24 @@ def _stream_handle(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _launch(name, index, *args):
+    """Call the library with the current stream of CUDA device ``index`` as the
+    last argument and that device current (the calls plan, and launch, on the
+    current device)."""
+    fn = getattr(_lib.load(), name)
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, name)
+
+
 def _cuda(t, name, dtype=None, ndim=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()
+            and (dtype is None or t.dtype is dtype) and (ndim is None or t.dim() == ndim)):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -175,14 +192,25 @@ def paged_attn_prefill(out, q, query_start, k_cache, v_cache, block_tables, cont
 
 
 def _same_device(first, *rest):
-    """The tensors' common device (None entries are skipped)."""
+    """Index of the tensors' common CUDA device (None entries are skipped)."""
+    index = first.get_device()
     for t in rest:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must be on one device")
-    return first.device
+    return index
 
 
-def _attn_shapes(q, out, k_cache, v_cache, weights):
+def _workspace(workspace, size, index):
+    """Address and bytes of the caller's workspace, or of one allocated here
+    (torch keeps its memory until the stream's work on it is done)."""
+    if workspace is None:
+        workspace = torch.empty(size(), dtype=torch.uint8, device=torch.device("cuda", index))
+    else:
+        _cuda(workspace, "workspace")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _attn_shapes(q, out, k_cache, v_cache):
     _cuda(q, "q", ndim=3)
     dtype = q.dtype
     if dtype not in _DTYPE_CODE:
@@ -218,7 +246,7 @@ def paged_attn_decode_weights(out, weights, q, k_cache, v_cache, block_tables, c
     plus each held position's softmax weight, summed over the query heads of
     the KV head's group.  Groups of at most 32 query heads.  Writes ``out``
     and returns it."""
-    _attn_shapes(q, out, k_cache, v_cache, weights)
+    _attn_shapes(q, out, k_cache, v_cache)
     _cuda(block_tables, "block_tables", torch.int32, 2)
     _cuda(context_lens, "context_lens", torch.int32, 1)
     S, Hq, D = q.shape
@@ -227,19 +255,20 @@ def paged_attn_decode_weights(out, weights, q, k_cache, v_cache, block_tables, c
     if block_tables.shape[0] != S or context_lens.shape[0] != S:
         raise ValueError("block_tables / context_lens must have one row per sequence")
     dev = _same_device(q, out, weights, k_cache, v_cache, block_tables, context_lens, workspace)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty(
-                decode_weights_workspace_size(S, Hq, Hkv, D, max_context_len, partition_size),
-                dtype=torch.uint8, device=dev)
-        _cuda(workspace, "workspace")
-        st = _lib.load().pkv_paged_attn_decode_weights(
-            out.data_ptr(), weights.data_ptr(), weights.stride(1), float(decay), q.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), S, Hq, Hkv, D,
-            B, NB, float(scale), _DTYPE_CODE[q.dtype], int(partition_size), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(dev))
-    _lib.check(st, "pkv_paged_attn_decode_weights")
+
+    def size():
+        sizes = (S, Hq, Hkv, D, max_context_len, partition_size)
+        if dev == torch._C._cuda_getDevice():
+            return decode_weights_workspace_size(*sizes)
+        with torch.cuda.device(dev):
+            return decode_weights_workspace_size(*sizes)
+
+    workspace, ws_ptr, ws_len = _workspace(workspace, size, dev)
+    _launch("pkv_paged_attn_decode_weights", dev, out.data_ptr(), weights.data_ptr(),
+            weights.shape[2], float(decay), q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), int(max_context_len), S, Hq, Hkv, D, B, NB, float(scale),
+            _DTYPE_CODE[q.dtype], int(partition_size), ws_ptr, ws_len)
     return out
 
 
@@ -252,7 +281,7 @@ def paged_attn_prefill_weights(out, weights, q, query_start, k_cache, v_cache, b
     queries of its sequence's chunk (0: all) and the query heads of the KV
     head's group.  ``workspace``: uint8, 4 bytes per query row and head.
     Writes ``out`` and returns it."""
-    _attn_shapes(q, out, k_cache, v_cache, weights)
+    _attn_shapes(q, out, k_cache, v_cache)
     _cuda(block_tables, "block_tables", torch.int32, 2)
     _cuda(context_lens, "context_lens", torch.int32, 1)
     _cuda(query_start, "query_start", torch.int32, 1)
@@ -264,19 +293,14 @@ def paged_attn_prefill_weights(out, weights, q, query_start, k_cache, v_cache, b
         raise ValueError("block_tables / query_start must match context_lens")
     dev = _same_device(q, out, weights, query_start, k_cache, v_cache, block_tables,
                        context_lens, workspace)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty(_lib.load().pkv_prefill_weights_workspace_size(T, Hq),
-                                    dtype=torch.uint8, device=dev)
-        _cuda(workspace, "workspace")
-        st = _lib.load().pkv_paged_attn_prefill_weights(
-            out.data_ptr(), weights.data_ptr(), weights.stride(1), float(decay), int(window),
-            q.data_ptr(), T, query_start.data_ptr(), int(max_query_len), k_cache.data_ptr(),
-            v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-            context_lens.data_ptr(), int(max_context_len), S, Hq, Hkv, D, B, NB, float(scale),
-            _DTYPE_CODE[q.dtype], workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(dev))
-    _lib.check(st, "pkv_paged_attn_prefill_weights")
+    workspace, ws_ptr, ws_len = _workspace(
+        workspace, lambda: _lib.load().pkv_prefill_weights_workspace_size(T, Hq), dev)
+    _launch("pkv_paged_attn_prefill_weights", dev, out.data_ptr(), weights.data_ptr(),
+            weights.shape[2], float(decay), int(window), q.data_ptr(), T,
+            query_start.data_ptr(), int(max_query_len), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+            int(max_context_len), S, Hq, Hkv, D, B, NB, float(scale), _DTYPE_CODE[q.dtype],
+            ws_ptr, ws_len)
     return out
 
 
@@ -343,15 +367,17 @@ def _token_rows(t, name, dtype):
     are dense (a slice of a joint projection, say)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dimensions")
     T, H, D = t.shape
-    if T > 0 and H > 0 and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
-        raise ValueError(f"{name} must have dense token rows")
+    s0, s1, s2 = t.stride()
     # (a dimension of one entry may carry any stride)
-    return t.stride(0) if T > 1 else H * D
+    if (s2 != 1 and D > 1) or (s1 != D and H > 1):
+        if t.numel():
+            raise ValueError(f"{name} must have dense token rows")
+    return s0 if T > 1 else H * D
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=None,
@@ -421,14 +447,11 @@ def rope_kv_append(q_out, q, k, v, positions, inv_freq, k_cache, v_cache, slot_m
     if positions.shape[0] != T or slot_mapping.shape[0] != T:
         raise ValueError("positions / slot_mapping must have one entry per token")
     dev = _same_device(q, q_out, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping)
-    with torch.cuda.device(dev):
-        st = _lib.load().pkv_rope_kv_append(
-            q_out.data_ptr(), strides[0], q.data_ptr(), strides[1], k.data_ptr(), strides[2],
-            v.data_ptr(), strides[3], positions.data_ptr(), inv_freq.data_ptr(),
-            2 * inv_freq.shape[0], 1 if interleaved else 0, float(attn_factor),
-            k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv, D, B, NB,
-            _DTYPE_CODE[dtype], _stream_handle(dev))
-    _lib.check(st, "pkv_rope_kv_append")
+    _launch("pkv_rope_kv_append", dev, q_out.data_ptr(), strides[0], q.data_ptr(), strides[1],
+            k.data_ptr(), strides[2], v.data_ptr(), strides[3], positions.data_ptr(),
+            inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
+            float(attn_factor), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+            T, Hq, Hkv, D, B, NB, _DTYPE_CODE[dtype])
     return q_out
 
 
@@ -450,12 +473,10 @@ def kv_evict_select(keep, weights, context_lens, max_context_len, recent=0, sink
     if context_lens.shape[0] != S or (new_lens is not None and new_lens.shape[0] != S):
         raise ValueError("context_lens / new_lens must have one entry per sequence")
     dev = _same_device(keep, weights, context_lens, new_lens)
-    with torch.cuda.device(dev):
-        st = _lib.load().pkv_kv_evict_select(
-            keep.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
-            weights.data_ptr(), weights.stride(1), context_lens.data_ptr(), int(max_context_len),
-            S, Hkv, budget, int(recent), int(sinks), _stream_handle(dev))
-    _lib.check(st, "pkv_kv_evict_select")
+    _launch("pkv_kv_evict_select", dev, keep.data_ptr(),
+            None if new_lens is None else new_lens.data_ptr(), weights.data_ptr(),
+            weights.shape[2], context_lens.data_ptr(), int(max_context_len), S, Hkv, budget,
+            int(recent), int(sinks))
     return keep
 
 
@@ -492,15 +513,12 @@ def kv_compact(k_cache, v_cache, block_tables, keep, context_lens, weights=None,
     if weights is not None:
         _weights(weights, S, Hkv, max_context_len)
     dev = _same_device(k_cache, v_cache, block_tables, keep, context_lens, weights, dst_tables)
-    with torch.cuda.device(dev):
-        st = _lib.load().pkv_kv_compact(
-            k_cache.data_ptr(), v_cache.data_ptr(),
+    _launch("pkv_kv_compact", dev, k_cache.data_ptr(), v_cache.data_ptr(),
             None if weights is None else weights.data_ptr(),
-            0 if weights is None else weights.stride(1), block_tables.data_ptr(),
+            0 if weights is None else weights.shape[2], block_tables.data_ptr(),
             block_tables.shape[1], dst_tables.data_ptr(), dst_tables.shape[1], keep.data_ptr(),
             budget, context_lens.data_ptr(), int(max_context_len), S, Hkv, D, B, NB,
-            _DTYPE_CODE[dtype], _stream_handle(dev))
-    _lib.check(st, "pkv_kv_compact")
+            _DTYPE_CODE[dtype])
 
 
 def check_copy_pairs(pairs, num_blocks):

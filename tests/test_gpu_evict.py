@@ -378,6 +378,19 @@ def test_select_long_row(cuda_device):
     _check_select(w, [200001], 70000, 1000, 4)
 
 
+def test_select_row_longer_than_shared_memory(cuda_device):
+    w = torch.exp(2 * torch.randn((1, 1, 420000), generator=_gen(2), device="cuda"))
+    _check_select(w, [419999], 100000, 7, 0)
+
+
+@pytest.mark.parametrize("S,H", [(1, 3), (20, 8), (40, 8), (90, 8)])
+def test_select_rows_per_launch(cuda_device, S, H):
+    """Every number of CTAs per row, sequences below and above the budget."""
+    lens = [(700 + 613 * s) % 9000 + 1 for s in range(S)]
+    w = torch.rand((S, H, 9001), generator=_gen(S), device="cuda")
+    _check_select(w, lens, 1200, 64, 2)
+
+
 def test_select_refuses_and_flags(cuda_device):
     w = torch.rand((2, 2, 50), device="cuda")
     keep = torch.empty((2, 2, 10), dtype=torch.int32, device="cuda")
