@@ -855,7 +855,7 @@ pkv_status_t pkv_kv_compact(void* k_cache, void* v_cache, float* weights, int64_
   p.num_blocks = num_blocks;
   cudaError_t err = status_word(&p.status);
   if (err != cudaSuccess) return cuda_fail(err);
-  err = pkv::launch_kv_compact(p, num_seqs, reinterpret_cast<cudaStream_t>(stream));
+  err = pkv::launch_kv_compact(p, num_seqs, device_sms(), reinterpret_cast<cudaStream_t>(stream));
   return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
 }
 

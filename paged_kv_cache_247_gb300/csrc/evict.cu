@@ -307,89 +307,189 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
 
 // ---- compaction ------------------------------------------------------------
 
-constexpr int kCmpThreads = 256;
-constexpr int kCmpChunks = 4;                  // 16-byte chunks of a row per CTA: a 64-byte slice
-constexpr int kCmpRows = kCmpThreads / kCmpChunks;
-constexpr int kCmpUnroll = 4;                  // rows in flight per thread
+// One warp moves K or V of one (sequence, KV head), or its weights, 32 rows (a
+// tile) at a time from the front, through a ring of tiles in shared memory:
+// rows are gathered by 16-byte asynchronous copies, and the kept rows of a
+// destination block, which lie side by side, go out as one bulk copy.
+//
+// keep[i] ascends and is at least i.  With rows moved in place a tile's sources
+// then lie at or behind its destinations and the next tiles' sources behind them
+// all: a tile may be stored as soon as its own loads have landed, whatever loads
+// of later tiles are in flight.  So a warp waits for nothing but its own copies.
+//
+// Bound by HBM.  64 sequences x 8 heads, 8k positions of 128 cut to 2k (1.1 GB
+// in all): 217 us (75 % of the copy rate) with tiles in registers and a barrier
+// between a tile's loads and its stores, whatever the rows or bytes in flight;
+// 326 us with a bulk copy per row, in and out (an SM starts one about every 23
+// cycles); 187 us so.
+constexpr int kCmpMinStages = 3, kCmpMaxStages = 20;
+constexpr int kCmpSmBytes = 226 * 1024;   // shared memory of an SM
+constexpr int kCmpFixedBytes = 1536;      // of a CTA beside its ring (1 KiB the system's)
 
-// A CTA moves one 64-byte column slice of K or of V of one (sequence, KV
-// head), or its weights, tile by tile from the front.  keep[i] ascends and is
-// at least i, so with rows moved in place a tile's sources lie at or behind
-// its destinations and the next tile's sources behind them all: one barrier
-// between a tile's loads and its stores is enough.
-__global__ void __launch_bounds__(kCmpThreads) kv_compact_kernel(const CompactParams p) {
+__device__ __forceinline__ void bulk_store(void* dst, const void* src_smem, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_addr(src_smem)), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void compact_weights(const CompactParams& p, const int32_t* keep,
+                                                float* w, int n, int m) {
+  constexpr int kRows = 8;
+  const int lane = threadIdx.x;
+  for (int i0 = 0; i0 < m; i0 += 32 * kRows) {
+    float x[kRows];
+    int k[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int i = i0 + u * 32 + lane;
+      k[u] = i < m ? __ldg(keep + i) : -1;
+      if (i < m && (k[u] < i || k[u] >= n)) {
+        atomicOr(p.status, PKV_DEV_BAD_KEEP);
+        k[u] = -1;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) x[u] = k[u] >= 0 ? w[k[u]] : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (k[u] >= 0) w[i0 + u * 32 + lane] = x[u];
+  }
+  __syncwarp();
+#pragma unroll 8
+  for (int i = m + lane; i < n; i += 32) w[i] = 0.f;
+}
+
+template <int CPR>  // 16-byte chunks per row
+__global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, int stages) {
+  constexpr int kRowBytes = CPR * 16;
+  extern __shared__ __align__(128) unsigned char ring[];  // [stages][32] rows
+  // Where each row goes (nullptr: it does not move), behind the ring.
+  unsigned char*(*to_ring)[32] =
+      reinterpret_cast<unsigned char*(*)[32]>(ring + stages * 32 * kRowBytes);
+  __shared__ uint64_t full[kCmpMaxStages];
+  const int lane = threadIdx.x;
+  if (lane == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 32);
+    fence_barrier_init();
+  }
+  __syncwarp();
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int tid = threadIdx.x;
-  const int h = blockIdx.y, s = blockIdx.z;
+  // The weights go first: last, they would be the launch's tail.
+  const int h = blockIdx.x, s = blockIdx.y;
+  const int job = p.weights ? (int)blockIdx.z - 1 : (int)blockIdx.z;  // -1: weights, 0: K, 1: V
   int n = p.context_lens[s];
   if (n < 0 || n > p.max_len) {
-    if (tid == 0 && h == 0 && blockIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+    if (lane == 0 && h == 0 && job == 0) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
     n = n < 0 ? 0 : p.max_len;
   }
   const int m = min(n, p.budget);
   const size_t row = (size_t)s * p.num_kv_heads + h;
   const int32_t* keep = p.keep + row * p.budget;
-  const int slices = p.head_dim * 2 / 16 / kCmpChunks;  // of one row
-
-  if ((int)blockIdx.x >= 2 * slices) {  // the weights
-    float* w = p.weights + row * p.weights_stride;
-    for (int i0 = 0; i0 < m; i0 += kCmpThreads * kCmpUnroll) {
-      float x[kCmpUnroll];
-      bool ok[kCmpUnroll];
-#pragma unroll
-      for (int u = 0; u < kCmpUnroll; ++u) {
-        const int i = i0 + u * kCmpThreads + tid;
-        const int k = i < m ? keep[i] : -1;
-        ok[u] = i < m && k >= i && k < n;
-        if (i < m && !ok[u]) atomicOr(p.status, PKV_DEV_BAD_KEEP);
-        x[u] = ok[u] ? w[k] : 0.f;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kCmpUnroll; ++u)
-        if (ok[u]) w[i0 + u * kCmpThreads + tid] = x[u];
-    }
-    __syncthreads();
-    for (int i = m + tid; i < n; i += kCmpThreads) w[i] = 0.f;
+  if (job < 0) {
+    compact_weights(p, keep, p.weights + row * p.weights_stride, n, m);
     return;
   }
 
-  const bool is_v = (int)blockIdx.x >= slices;
-  uint4* cache = static_cast<uint4*>(is_v ? p.v_cache : p.k_cache);
-  const int cpr = p.head_dim * 2 / 16;
-  const int c = ((int)blockIdx.x - (is_v ? slices : 0)) * kCmpChunks + tid % kCmpChunks;
+  unsigned char* cache = static_cast<unsigned char*>(job == 1 ? p.v_cache : p.k_cache);
   const int32_t* src_row = p.src_tables + (size_t)s * p.max_blocks_per_seq;
   const int32_t* dst_row = p.dst_tables + (size_t)s * p.dst_blocks_per_seq;
-  const int lane_row = tid / kCmpChunks;
   const int mask = p.block_size - 1;
-  for (int i0 = 0; i0 < m; i0 += kCmpRows * kCmpUnroll) {
-    uint4 x[kCmpUnroll];
-    long long to[kCmpUnroll];
-#pragma unroll
-    for (int u = 0; u < kCmpUnroll; ++u) {
-      const int i = i0 + u * kCmpRows + lane_row;
-      to[u] = -1;
-      if (i >= m) continue;
-      const int k = keep[i];
-      if (k < i || k >= n) {
-        atomicOr(p.status, PKV_DEV_BAD_KEEP);
-        continue;
-      }
-      const int sb = src_row[k >> p.log2_block], db = dst_row[i >> p.log2_block];
-      if ((unsigned)sb >= (unsigned)p.num_blocks || (unsigned)db >= (unsigned)p.num_blocks) {
-        atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
-        continue;
-      }
-      if (sb == db && k == i) continue;  // already in place
-      x[u] = cache[(((long long)sb * p.num_kv_heads + h) * p.block_size + (k & mask)) * cpr + c];
-      to[u] = (((long long)db * p.num_kv_heads + h) * p.block_size + (i & mask)) * cpr + c;
+  const int tiles = (m + 31) / 32;
+  auto at = [&](int block, int pos) {
+    return cache +
+           (((long long)block * p.num_kv_heads + h) * p.block_size + (pos & mask)) * kRowBytes;
+  };
+  // The lane's row of the next tile to load: its kept position and block ids,
+  // read a tile ahead.
+  int k_next = -1, sb_next = 0, db_next = 0;
+  auto look = [&](int j) {
+    const int i = j * 32 + lane;
+    k_next = -1;
+    if (i >= m) return;
+    const int k = __ldg(keep + i);
+    db_next = __ldg(dst_row + (i >> p.log2_block));
+    if (k < i || k >= n) {
+      atomicOr(p.status, PKV_DEV_BAD_KEEP);
+      return;
     }
-    __syncthreads();
+    sb_next = __ldg(src_row + (k >> p.log2_block));
+    k_next = k;
+  };
+  auto load = [&](int j, int st) {
+    const int i = j * 32 + lane;
+    bool moves = k_next >= 0;
+    if (moves && ((unsigned)sb_next >= (unsigned)p.num_blocks ||
+                  (unsigned)db_next >= (unsigned)p.num_blocks)) {
+      atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
+      moves = false;
+    }
+    moves = moves && (sb_next != db_next || k_next != i);
+    to_ring[st][lane] = moves ? at(db_next, i) : nullptr;
+    const unsigned who = __ballot_sync(kFull, moves);
+    const unsigned long long from =
+        reinterpret_cast<unsigned long long>(moves ? at(sb_next, k_next) : cache);
+    look(j + 1);
+    // 32 / CPR rows per step: CPR lanes with one chunk each.
+    const uint32_t to = smem_addr(ring) + (uint32_t)(st * 32 * kRowBytes) + lane * 16;
 #pragma unroll
-    for (int u = 0; u < kCmpUnroll; ++u)
-      if (to[u] >= 0) cache[to[u]] = x[u];
+    for (int c = 0; c < CPR; ++c) {
+      const int r = c * (32 / CPR) + lane / CPR;
+      const unsigned long long src = __shfl_sync(kFull, from, r) + lane % CPR * 16;
+      if (who >> r & 1u)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + c * 512), "l"(src)
+                     : "memory");
+    }
+    // Every lane arrives once its copies have landed.
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                     smem_addr(&full[st]))
+                 : "memory");
+  };
+  look(0);
+  int ahead = 0, ahead_st = 0;  // the next tile to load and its stage
+  auto load_next = [&]() {
+    load(ahead++, ahead_st);
+    if (++ahead_st == stages) ahead_st = 0;
+  };
+  while (ahead < min(stages - 2, tiles)) load_next();
+  const int seg = min(p.block_size, 32);  // rows of a tile in one destination block
+  const unsigned seg_bits = (seg == 32 ? kFull : (1u << seg) - 1u) << (lane & ~(seg - 1));
+  int st = 0, phase = 0;
+  bool ok = true;
+  for (int j = 0; j < tiles; ++j) {
+    if (ahead < tiles) {
+      // Its stage was last read by the stores of tile j - 2, of which this lane's
+      // are done once at most its newest group is not.
+      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+      load_next();
+    }
+    if (!mbar_wait_warp(&full[st], phase, p.status)) {
+      ok = false;
+      break;
+    }
+    // The rows were written by plain copies: order them before the bulk copy.
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    unsigned char* to = to_ring[st][lane];
+    const unsigned who = __ballot_sync(kFull, to != nullptr);
+    const int left = m - j * 32;
+    const unsigned there = left >= 32 ? kFull : (1u << left) - 1u;
+    const unsigned char* src = ring + (st * 32 + lane) * kRowBytes;
+    if ((who & seg_bits) == (there & seg_bits)) {  // the block's rows side by side
+      if (to && (lane & (seg - 1)) == 0) bulk_store(to, src, __popc(who & seg_bits) * kRowBytes);
+    } else if (to) {
+      bulk_store(to, src, kRowBytes);
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1;
+    }
   }
+  // Copies still in flight at exit land first (loads: only after a timeout).
+  if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 }  // namespace
@@ -442,10 +542,31 @@ cudaError_t launch_kv_evict_select(SelectParams p, int num_seqs, int sm_count,
   return err != cudaSuccess ? err : last;
 }
 
-cudaError_t launch_kv_compact(const CompactParams& p, int num_seqs, cudaStream_t stream) {
-  const int slices = 2 * (p.head_dim * 2 / 16 / kCmpChunks) + (p.weights ? 1 : 0);
-  return launch_overlapped(kv_compact_kernel, dim3(slices, p.num_kv_heads, num_seqs),
-                           dim3(kCmpThreads), 0, stream, p);
+cudaError_t launch_kv_compact(const CompactParams& p, int num_seqs, int sm_count,
+                              cudaStream_t stream) {
+  // Stages of one warp's ring: what an SM's shared memory holds for its share of
+  // the warps that move rows, so that all of them run at once.
+  const int tile = 32 * p.head_dim * 2, stage = tile + 32 * 8;
+  const long long warps = 2LL * p.num_kv_heads * num_seqs;
+  const long long per_sm = (warps + sm_count - 1) / sm_count;
+  const long long room = kCmpSmBytes / per_sm - kCmpFixedBytes;
+  const int stages = (int)std::max<long long>(
+      kCmpMinStages, std::min<long long>(kCmpMaxStages, room / stage));
+  const dim3 grid(p.num_kv_heads, num_seqs, p.weights ? 3 : 2);
+  auto kernel = p.head_dim == 64 ? kv_compact_kernel<8> : kv_compact_kernel<16>;
+  static unsigned long long configured = 0;  // bit per device ordinal (< 64)
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    for (auto k : {kv_compact_kernel<8>, kv_compact_kernel<16>}) {
+      err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kCmpMaxStages * (32 * 256 + 32 * 8));
+      if (err != cudaSuccess) return err;
+    }
+    if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  return launch_overlapped(kernel, grid, dim3(32), (size_t)stages * stage, stream, p, stages);
 }
 
 }  // namespace pkv

@@ -209,7 +209,8 @@ struct CompactParams {
   int num_blocks;
 };
 
-cudaError_t launch_kv_compact(const CompactParams& p, int num_seqs, cudaStream_t stream);
+cudaError_t launch_kv_compact(const CompactParams& p, int num_seqs, int sm_count,
+                              cudaStream_t stream);
 
 // kv_append indexes (token, 16-byte chunk) pairs with 32 bits: a call may move
 // at most this many chunks of K (and as many of V), 32 GiB each.

@@ -13,6 +13,8 @@
 //
 // Bound by HBM: (Hq + 2 Hkv) D elements read and as many written per token.
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "overlap.cuh"
@@ -21,8 +23,19 @@ namespace pkv {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeUnits = 2;   // units in flight per thread before the first is used
+constexpr int kRopeTokens = 8;  // most tokens per CTA
 
-enum RopeLayout { kInterleaved = 0, kHalf = 1, kHalfScalar = 2 };
+enum RopeLayout { kInterleaved = 0, kHalf = 1 };
+
+// Plain loads (q_out may be q), not kept in L1.
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
 
 __device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
   const float x = a * cs.x - b * cs.y;
@@ -62,98 +75,187 @@ __device__ __forceinline__ void rotate_halves(uint4& lo, uint4& hi, const float2
   }
 }
 
-// Every unit of a head row (16 elements; two elements in the scalar layout)
-// is read and written by one thread, reads first, so q_out may be q.
-template <typename T, int LAYOUT>
-__device__ __forceinline__ void rope_unit(const T* src, T* dst, int u, int rot, const float2* cs) {
-  if constexpr (LAYOUT == kHalfScalar) {
-    const int half = rot / 2;
-    const int i = u < half ? u : 2 * u;          // past the pairs: elements R, R + 2, ...
-    const int j = u < half ? u + half : 2 * u + 1;
-    float a = static_cast<float>(src[i]), b = static_cast<float>(src[j]);
-    if (u < half) rotate(a, b, cs[u]);
-    dst[i] = static_cast<T>(a);
-    dst[j] = static_cast<T>(b);
-  } else {
-    // chunks c0 and c1 of the row
-    int c0 = 2 * u, c1 = 2 * u + 1;
-    const bool turned = LAYOUT == kHalf && u < rot / 16;
-    if (turned) {
-      c0 = u;
-      c1 = u + rot / 16;
+// What a CTA knows of its tokens: (cos, sin) of each pair, and where k and v
+// go (row of head 0 in the caches, -1: nowhere).
+struct RopeTokens {
+  float2 cs[kRopeTokens][64];
+  long long row0[kRopeTokens];
+  int padding[kRopeTokens];
+};
+
+__device__ __forceinline__ void prepare_tokens(const RopeParams& p, RopeTokens& sm, int t0, int n) {
+  const int pairs = p.rot_dim / 2;
+  for (int i = threadIdx.x; i < n * pairs; i += blockDim.x) {
+    const int tok = i / pairs, pair = i - tok * pairs;
+    const double turns =
+        (double)p.positions[t0 + tok] * (p.inv_freq[pair] * 0.15915494309189533577);
+    float s, c;
+    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    sm.cs[tok][pair] = make_float2(c * p.factor, s * p.factor);
+  }
+  if (threadIdx.x < n) {
+    const int t = t0 + threadIdx.x;
+    const bool padding = p.positions[t] < 0;
+    const long long slot = p.slot_mapping[t];
+    long long row0 = -1;
+    if (!padding && slot >= 0) {
+      if (slot >= p.num_slots) {
+        atomicOr(p.status, PKV_DEV_BAD_SLOT);
+      } else {
+        const long long blk = slot / p.block_size;
+        row0 = blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size);
+      }
     }
-    uint4 x = reinterpret_cast<const uint4*>(src)[c0];
-    uint4 y = reinterpret_cast<const uint4*>(src)[c1];
-    if (turned) {
-      rotate_halves<T>(x, y, cs, 8 * u);
-    } else if (LAYOUT == kInterleaved) {
-      x = rotate_neighbours<T>(x, cs, 4 * c0, rot / 2);
-      y = rotate_neighbours<T>(y, cs, 4 * c1, rot / 2);
-    }
-    reinterpret_cast<uint4*>(dst)[c0] = x;
-    reinterpret_cast<uint4*>(dst)[c1] = y;
+    sm.row0[threadIdx.x] = row0;
+    sm.padding[threadIdx.x] = padding;
   }
 }
 
-// One CTA per token.
+// A unit is two 16-byte chunks of a head row of q, k or v: chunks w and w + R/16
+// where they hold the two halves of the same pairs, else chunks that one thread
+// can turn alone.  Each is read and written by one thread, so q_out may be q.
+// A CTA takes as many tokens as give each thread kRopeUnits units, and issues
+// those loads before it looks at positions and slots: the angles (64-bit
+// arithmetic at a low rate, and a barrier) then overlap them.  (16,384 tokens,
+// 32 + 2 x 8 heads of 128: 88 us with the angles first and a CTA per token,
+// 68 us so.)
 template <typename T, int LAYOUT>
-__global__ void __launch_bounds__(kRopeThreads) rope_kv_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_kv_append_kernel(const RopeParams p, int num_tokens, int tokens_per_cta) {
   grid_dep_wait();
   grid_dep_launch_dependents();
-  __shared__ float2 cs[64];  // (cos, sin) of each pair
-  const int t = blockIdx.x;
-  const int pos = p.positions[t];
-  if (pos < 0) return;  // padding
-  const int pairs = p.rot_dim / 2;
-  if (threadIdx.x < pairs) {
-    const double turns = (double)pos * (p.inv_freq[threadIdx.x] * 0.15915494309189533577);
-    float s, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    cs[threadIdx.x] = make_float2(c * p.factor, s * p.factor);
-  }
-  const long long slot = p.slot_mapping[t];
-  bool store = slot >= 0;
-  if (slot >= p.num_slots) {
-    if (threadIdx.x == 0) atomicOr(p.status, PKV_DEV_BAD_SLOT);
-    store = false;
-  }
-  __syncthreads();
+  __shared__ RopeTokens sm;
+  const int t0 = blockIdx.x * tokens_per_cta;
+  const int n = min(tokens_per_cta, num_tokens - t0);
   const int D = p.head_dim;
-  const long long blk = store ? slot / p.block_size : 0;
-  const long long off = store ? slot - blk * p.block_size : 0;
-  const int units = LAYOUT == kHalfScalar ? D / 2 : D / 16;
-  const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
-  T* qo = static_cast<T*>(p.q_out) + t * p.q_out_stride;
-  for (int i = threadIdx.x; i < p.num_q_heads * units; i += kRopeThreads) {
-    const int h = i / units;
-    rope_unit<T, LAYOUT>(q + h * D, qo + h * D, i - h * units, p.rot_dim, cs);
+  const int upr = D / 16, log2_upr = D == 128 ? 3 : 2;  // units per head row
+  const int units = (p.num_q_heads + 2 * p.num_kv_heads) * upr;
+  const int total = n * units;
+  const int turned = LAYOUT == kHalf ? p.rot_dim / 16 : 0;  // units with both halves of pairs
+
+  auto chunk0 = [&](int w) { return w < turned || LAYOUT != kHalf ? w : 2 * w; };
+  auto chunk1 = [&](int w) {
+    return LAYOUT != kHalf ? w + upr : (w < turned ? w + turned : 2 * w + 1);
+  };
+  // Head row of unit u of token t.
+  auto source = [&](int t, int h) {
+    const long long tt = t0 + t;
+    if (h < p.num_q_heads) return static_cast<const T*>(p.q) + tt * p.q_stride + (long long)h * D;
+    h -= p.num_q_heads;
+    if (h < p.num_kv_heads)
+      return static_cast<const T*>(p.k) + tt * p.k_stride + (long long)h * D;
+    return static_cast<const T*>(p.v) + tt * p.v_stride + (long long)(h - p.num_kv_heads) * D;
+  };
+  uint4 x[kRopeUnits], y[kRopeUnits];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kRopeUnits; ++i) {
+      const int g = base + i * blockDim.x + threadIdx.x;
+      if (g >= total) continue;
+      const int t = n == 1 ? 0 : g / units;
+      const int u = g - t * units, w = u & (upr - 1);
+      const uint4* src = reinterpret_cast<const uint4*>(source(t, u >> log2_upr));
+      x[i] = load_once(src + chunk0(w));
+      y[i] = load_once(src + chunk1(w));
+    }
+  };
+  load(0);
+  prepare_tokens(p, sm, t0, n);
+  __syncthreads();
+  for (int base = 0; base < total; base += kRopeUnits * blockDim.x) {
+    if (base > 0) load(base);
+#pragma unroll
+    for (int i = 0; i < kRopeUnits; ++i) {
+      const int g = base + i * blockDim.x + threadIdx.x;
+      if (g >= total) continue;
+      const int t = n == 1 ? 0 : g / units;
+      const int u = g - t * units, w = u & (upr - 1);
+      int h = u >> log2_upr;
+      const bool is_q = h < p.num_q_heads;
+      const bool is_v = h >= p.num_q_heads + p.num_kv_heads;
+      if (is_q ? sm.padding[t] != 0 : sm.row0[t] < 0) continue;
+      if (!is_v) {
+        const float2* cs = sm.cs[t];
+        if (LAYOUT == kInterleaved) {
+          x[i] = rotate_neighbours<T>(x[i], cs, 4 * chunk0(w), p.rot_dim / 2);
+          y[i] = rotate_neighbours<T>(y[i], cs, 4 * chunk1(w), p.rot_dim / 2);
+        } else if (w < turned) {
+          rotate_halves<T>(x[i], y[i], cs, 8 * w);
+        }
+      }
+      T* dst;
+      if (is_q) {
+        dst = static_cast<T*>(p.q_out) + (t0 + t) * p.q_out_stride + (long long)h * D;
+      } else {
+        h -= p.num_q_heads + (is_v ? p.num_kv_heads : 0);
+        dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) +
+              (sm.row0[t] + (long long)h * p.block_size) * D;
+      }
+      reinterpret_cast<uint4*>(dst)[chunk0(w)] = x[i];
+      reinterpret_cast<uint4*>(dst)[chunk1(w)] = y[i];
+    }
   }
-  if (!store) return;
-  const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
+}
+
+// The half layout where R is not a multiple of 16, so that a pair's halves lie
+// in chunks at different offsets: one pair of elements per thread.  One CTA per
+// token.
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_kv_append_scalar_kernel(const RopeParams p) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  __shared__ RopeTokens sm;
+  const int t = blockIdx.x;
+  prepare_tokens(p, sm, t, 1);
+  __syncthreads();
+  if (sm.padding[0]) return;
+  const int D = p.head_dim, half = p.rot_dim / 2;
+  auto turn_rows = [&](const T* src, T* dst, long long dst_head, int heads) {
+    for (int g = threadIdx.x; g < heads * (D / 2); g += kRopeThreads) {
+      const int h = g / (D / 2), u = g - h * (D / 2);
+      const int i = u < half ? u : 2 * u;  // past the pairs: elements R, R + 2, ...
+      const int j = u < half ? u + half : 2 * u + 1;
+      const T* row = src + (long long)h * D;
+      T* to = dst + h * dst_head;
+      float a = static_cast<float>(row[i]), b = static_cast<float>(row[j]);
+      if (u < half) rotate(a, b, sm.cs[0][u]);
+      to[i] = static_cast<T>(a);
+      to[j] = static_cast<T>(b);
+    }
+  };
+  turn_rows(static_cast<const T*>(p.q) + t * p.q_stride,
+            static_cast<T*>(p.q_out) + t * p.q_out_stride, D, p.num_q_heads);
+  if (sm.row0[0] < 0) return;
+  const long long dst_head = (long long)p.block_size * D;
+  turn_rows(static_cast<const T*>(p.k) + t * p.k_stride,
+            static_cast<T*>(p.k_cache) + sm.row0[0] * D, dst_head, p.num_kv_heads);
   const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
-  T* kc = static_cast<T*>(p.k_cache);
-  T* vc = static_cast<T*>(p.v_cache);
-  const size_t row0 = (size_t)blk * p.num_kv_heads * p.block_size + off;
-  for (int i = threadIdx.x; i < p.num_kv_heads * units; i += kRopeThreads) {
-    const int h = i / units;
-    rope_unit<T, LAYOUT>(k + h * D, kc + (row0 + (size_t)h * p.block_size) * D, i - h * units,
-                         p.rot_dim, cs);
-  }
+  T* vc = static_cast<T*>(p.v_cache) + sm.row0[0] * D;
   for (int i = threadIdx.x; i < p.num_kv_heads * (D / 8); i += kRopeThreads) {
     const int h = i / (D / 8), c = i - h * (D / 8);
-    reinterpret_cast<uint4*>(vc + (row0 + (size_t)h * p.block_size) * D)[c] =
-        reinterpret_cast<const uint4*>(v + h * D)[c];
+    reinterpret_cast<uint4*>(vc + h * dst_head)[c] = reinterpret_cast<const uint4*>(v + h * D)[c];
   }
 }
 
 template <typename T>
 cudaError_t launch_rope_typed(const RopeParams& p, int num_tokens, cudaStream_t stream) {
-  const dim3 grid(num_tokens), block(kRopeThreads);
-  if (p.interleaved)
-    return launch_overlapped(rope_kv_append_kernel<T, kInterleaved>, grid, block, 0, stream, p);
-  if (p.rot_dim % 16 == 0)
-    return launch_overlapped(rope_kv_append_kernel<T, kHalf>, grid, block, 0, stream, p);
-  return launch_overlapped(rope_kv_append_kernel<T, kHalfScalar>, grid, block, 0, stream, p);
+  if (!p.interleaved && p.rot_dim % 16)
+    return launch_overlapped(rope_kv_append_scalar_kernel<T>, dim3(num_tokens), dim3(kRopeThreads),
+                             0, stream, p);
+  const long long units = (p.num_q_heads + 2LL * p.num_kv_heads) * (p.head_dim / 16);
+  const long long span = (long long)kRopeUnits * kRopeThreads;  // units of a full CTA
+  // Several tokens per CTA only where there are CTAs to spare: a short launch
+  // takes one CTA's chain of latencies however few tokens a CTA has.
+  const int tokens = (int)std::max(
+      1LL, std::min({(long long)kRopeTokens, span / units, (long long)num_tokens / 1024}));
+  const long long want = (tokens * units + kRopeUnits - 1) / kRopeUnits;
+  const int threads = (int)std::min<long long>(kRopeThreads, (want + 31) / 32 * 32);
+  const dim3 grid((num_tokens + tokens - 1) / tokens);
+  return p.interleaved ? launch_overlapped(rope_kv_append_kernel<T, kInterleaved>, grid,
+                                           dim3(threads), 0, stream, p, num_tokens, tokens)
+                       : launch_overlapped(rope_kv_append_kernel<T, kHalf>, grid, dim3(threads), 0,
+                                           stream, p, num_tokens, tokens);
 }
 
 }  // namespace
