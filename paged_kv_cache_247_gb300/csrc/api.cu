@@ -338,22 +338,39 @@ pkv_status_t check_weights(const WeightsArgs& w, int max_context_len) {
   return max_context_len > kMaxPositions ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
 
-// Workspace of the decode call with weights: the partials when the context is
-// split, every partition's maximum and sum, and the step's logits, rows
-// 16-byte aligned.
+// CTAs for the tensor-core decode kernel's persistent walk: as many as the SMs,
+// or fewer so that every CTA walks the same number of items.  512 items on 152
+// SMs, say, run as 4 rounds of 128 CTAs instead of 3 rounds of 152 and a fourth
+// of 56; each round still keeps HBM busy (one CTA streams about twice its
+// share), and no CTA waits out a short last round.
+int tc_ctas(long long items) {
+  const long long sms = device_sms();
+  const long long rounds = (items + sms - 1) / sms;
+  return rounds > 0 ? (int)std::max(1LL, (items + rounds - 1) / rounds) : 1;
+}
+
+// Workspace of the decode call with weights, in floats.  A split call: the
+// partials, every partition's maximum and sum, and the step's logits; every
+// call: the CTAs' own scratch for the logits of contexts of one partition.
+// Rows of logits are whole 16-byte multiples.
 struct DecodeWeightsLayout {
-  size_t m, x, floats;  // offsets of ws_m and ws_x, and the whole, in floats
-  long long x_stride;
+  size_t m, x, own, floats;  // offsets of ws_m, ws_x and ws_own, and the whole
+  long long x_stride, own_stride;
 };
 
-DecodeWeightsLayout decode_weights_layout(int num_seqs, int num_q_heads, int head_dim,
-                                          int max_context_len, long long parts) {
+DecodeWeightsLayout decode_weights_layout(int num_seqs, int num_q_heads, int num_kv_heads,
+                                          int head_dim, int max_context_len, int partition) {
   DecodeWeightsLayout l{};
-  const size_t pairs = (size_t)num_seqs * num_q_heads, rows = pairs * parts;
-  l.x_stride = ((long long)max_context_len + 3) / 4 * 4;
-  l.m = parts > 1 ? rows * head_dim : 0;
-  l.x = (l.m + 2 * rows + 3) / 4 * 4;
-  l.floats = l.x + pairs * l.x_stride;
+  const long long parts = num_parts_for(max_context_len, partition);
+  const size_t pairs = (size_t)num_seqs * num_q_heads, rows = parts > 1 ? pairs * parts : 0;
+  auto whole = [](long long n) { return (n + 3) / 4 * 4; };
+  l.x_stride = parts > 1 ? whole(max_context_len) : 0;
+  l.own_stride = whole(std::min(max_context_len, partition));
+  l.m = rows * head_dim;
+  l.x = whole(l.m + 2 * rows);
+  l.own = l.x + pairs * l.x_stride;
+  const long long ctas = tc_ctas((long long)num_seqs * num_kv_heads * parts);
+  l.floats = l.own + (size_t)ctas * 2 * (num_q_heads / num_kv_heads) * l.own_stride;
   return l;
 }
 
@@ -430,17 +447,21 @@ pkv_status_t paged_decode_impl(void* out, const void* q, const void* k_new, cons
   p.num_parts = (int)parts;
   p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax is evaluated with exp2
   if (wa) {
-    const DecodeWeightsLayout l =
-        decode_weights_layout(num_seqs, num_q_heads, head_dim, max_context_len, parts);
-    if (!workspace || workspace_bytes < l.floats * sizeof(float))
+    const DecodeWeightsLayout l = decode_weights_layout(num_seqs, num_q_heads, num_kv_heads,
+                                                        head_dim, max_context_len, part);
+    if (l.floats > 0 && (!workspace || workspace_bytes < l.floats * sizeof(float)))
       return PKV_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
     float* ws = static_cast<float*>(workspace);
-    p.ws_o = ws;
-    p.ws_m = ws + l.m;
-    p.ws_l = p.ws_m + (size_t)num_seqs * num_q_heads * parts;
-    p.ws_x = ws + l.x;
-    p.x_stride = l.x_stride;
+    if (parts > 1) {
+      p.ws_o = ws;
+      p.ws_m = ws + l.m;
+      p.ws_l = p.ws_m + (size_t)num_seqs * num_q_heads * parts;
+      p.ws_x = ws + l.x;
+      p.x_stride = l.x_stride;
+    }
+    p.ws_own = ws + l.own;
+    p.own_stride = l.own_stride;
     p.weights = wa->weights;
     p.weights_stride = wa->stride;
     p.decay = wa->decay;
@@ -458,19 +479,11 @@ pkv_status_t paged_decode_impl(void* out, const void* q, const void* k_new, cons
   if (err != cudaSuccess) return cuda_fail(err);
   if (plan.tc) {
     bool unsupported = false;
-    // CTAs for the persistent walk: as many as the SMs, or fewer so that
-    // every CTA walks the same number of items.  512 items on 152 SMs, say,
-    // run as 4 rounds of 128 CTAs instead of 3 rounds of 152 and a fourth of
-    // 56; each round still keeps HBM busy (one CTA streams about twice its
-    // share), and no CTA waits out a short last round.
-    const long long items = parts * num_kv_heads * (long long)num_seqs;
-    const long long sms = device_sms();
-    const long long rounds = (items + sms - 1) / sms;
-    const int ctas = (int)std::max(1LL, (items + rounds - 1) / rounds);
+    const int ctas = tc_ctas(parts * num_kv_heads * (long long)num_seqs);
     err = pkv::launch_paged_decode_tc(p, dtype, head_dim, ctas,
                                       reinterpret_cast<cudaStream_t>(stream), &unsupported);
     if (unsupported) return PKV_ERR_UNSUPPORTED;
-    if (wa && err == cudaSuccess && max_context_len > 0)
+    if (wa && err == cudaSuccess && parts > 1)
       err = pkv::launch_decode_weights(p, reinterpret_cast<cudaStream_t>(stream));
   } else {
     err = pkv::launch_paged_decode(p, dtype, head_dim, gt,
@@ -521,8 +534,8 @@ size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_
   const int part = partition_size ? partition_size
                                   : tc_partition(num_seqs, num_kv_heads, max_context_len);
   if (!pkv::decode_tc_supported(head_dim, num_q_heads / num_kv_heads, part)) return (size_t)-1;
-  return decode_weights_layout(num_seqs, num_q_heads, head_dim, max_context_len,
-                               num_parts_for(max_context_len, part)).floats * sizeof(float);
+  return decode_weights_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, part)
+             .floats * sizeof(float);
 }
 
 pkv_status_t pkv_paged_attn_decode_weights(

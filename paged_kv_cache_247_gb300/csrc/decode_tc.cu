@@ -90,6 +90,7 @@ struct TcShape {
   static constexpr int kVWarp = kKWarp + 1;    // V producer
   static constexpr int kSWarp = kKWarp + 2;    // S^T issuer, owns tensor memory
   static constexpr int kOWarp = kKWarp + 3;    // O^T issuer
+  static constexpr int kWWarp = kKWarp + 4;    // weights warpgroup (where there is one)
   static constexpr int kThreads = kKeyThreads + 4 * 32;
   static constexpr int kQBytes = N * D * 2;    // D / 64 atoms of N rows x 128 bytes
   // P^T rows: the padded group for O^T; for O the MMA's 128 rows, except that
@@ -116,7 +117,8 @@ struct TcShape {
   static constexpr int kRed = kP + kSB * kPBuf;     // [KG][4 warps][NHW] floats
   static constexpr int kBar = kRed + KG * 4 * NHW * 4;
   static constexpr int kTmemSlot = kBar + kBarSlots * 8;
-  static constexpr int kBytes = kTmemSlot + 16 + 1024;  // + alignment slack
+  static constexpr int kLse = kTmemSlot + 16;           // [2][NH] log-sums (weights)
+  static constexpr int kBytes = kLse + 2 * NH * 4 + 1024;  // + alignment slack
   static_assert(kBytes <= 227 * 1024, "shared memory overflow");
   static constexpr int kColO = kSB * N;                 // S^T buffers first
   static constexpr int kTmemCols = pow2_at_least(kSB * N + 2 * kOCols);
@@ -171,10 +173,51 @@ __device__ __forceinline__ bool group_any(int kg, bool v) {
 
 __device__ __forceinline__ void group_sync(int kg) { named_barrier_sync(1 + kg, 128); }
 
-// kWeights: the logits and every item's (m, l) are kept for the accumulated
-// attention weights.
+// Add an unsplit item's weights from this CTA's logits in buffer b: thread t of
+// 128 in warpgroup `wg` of `wgs` that share the positions.
+template <int NH>
+__device__ __forceinline__ void add_weights(const DecodeParams& p, const Item& it, int b,
+                                            const float* s_lse, int t, int wg, int wgs) {
+  constexpr int kPer = NH <= 8 ? 8 : 4;  // positions per thread and step
+  float* w = p.weights + ((size_t)it.s * p.num_kv_heads + it.kvh) * p.weights_stride;
+  const float* xr = p.ws_own + ((size_t)blockIdx.x * 2 + b) * p.group * p.own_stride;
+  const float* lse = s_lse + b * NH;
+  for (int t0 = wg * 128 * kPer + t; t0 < it.ctx; t0 += wgs * 128 * kPer) {
+    float sum[kPer], old[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      sum[u] = 0.f;
+      old[u] = t0 + 128 * u < it.ctx && p.decay != 0.f ? w[t0 + 128 * u] : 0.f;
+    }
+#pragma unroll 4
+    for (int g = 0; g < p.group; ++g) {
+      float x[kPer];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u)
+        x[u] = t0 + 128 * u < it.ctx ? __ldcg(xr + (size_t)g * p.own_stride + t0 + 128 * u)
+                                     : -CUDART_INF_F;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) sum[u] += ex2(x[u] - lse[g]);
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (t0 + 128 * u < it.ctx)
+        w[t0 + 128 * u] = p.decay == 0.f ? sum[u] : fmaf(p.decay, old[u], sum[u]);
+  }
+}
+
+// kWeights: the accumulated attention weights, weights[t] = decay * weights[t] +
+// sum_g 2^(x_g(t) - lse_g).  A position's weight is known once its row's sum is,
+// at the end of the context, so the base-2 logits x are kept.  Where a work item
+// is a whole context, one more warpgroup finishes its weights while the others
+// stream the next item: the logits of two items lie in this CTA's own scratch,
+// which is used over and over and so stays in L2.  The partitions of a split
+// context leave logits and (m, l) for decode_weights_kernel.  (64 sequences of
+// 8k over 8 KV heads, groups of 4: 388 us with that kernel after an unsplit
+// decode too, 343 us so; the last item's weights, which nothing overlaps, are
+// shared with the key warpgroups: 360 us without.)
 template <typename T, int NH, int D, bool kWeights>
-__global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
+__global__ void __launch_bounds__(TcShape<NH, D>::kThreads + (kWeights ? 128 : 0), 1)
     paged_decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap,
                            const __grid_constant__ CUtensorMap qmap, int num_items) {
@@ -206,7 +249,10 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
   uint64_t* q_empty = q_full + 2;      // [2] S^T MMAs of that item done (commit)
   uint64_t* o_free = q_empty + 2;      // [2] O^T buffer read by the key warpgroups
   uint64_t* drain = o_free + 2;        // [2] each issuer's last MMAs finished
-  static_assert(4 * S + 4 * SB + 8 <= kBarSlots, "barrier area too small");
+  uint64_t* w_full = drain + 2;        // [2] an item's logits and log-sums written
+  uint64_t* w_free = w_full + 2;       // [2] read by the weights warpgroup
+  static_assert(4 * S + 4 * SB + 12 <= kBarSlots, "barrier area too small");
+  float* s_lse = reinterpret_cast<float*>(smem + L::kLse);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
 
   const int warp = threadIdx.x >> 5;
@@ -231,6 +277,8 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
       mbar_init(&q_empty[b], 1);
       mbar_init(&o_free[b], L::kKeyThreads);
       mbar_init(&drain[b], 1);
+      mbar_init(&w_full[b], L::kKeyThreads);
+      mbar_init(&w_free[b], 128);
     }
     fence_barrier_init();
   }
@@ -425,6 +473,20 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
     mma_commit_warp(d);
     mbar_drain(d, 0);
     __syncwarp();
+  } else if (kWeights && warp >= L::kWWarp) {
+    // -------------------------------------------------- weights warpgroup
+    int k_w = 0;
+    for (int j = blockIdx.x; j < num_items; j += gridDim.x) {
+      const Item it = item_at(p, j);
+      if (it.n_tiles == 0 || it.nparts_seq > 1) continue;
+      const int b = k_w & 1;
+      if (!mbar_wait(&w_full[b], (k_w >> 1) & 1, p.status) || timed_out(p.status)) break;
+      // The last item has the key warpgroups' help.
+      const bool last = j + gridDim.x >= num_items;
+      add_weights<NH>(p, it, b, s_lse, threadIdx.x & 127, 0, last ? L::KG + 1 : 1);
+      mbar_arrive(&w_free[b]);
+      ++k_w;
+    }
   } else {
     // ----------------------------------------------------- key warpgroups
     const int kg = warp >> 2;            // which half of the heads
@@ -441,6 +503,7 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
         reinterpret_cast<uint4*>(sP)[i] = make_uint4(0, 0, 0, 0);
     }
     int kt = 0, k_item = 0;
+    int k_w = 0;  // items whose weights the weights warpgroup finishes
     bool ok = true;
     for (int j = blockIdx.x; j < num_items; j += gridDim.x) {
       const Item it = item_at(p, j);
@@ -467,6 +530,20 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
         mref[g] = -CUDART_INF_F;
         l_part[g] = 0.f;
       }
+      // Where the logits go: this CTA's scratch, or the split context's rows.
+      const bool own_w = kWeights && it.nparts_seq == 1;
+      float* x_rows = nullptr;
+      long long x_stride = 0;
+      if constexpr (kWeights) {
+        const int b = k_w & 1;
+        x_stride = own_w ? p.own_stride : p.x_stride;
+        x_rows = (own_w ? p.ws_own + (((size_t)blockIdx.x * 2 + b) * G + hb) * x_stride
+                        : p.ws_x + ((size_t)it.s * p.num_q_heads + h0 + hb) * x_stride) +
+                 it.t_begin + t;
+        if (own_w && k_w >= 2 && ok &&
+            !mbar_wait_warp(&w_free[b], ((k_w - 2) >> 1) & 1, p.status))
+          ok = false;
+      }
       for (int i = 0; i < it.n_tiles; ++i, ++kt) {
         const int nvalid = min(kKeys, it.t_end - (it.t_begin + i * kKeys));
         const bool valid = t < nvalid;
@@ -486,11 +563,10 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
           exceed |= valid && hb + g < G && x[g] > mref[g] + 8.f;
         }
         if constexpr (kWeights) {
-          float* xr = p.ws_x + ((size_t)it.s * p.num_q_heads + h0 + hb) * p.x_stride +
-                      it.t_begin + i * kKeys + t;
+          float* xr = x_rows + i * kKeys;
 #pragma unroll
           for (int g = 0; g < NHW; ++g)
-            if (valid && hb + g < G) xr[(size_t)g * p.x_stride] = x[g];
+            if (valid && hb + g < G) xr[(size_t)g * x_stride] = x[g];
         }
         if (group_any(kg, exceed)) {
           // Some key exceeds its head's running max by more than 8: the tile
@@ -625,7 +701,7 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
             for (int g = 0; g < NHW; ++g)
               if (hb + g < G) dst[(size_t)g * p.num_parts * D] = o[g] * inv[g];
           }
-          if (kWeights || it.nparts_seq > 1) {
+          if (own_w || it.nparts_seq > 1) {
             const size_t r0 = row0 * p.num_parts + it.part;
             // Thread g writes head g's maximum and sum (one thread writing
             // them all took longer than the whole tile).
@@ -637,8 +713,12 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
                 lg = l[g];
               }
             if (d < NHW && hb + d < G) {
-              p.ws_m[r0 + (size_t)d * p.num_parts] = mg;
-              p.ws_l[r0 + (size_t)d * p.num_parts] = lg;
+              if (own_w) {
+                s_lse[(k_w & 1) * NH + hb + d] = mg + log2f(lg);
+              } else {
+                p.ws_m[r0 + (size_t)d * p.num_parts] = mg;
+                p.ws_l[r0 + (size_t)d * p.num_parts] = lg;
+              }
             }
           }
         }
@@ -686,9 +766,23 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&o_free[ob]);
-        if (ok && mine && (kWeights || it.nparts_seq > 1)) {
+        if (ok && mine && own_w) {
+          s_lse[(k_w & 1) * NH + t] = m + log2f(l);
+        } else if (ok && mine && it.nparts_seq > 1) {
           p.ws_m[r] = m;
           p.ws_l[r] = l;
+        }
+      }
+      if constexpr (kWeights) {
+        if (own_w) {
+          const int b = k_w & 1;
+          mbar_arrive(&w_full[b]);
+          // Nothing is left to stream after the last item: finished by the
+          // weights warpgroup alone, its weights were the launch's tail.
+          if (j + gridDim.x >= num_items && ok &&
+              mbar_wait(&w_full[b], (k_w >> 1) & 1, p.status) && !timed_out(p.status))
+            add_weights<NH>(p, it, b, s_lse, t, kg + 1, L::KG + 1);
+          ++k_w;
         }
       }
       ++k_item;
@@ -721,8 +815,9 @@ cudaError_t launch_tc_typed(const DecodeParams& p, const CUtensorMap& km, const 
   }
   const long long items = (long long)p.num_parts * p.num_kv_heads * p.num_seqs;
   const int grid = (int)(items < sms ? items : sms);
-  err = launch_overlapped(paged_decode_tc_kernel<T, NH, D, kWeights>, dim3(grid), dim3(L::kThreads),
-                          L::kBytes, stream, p, km, vm, qm, (int)items);
+  err = launch_overlapped(paged_decode_tc_kernel<T, NH, D, kWeights>, dim3(grid),
+                          dim3(L::kThreads + (kWeights ? 128 : 0)), L::kBytes, stream, p, km, vm,
+                          qm, (int)items);
   if (err != cudaSuccess || p.num_parts <= 1) return err;
   return launch_decode_reduce(p, std::is_same<T, __nv_bfloat16>::value ? PKV_BF16 : PKV_F16, D,
                               stream);
@@ -731,7 +826,7 @@ cudaError_t launch_tc_typed(const DecodeParams& p, const CUtensorMap& km, const 
 template <typename T, int NH, int D>
 cudaError_t launch_tc_heads(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                             const CUtensorMap& qm, int sms, cudaStream_t stream) {
-  return p.ws_x ? launch_tc_typed<T, NH, D, true>(p, km, vm, qm, sms, stream)
+  return p.weights ? launch_tc_typed<T, NH, D, true>(p, km, vm, qm, sms, stream)
                 : launch_tc_typed<T, NH, D, false>(p, km, vm, qm, sms, stream);
 }
 

@@ -35,10 +35,12 @@ struct DecodeParams {
   int partition_size;  // tokens per CTA (multiple of 32)
   int num_parts;       // ceil(max_context_len / partition_size), >= 1
   float qscale;        // scale * log2(e): logits are kept in base-2 units
-  // Accumulated attention weights (ws_x == nullptr: none; tensor-core kernel
-  // only).  ws_m and ws_l are then written for unsplit contexts too.
-  float* ws_x;             // base-2 logits [S, Hq, x_stride]
+  // Accumulated attention weights (weights == nullptr: none; tensor-core kernel
+  // only).
+  float* ws_x;             // split contexts: base-2 logits [S, Hq, x_stride]
   long long x_stride;
+  float* ws_own;           // unsplit ones: [CTAs, 2, group, own_stride], used in turn
+  long long own_stride;
   float* weights;          // [S, Hkv, weights_stride]
   long long weights_stride;
   float decay;

@@ -28,7 +28,7 @@ __device__ __forceinline__ float decayed(float decay, float old, float add) {
   return decay == 0.f ? add : fmaf(decay, old, add);
 }
 
-// ---- decode ----------------------------------------------------------------
+// ---- decode: split contexts -------------------------------------------------
 
 constexpr int kDwThreads = 256;
 constexpr int kDwPer = 4;  // positions per thread
@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kDwThreads) decode_weights_kernel(const Decode
   ctx = ctx < 0 ? 0 : (ctx > cap ? (int)cap : ctx);
   if (t0 >= ctx) return;
   const int np = (ctx + p.partition_size - 1) / p.partition_size;
+  if (np <= 1) return;  // done by the decode kernel
   const size_t row0 = (size_t)s * p.num_q_heads + (size_t)kvh * p.group;
   const int lane = threadIdx.x & 31;
   for (int g = threadIdx.x >> 5; g < p.group; g += kDwThreads / 32) {

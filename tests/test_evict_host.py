@@ -69,10 +69,15 @@ def test_decode_weights_refusals(lib, over, expect):
 
 def test_decode_weights_workspace(lib):
     size = lib.pkv_decode_weights_workspace_size
-    # unsplit: a maximum, a sum and the padded logits per (sequence, head)
-    assert size(2, 8, 2, 128, 61, 0) == 4 * (2 * 2 * 8 + 2 * 8 * 64)
-    # split in three: the partial outputs too
-    assert size(2, 8, 2, 64, 300, 128) == 4 * (2 * 8 * 3 * 66 + 2 * 8 * 300)
+    # unsplit: two rows of logits per query head of the group and CTA (one CTA per
+    # (sequence, KV head) here), padded to 16 bytes
+    assert size(2, 8, 2, 128, 61, 0) == 4 * (4 * 2 * 4 * 64)
+    # split in three: the partial outputs, maxima and sums, every logit, and the
+    # scratch of 12 CTAs for sequences of one partition
+    assert size(2, 8, 2, 64, 300, 128) == 4 * (2 * 8 * 3 * 66 + 2 * 8 * 300 + 12 * 2 * 4 * 128)
+    # 512 items on 152 SMs (assumed here): 4 rounds of 128 CTAs
+    assert size(64, 32, 8, 128, 8192, 8192) == 4 * (128 * 2 * 4 * 8192)
+    assert size(2, 8, 2, 128, 0, 0) == 0
     for bad in ((2, 66, 2, 128, 64, 0), (2, 8, 2, 128, 64, 96), (2, 8, 2, 96, 64, 0),
                 (2, 7, 2, 128, 64, 0), (2, 8, 2, 128, (1 << 30) + 1, 0)):
         assert size(*bad) == ctypes.c_size_t(-1).value
