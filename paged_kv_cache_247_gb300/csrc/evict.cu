@@ -401,36 +401,60 @@ __global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, i
     return cache +
            (((long long)block * p.num_kv_heads + h) * p.block_size + (pos & mask)) * kRowBytes;
   };
-  // The lane's row of the next tile to load: its kept position and block ids,
-  // read a tile ahead.
-  int k_next = -1, sb_next = 0, db_next = 0;
-  auto look = [&](int j) {
-    const int i = j * 32 + lane;
-    k_next = -1;
-    if (i >= m) return;
-    const int k = __ldg(keep + i);
-    db_next = __ldg(dst_row + (i >> p.log2_block));
-    if (k < i || k >= n) {
-      atomicOr(p.status, PKV_DEV_BAD_KEEP);
-      return;
+  // The lane's rows of the next tiles to load, four tiles (a group) at a time:
+  // kept positions and destination blocks are read two groups ahead, source
+  // blocks (which depend on the positions) one group ahead.
+  struct Group {
+    int k[4], sb[4], db[4];  // k < 0: no row
+  } cur, nxt, fut;
+  auto fetch = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = (g * 4 + u) * 32 + lane;
+      fut.k[u] = i < m ? __ldg(keep + i) : -1;
+      fut.db[u] = i < m ? __ldg(dst_row + (i >> p.log2_block)) : 0;
     }
-    sb_next = __ldg(src_row + (k >> p.log2_block));
-    k_next = k;
   };
+  auto resolve = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = (g * 4 + u) * 32 + lane;
+      const bool good = fut.k[u] >= i && fut.k[u] < n;
+      if (i < m && !good) atomicOr(p.status, PKV_DEV_BAD_KEEP);
+      nxt.k[u] = i < m && good ? fut.k[u] : -1;
+      nxt.db[u] = fut.db[u];
+      nxt.sb[u] = nxt.k[u] >= 0 ? __ldg(src_row + (fut.k[u] >> p.log2_block)) : 0;
+    }
+  };
+  fetch(0);
+  resolve(0);
+  fetch(1);
   auto load = [&](int j, int st) {
-    const int i = j * 32 + lane;
-    bool moves = k_next >= 0;
-    if (moves && ((unsigned)sb_next >= (unsigned)p.num_blocks ||
-                  (unsigned)db_next >= (unsigned)p.num_blocks)) {
+    const int i = j * 32 + lane, u = j & 3;
+    if (u == 0) {
+      cur = nxt;
+      resolve(j / 4 + 1);
+      fetch(j / 4 + 2);
+    }
+    int k = cur.k[0], sb = cur.sb[0], db = cur.db[0];
+#pragma unroll
+    for (int v = 1; v < 4; ++v)
+      if (u == v) {
+        k = cur.k[v];
+        sb = cur.sb[v];
+        db = cur.db[v];
+      }
+    bool moves = k >= 0;
+    if (moves &&
+        ((unsigned)sb >= (unsigned)p.num_blocks || (unsigned)db >= (unsigned)p.num_blocks)) {
       atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
       moves = false;
     }
-    moves = moves && (sb_next != db_next || k_next != i);
-    to_ring[st][lane] = moves ? at(db_next, i) : nullptr;
+    moves = moves && (sb != db || k != i);
+    to_ring[st][lane] = moves ? at(db, i) : nullptr;
     const unsigned who = __ballot_sync(kFull, moves);
     const unsigned long long from =
-        reinterpret_cast<unsigned long long>(moves ? at(sb_next, k_next) : cache);
-    look(j + 1);
+        reinterpret_cast<unsigned long long>(moves ? at(sb, k) : cache);
     // 32 / CPR rows per step: CPR lanes with one chunk each.
     const uint32_t to = smem_addr(ring) + (uint32_t)(st * 32 * kRowBytes) + lane * 16;
 #pragma unroll
@@ -446,7 +470,6 @@ __global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, i
                      smem_addr(&full[st]))
                  : "memory");
   };
-  look(0);
   int ahead = 0, ahead_st = 0;  // the next tile to load and its stage
   auto load_next = [&]() {
     load(ahead++, ahead_st);

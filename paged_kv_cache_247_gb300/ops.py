@@ -194,9 +194,10 @@ def paged_attn_prefill(out, q, query_start, k_cache, v_cache, block_tables, cont
 def _same_device(first, *rest):
     """Index of the tensors' common CUDA device (None entries are skipped)."""
     index = first.get_device()
-    for t in rest:
-        if t is not None and t.get_device() != index:
-            raise ValueError("all tensors must be on one device")
+    if torch.cuda.device_count() > 1:  # (with one GPU there is no other)
+        for t in rest:
+            if t is not None and t.get_device() != index:
+                raise ValueError("all tensors must be on one device")
     return index
 
 
@@ -362,21 +363,20 @@ def kv_append(k, v, k_cache, v_cache, slot_mapping):
     _lib.check(st, "pkv_kv_append")
 
 
-def _token_rows(t, name, dtype):
-    """Element stride between the tokens of a [T, H, D] tensor whose token rows
-    are dense (a slice of a joint projection, say)."""
+def _token_rows(t, name, dtype, shape):
+    """Element stride between the tokens of a [T, H, D] tensor of this shape
+    whose token rows are dense (a slice of a joint projection, say)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dimensions")
-    T, H, D = t.shape
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    T, H, D = shape
     s0, s1, s2 = t.stride()
     # (a dimension of one entry may carry any stride)
-    if (s2 != 1 and D > 1) or (s1 != D and H > 1):
-        if t.numel():
-            raise ValueError(f"{name} must have dense token rows")
+    if ((s2 != 1 and D > 1) or (s1 != D and H > 1)) and t.numel():
+        raise ValueError(f"{name} must have dense token rows")
     return s0 if T > 1 else H * D
 
 
@@ -429,21 +429,22 @@ def rope_kv_append(q_out, q, k, v, positions, inv_freq, k_cache, v_cache, slot_m
     dimensions from rot_dim on pass through.  Pairs are neighbours if
     ``interleaved``, else rot_dim / 2 apart.  q, k, v and q_out may be slices
     of wider token rows.  Returns ``q_out``."""
-    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE_CODE:
-        raise ValueError("q must be float16 or bfloat16")
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE_CODE or q.dim() != 3:
+        raise ValueError("q must be float16 or bfloat16 with 3 dimensions")
     dtype = q.dtype
-    strides = [_token_rows(t, n, dtype) for t, n in
-               ((q_out, "q_out"), (q, "q"), (k, "k"), (v, "v"))]
     _cuda(k_cache, "k_cache", dtype, 4)
     _cuda(v_cache, "v_cache", dtype, 4)
+    q_shape, cache_shape = q.shape, k_cache.shape
+    T, Hq, D = q_shape
+    NB, Hkv, B, D2 = cache_shape
+    kv_shape = (T, Hkv, D)
+    strides = (_token_rows(q_out, "q_out", dtype, q_shape), _token_rows(q, "q", dtype, q_shape),
+               _token_rows(k, "k", dtype, kv_shape), _token_rows(v, "v", dtype, kv_shape))
     _cuda(positions, "positions", torch.int32, 1)
     _cuda(inv_freq, "inv_freq", torch.float64, 1)
     _cuda(slot_mapping, "slot_mapping", torch.int64, 1)
-    T, Hq, D = q.shape
-    NB, Hkv, B, D2 = k_cache.shape
-    if (q_out.shape != q.shape or k.shape != (T, Hkv, D) or v.shape != k.shape or D2 != D
-            or v_cache.shape != k_cache.shape):
-        raise ValueError("shape mismatch between q, q_out, the new rows and the caches")
+    if D2 != D or v_cache.shape != cache_shape:
+        raise ValueError("shape mismatch between q and the caches")
     if positions.shape[0] != T or slot_mapping.shape[0] != T:
         raise ValueError("positions / slot_mapping must have one entry per token")
     dev = _same_device(q, q_out, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping)
