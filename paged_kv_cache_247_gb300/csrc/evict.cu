@@ -307,24 +307,28 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
 
 // ---- compaction ------------------------------------------------------------
 
-// One warp moves K or V of one (sequence, KV head), or its weights, 32 rows (a
-// tile) at a time from the front, through a ring of tiles in shared memory:
+// A CTA of one to eight warps moves K or V of one (sequence, KV head), or its
+// weights, from the front, 32 rows (a tile) per warp and round, through a ring of
+// tiles in shared memory for each warp:
 // rows are gathered by 16-byte asynchronous copies, and the kept rows of a
 // destination block, which lie side by side, go out as one bulk copy.
 //
 // keep[i] ascends and is at least i.  With rows moved in place a tile's sources
 // then lie at or behind its destinations and the next tiles' sources behind them
-// all: a tile may be stored as soon as its own loads have landed, whatever loads
-// of later tiles are in flight.  So a warp waits for nothing but its own copies.
+// all: a round may be stored as soon as its own loads have landed, whatever loads
+// of later rounds are in flight.
 //
-// Bound by HBM.  64 sequences x 8 heads, 8k positions of 128 cut to 2k (1.1 GB
+// Bound by HBM.  64 sequences x 8 heads, 6-8k positions of 128 cut to 2k (1.1 GB
 // in all): 217 us (75 % of the copy rate) with tiles in registers and a barrier
 // between a tile's loads and its stores, whatever the rows or bytes in flight;
 // 326 us with a bulk copy per row, in and out (an SM starts one about every 23
-// cycles); 187 us so.
-constexpr int kCmpMinStages = 3, kCmpMaxStages = 20;
+// cycles); 180 us so (91 %).  With few pairs a CTA's chain of rounds bounds it:
+// one sequence x 8 heads cut from 131,072 to 32,768 takes 195 us on eight warps
+// per CTA (1.4 TB/s), 466 us on one.
+constexpr int kCmpMaxWarps = 8;
+constexpr int kCmpMinStages = 3, kCmpMaxStages = 8;
 constexpr int kCmpSmBytes = 226 * 1024;   // shared memory of an SM
-constexpr int kCmpFixedBytes = 1536;      // of a CTA beside its ring (1 KiB the system's)
+constexpr int kCmpFixedBytes = 1024 + kCmpMaxWarps * kCmpMaxStages * 8;  // of a CTA beside its rings
 
 __device__ __forceinline__ void bulk_store(void* dst, const void* src_smem, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
@@ -332,43 +336,69 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src_smem, uint
                : "memory");
 }
 
+// The weights, 16 per thread and step: the kept positions are read two steps
+// ahead and the values one step ahead of the step that is stored (which, as with
+// rows, only its own loads have to precede).
 __device__ __forceinline__ void compact_weights(const CompactParams& p, const int32_t* keep,
                                                 float* w, int n, int m) {
-  constexpr int kRows = 8;
-  const int lane = threadIdx.x;
-  for (int i0 = 0; i0 < m; i0 += 32 * kRows) {
-    float x[kRows];
-    int k[kRows];
+  constexpr int kPer = 16;
+  const int threads = blockDim.x, step = threads * kPer, tid = threadIdx.x;
+  int k[kPer];
+  bool here[kPer], next[kPer];
+  float x[kPer], y[kPer];
+  auto fetch = [&](int i0) {
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int i = i0 + u * 32 + lane;
+    for (int u = 0; u < kPer; ++u) {
+      const int i = i0 + u * threads + tid;
       k[u] = i < m ? __ldg(keep + i) : -1;
-      if (i < m && (k[u] < i || k[u] >= n)) {
-        atomicOr(p.status, PKV_DEV_BAD_KEEP);
-        k[u] = -1;
-      }
     }
+  };
+  auto read = [&](int i0) {  // the values of the positions in k
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) x[u] = k[u] >= 0 ? w[k[u]] : 0.f;
-    __syncwarp();
+    for (int u = 0; u < kPer; ++u) {
+      const int i = i0 + u * threads + tid;
+      next[u] = k[u] >= i && k[u] < n;  // (never where there is no entry: k is -1)
+      if (i < m && !next[u]) atomicOr(p.status, PKV_DEV_BAD_KEEP);
+      y[u] = next[u] ? __ldcg(w + k[u]) : 0.f;
+    }
+  };
+  fetch(0);
+  read(0);
+  fetch(step);
+  for (int i0 = 0; i0 < m; i0 += step) {
 #pragma unroll
-    for (int u = 0; u < kRows; ++u)
-      if (k[u] >= 0) w[i0 + u * 32 + lane] = x[u];
+    for (int u = 0; u < kPer; ++u) {
+      x[u] = y[u];
+      here[u] = next[u];
+    }
+    if (i0 + step < m) {
+      read(i0 + step);
+      fetch(i0 + 2 * step);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (here[u]) w[i0 + u * threads + tid] = x[u];
   }
-  __syncwarp();
+  __syncthreads();
 #pragma unroll 8
-  for (int i = m + lane; i < n; i += 32) w[i] = 0.f;
+  for (int i = m + tid; i < n; i += threads) w[i] = 0.f;
 }
 
 template <int CPR>  // 16-byte chunks per row
-__global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, int stages) {
+__global__ void __launch_bounds__(kCmpMaxWarps * 32) kv_compact_kernel(const CompactParams p,
+                                                                      int stages) {
   constexpr int kRowBytes = CPR * 16;
-  extern __shared__ __align__(128) unsigned char ring[];  // [stages][32] rows
-  // Where each row goes (nullptr: it does not move), behind the ring.
+  constexpr int kStageBytes = 32 * kRowBytes + 32 * 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t bars[kCmpMaxWarps * kCmpMaxStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  // This warp's ring: [stages][32] rows, and where each row goes (nullptr: it
+  // does not move).
+  unsigned char* ring = smem + warp * stages * kStageBytes;
   unsigned char*(*to_ring)[32] =
       reinterpret_cast<unsigned char*(*)[32]>(ring + stages * 32 * kRowBytes);
-  __shared__ uint64_t full[kCmpMaxStages];
-  const int lane = threadIdx.x;
+  uint64_t* full = bars + warp * stages;
   if (lane == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 32);
     fence_barrier_init();
@@ -376,18 +406,16 @@ __global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, i
   __syncwarp();
   grid_dep_wait();
   grid_dep_launch_dependents();
-  // The weights go first: last, they would be the launch's tail.
-  const int h = blockIdx.x, s = blockIdx.y;
-  const int job = p.weights ? (int)blockIdx.z - 1 : (int)blockIdx.z;  // -1: weights, 0: K, 1: V
+  const int h = blockIdx.x, s = blockIdx.y, job = blockIdx.z;  // 0: K, 1: V, 2: weights
   int n = p.context_lens[s];
   if (n < 0 || n > p.max_len) {
-    if (lane == 0 && h == 0 && job == 0) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+    if (threadIdx.x == 0 && h == 0 && job == 0) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
     n = n < 0 ? 0 : p.max_len;
   }
   const int m = min(n, p.budget);
   const size_t row = (size_t)s * p.num_kv_heads + h;
   const int32_t* keep = p.keep + row * p.budget;
-  if (job < 0) {
+  if (job == 2) {
     compact_weights(p, keep, p.weights + row * p.weights_stride, n, m);
     return;
   }
@@ -396,7 +424,9 @@ __global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, i
   const int32_t* src_row = p.src_tables + (size_t)s * p.max_blocks_per_seq;
   const int32_t* dst_row = p.dst_tables + (size_t)s * p.dst_blocks_per_seq;
   const int mask = p.block_size - 1;
-  const int tiles = (m + 31) / 32;
+  // The warp's q-th tile is tile q * warps + warp; a round is one tile per warp.
+  const int rounds = ((m + 31) / 32 + warps - 1) / warps;
+  auto first_row = [&](int q) { return (q * warps + warp) * 32; };
   auto at = [&](int block, int pos) {
     return cache +
            (((long long)block * p.num_kv_heads + h) * p.block_size + (pos & mask)) * kRowBytes;
@@ -410,7 +440,7 @@ __global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, i
   auto fetch = [&](int g) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = (g * 4 + u) * 32 + lane;
+      const int i = first_row(g * 4 + u) + lane;
       fut.k[u] = i < m ? __ldg(keep + i) : -1;
       fut.db[u] = i < m ? __ldg(dst_row + (i >> p.log2_block)) : 0;
     }
@@ -418,7 +448,7 @@ __global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, i
   auto resolve = [&](int g) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = (g * 4 + u) * 32 + lane;
+      const int i = first_row(g * 4 + u) + lane;
       const bool good = fut.k[u] >= i && fut.k[u] < n;
       if (i < m && !good) atomicOr(p.status, PKV_DEV_BAD_KEEP);
       nxt.k[u] = i < m && good ? fut.k[u] : -1;
@@ -429,12 +459,12 @@ __global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, i
   fetch(0);
   resolve(0);
   fetch(1);
-  auto load = [&](int j, int st) {
-    const int i = j * 32 + lane, u = j & 3;
+  auto load = [&](int q, int st) {
+    const int i = first_row(q) + lane, u = q & 3;
     if (u == 0) {
       cur = nxt;
-      resolve(j / 4 + 1);
-      fetch(j / 4 + 2);
+      resolve(q / 4 + 1);
+      fetch(q / 4 + 2);
     }
     int k = cur.k[0], sb = cur.sb[0], db = cur.db[0];
 #pragma unroll
@@ -475,36 +505,38 @@ __global__ void __launch_bounds__(32) kv_compact_kernel(const CompactParams p, i
     load(ahead++, ahead_st);
     if (++ahead_st == stages) ahead_st = 0;
   };
-  while (ahead < min(stages - 2, tiles)) load_next();
+  while (ahead < min(stages - 2, rounds)) load_next();
   const int seg = min(p.block_size, 32);  // rows of a tile in one destination block
   const unsigned seg_bits = (seg == 32 ? kFull : (1u << seg) - 1u) << (lane & ~(seg - 1));
   int st = 0, phase = 0;
   bool ok = true;
-  for (int j = 0; j < tiles; ++j) {
-    if (ahead < tiles) {
-      // Its stage was last read by the stores of tile j - 2, of which this lane's
+  for (int q = 0; q < rounds; ++q) {
+    if (ok && ahead < rounds) {
+      // Its stage was last read by the stores of tile q - 2, of which this lane's
       // are done once at most its newest group is not.
       asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       __syncwarp();
       load_next();
     }
-    if (!mbar_wait_warp(&full[st], phase, p.status)) {
-      ok = false;
-      break;
+    // (A wait that gives up, never expected, leaves ok false: the loop runs on
+    // without copies, so that the barriers stay matched.)
+    if (ok && !mbar_wait_warp(&full[st], phase, p.status)) ok = false;
+    if (warps > 1) __syncthreads();  // every warp's tile of the round has landed
+    if (ok) {
+      // The rows were written by plain copies: order them before the bulk copy.
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      unsigned char* to = to_ring[st][lane];
+      const unsigned who = __ballot_sync(kFull, to != nullptr);
+      const int left = m - first_row(q);
+      const unsigned there = left >= 32 ? kFull : (left > 0 ? (1u << left) - 1u : 0u);
+      const unsigned char* src = ring + (st * 32 + lane) * kRowBytes;
+      if ((who & seg_bits) == (there & seg_bits)) {  // the block's rows side by side
+        if (to && (lane & (seg - 1)) == 0) bulk_store(to, src, __popc(who & seg_bits) * kRowBytes);
+      } else if (to) {
+        bulk_store(to, src, kRowBytes);
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-    // The rows were written by plain copies: order them before the bulk copy.
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    unsigned char* to = to_ring[st][lane];
-    const unsigned who = __ballot_sync(kFull, to != nullptr);
-    const int left = m - j * 32;
-    const unsigned there = left >= 32 ? kFull : (1u << left) - 1u;
-    const unsigned char* src = ring + (st * 32 + lane) * kRowBytes;
-    if ((who & seg_bits) == (there & seg_bits)) {  // the block's rows side by side
-      if (to && (lane & (seg - 1)) == 0) bulk_store(to, src, __popc(who & seg_bits) * kRowBytes);
-    } else if (to) {
-      bulk_store(to, src, kRowBytes);
-    }
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     if (++st == stages) {
       st = 0;
       phase ^= 1;
@@ -567,12 +599,15 @@ cudaError_t launch_kv_evict_select(SelectParams p, int num_seqs, int sm_count,
 
 cudaError_t launch_kv_compact(const CompactParams& p, int num_seqs, int sm_count,
                               cudaStream_t stream) {
-  // Stages of one warp's ring: what an SM's shared memory holds for its share of
-  // the warps that move rows, so that all of them run at once.
-  const int tile = 32 * p.head_dim * 2, stage = tile + 32 * 8;
-  const long long warps = 2LL * p.num_kv_heads * num_seqs;
-  const long long per_sm = (warps + sm_count - 1) / sm_count;
-  const long long room = kCmpSmBytes / per_sm - kCmpFixedBytes;
+  // One warp alone moves about 40 GB/s: as many warps per CTA as give the launch
+  // seven per SM (which filled HBM), and for each a ring of as many tiles as the
+  // SM's shared memory holds for its share of the CTAs, so that all run at once.
+  const long long ctas = 2LL * p.num_kv_heads * num_seqs;
+  int warps = 1;
+  while (warps < kCmpMaxWarps && ctas * warps * 2 <= 7LL * sm_count) warps *= 2;
+  const int stage = 32 * p.head_dim * 2 + 32 * 8;
+  const long long per_sm = (ctas + sm_count - 1) / sm_count;
+  const long long room = (kCmpSmBytes / per_sm - kCmpFixedBytes) / warps;
   const int stages = (int)std::max<long long>(
       kCmpMinStages, std::min<long long>(kCmpMaxStages, room / stage));
   const dim3 grid(p.num_kv_heads, num_seqs, p.weights ? 3 : 2);
@@ -584,12 +619,13 @@ cudaError_t launch_kv_compact(const CompactParams& p, int num_seqs, int sm_count
   if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
     for (auto k : {kv_compact_kernel<8>, kv_compact_kernel<16>}) {
       err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kCmpMaxStages * (32 * 256 + 32 * 8));
+                                 kCmpSmBytes - kCmpFixedBytes);
       if (err != cudaSuccess) return err;
     }
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
-  return launch_overlapped(kernel, grid, dim3(32), (size_t)stages * stage, stream, p, stages);
+  return launch_overlapped(kernel, grid, dim3(32 * warps), (size_t)warps * stages * stage, stream,
+                           p, stages);
 }
 
 }  // namespace pkv
