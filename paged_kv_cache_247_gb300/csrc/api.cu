@@ -414,6 +414,8 @@ pkv_status_t paged_decode_impl(void* out, const void* q, const void* k_new, cons
     plan = {true, partition_size ? partition_size
                                  : tc_partition(num_seqs, num_kv_heads, max_context_len)};
     if (!pkv::decode_tc_supported(head_dim, group, plan.partition)) return PKV_ERR_UNSUPPORTED;
+    if (num_parts_for(max_context_len, plan.partition) * num_kv_heads * num_seqs > 0x7fffffffLL)
+      return PKV_ERR_UNSUPPORTED;  // work items are counted in 32 bits
   }
   const int head_chunks = plan.tc ? 1 : (group + gt - 1) / gt;
   const int part = plan.partition;

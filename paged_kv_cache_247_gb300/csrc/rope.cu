@@ -251,7 +251,7 @@ cudaError_t launch_rope_typed(const RopeParams& p, int num_tokens, cudaStream_t 
       1LL, std::min({(long long)kRopeTokens, span / units, (long long)num_tokens / 1024}));
   const long long want = (tokens * units + kRopeUnits - 1) / kRopeUnits;
   const int threads = (int)std::min<long long>(kRopeThreads, (want + 31) / 32 * 32);
-  const dim3 grid((num_tokens + tokens - 1) / tokens);
+  const dim3 grid((unsigned)(((long long)num_tokens + tokens - 1) / tokens));
   return p.interleaved ? launch_overlapped(rope_kv_append_kernel<T, kInterleaved>, grid,
                                            dim3(threads), 0, stream, p, num_tokens, tokens)
                        : launch_overlapped(rope_kv_append_kernel<T, kHalf>, grid, dim3(threads), 0,

@@ -100,13 +100,20 @@ __global__ void __launch_bounds__(kDwThreads) decode_weights_kernel(const Decode
 //   issuer warp         the products; owns the tensor memory
 //   column warp         each Q tile's log-sums and positions into a ring
 //
-// Every Q tile is read from L2 once per KT key tiles: with KT = 1 and two CTAs
-// per SM the Q tiles (32 KiB for 4.2 MFLOP) came at 10 TB/s and bounded the
-// kernel (8 chunks of 2,048 over contexts of 4,096, 32 heads over 8 of 128:
-// 423 us; KT = 2: 370 us).  Where a sequence has at most 32 rows per KV head
-// (a short window), NR = 32, KT = 1 and one warpgroup leave room for four CTAs
-// per SM, which hide each other's chain of latencies (16 prompts, 40 heads,
-// window 32: 47 -> 27 us).
+// What bounds it is the chain from one product to the next through four S^T
+// buffers: a wait on a ready barrier takes a warp about 150 cycles, eight MMAs
+// and their commit 700, the sums of 128 columns 1,900 with four warps per
+// scheduler.  On 8 chunks of 2,048 queries over contexts of 4,096 (32 heads over
+// 8 of 128) the products alone would take 187 us (64 cycles per 128 x 128 x 16)
+// and the exponentials 174 (32 a cycle and SM).  Measured: 628 us with KT = 1 and
+// every product masked, 423 with masks only where some row does not see some key,
+// 370 with KT = 2 (half the Q tiles per key); 290 of them remain with the sums
+// left out.  Slower: K as an operand in tensor memory (three warpgroups 402,
+// 96-row tiles 407), an issuer warp per key tile and asynchronous copies of the
+// log-sums (395), a buffer given back once its last 64 columns are in registers
+// (408).  Where a sequence has at most 32 rows per KV head (a short window),
+// NR = 32, KT = 1 and one warpgroup leave room for four CTAs per SM, which hide
+// each other's chain of latencies (16 prompts, 40 heads, window 32: 47 -> 27 us).
 
 constexpr int kKeys = kTileKeys;
 
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(PwShape<D, NR>::kThreads, PwShape<D, NR>::kCta
   int ctx = p.context_lens[s];
   const long long cap = min((long long)p.max_context_len,
                             (long long)p.max_blocks_per_seq * p.block_size);
-  if (nq <= 0 || ctx < nq) return;  // flagged by the attention kernel
+  if (nq <= 0 || q0 < 0 || ctx < nq) return;  // (a context too short: flagged by the attention)
   if (ctx > cap) ctx = (int)cap;
   const int key0 = kt * KT * kKeys;
   if (key0 >= ctx) return;
