@@ -201,11 +201,12 @@ def _same_device(first, *rest):
     return index
 
 
-def _workspace(workspace, size, index):
-    """Address and bytes of the caller's workspace, or of one allocated here
-    (torch keeps its memory until the stream's work on it is done)."""
+def _workspace(workspace, size, like):
+    """The caller's workspace, or one of ``size()`` bytes allocated here beside
+    ``like``, an fp32 tensor (torch keeps its memory until the stream's work on
+    it is done); and its address and bytes."""
     if workspace is None:
-        workspace = torch.empty(size(), dtype=torch.uint8, device=torch.device("cuda", index))
+        workspace = like.new_empty((size() + 3) >> 2)
     else:
         _cuda(workspace, "workspace")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -264,7 +265,7 @@ def paged_attn_decode_weights(out, weights, q, k_cache, v_cache, block_tables, c
         with torch.cuda.device(dev):
             return decode_weights_workspace_size(*sizes)
 
-    workspace, ws_ptr, ws_len = _workspace(workspace, size, dev)
+    workspace, ws_ptr, ws_len = _workspace(workspace, size, weights)
     _launch("pkv_paged_attn_decode_weights", dev, out.data_ptr(), weights.data_ptr(),
             weights.shape[2], float(decay), q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
@@ -295,7 +296,7 @@ def paged_attn_prefill_weights(out, weights, q, query_start, k_cache, v_cache, b
     dev = _same_device(q, out, weights, query_start, k_cache, v_cache, block_tables,
                        context_lens, workspace)
     workspace, ws_ptr, ws_len = _workspace(
-        workspace, lambda: _lib.load().pkv_prefill_weights_workspace_size(T, Hq), dev)
+        workspace, lambda: _lib.load().pkv_prefill_weights_workspace_size(T, Hq), weights)
     _launch("pkv_paged_attn_prefill_weights", dev, out.data_ptr(), weights.data_ptr(),
             weights.shape[2], float(decay), int(window), q.data_ptr(), T,
             query_start.data_ptr(), int(max_query_len), k_cache.data_ptr(), v_cache.data_ptr(),

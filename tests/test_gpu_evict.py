@@ -209,9 +209,13 @@ def test_decode_weights(cuda_device, dtype, hq, hkv, D, B, lens, part, decay, sl
         weights.fill_(float("nan"))                 # overwritten unread
     old = weights.clone()
     out = torch.full_like(case.q, float("nan"))
+    # whatever the workspace held before
+    ws = torch.full((pkv.decode_weights_workspace_size(S, hq, hkv, D, case.max_context_len, part)
+                     // 4,), float("nan"), device="cuda")
     res = pkv.paged_attn_decode_weights(out, weights, case.q, case.k_cache, case.v_cache,
                                         case.block_tables, case.context_lens, case.scale,
-                                        case.max_context_len, decay=decay, partition_size=part)
+                                        case.max_context_len, decay=decay, partition_size=part,
+                                        workspace=ws)
     assert res is out
     assert_within_tol(out, oracle_decode(case), case.q.dtype, "out")
     _check_weights(weights, old, case, case.q, [1] * S, decay)
@@ -282,7 +286,9 @@ def test_prefill_weights(cuda_device, dtype, hq, hkv, D, B, lens, chunks, window
     out = torch.full_like(q, 3.0)
     args = (q, start, case.k_cache, case.v_cache, case.block_tables, case.context_lens, case.scale,
             case.max_context_len, max(chunks))
-    pkv.paged_attn_prefill_weights(out, weights, *args, window=window, decay=decay)
+    pkv.paged_attn_prefill_weights(out, weights, *args, window=window, decay=decay,
+                                   workspace=torch.full((q.shape[0] * hq,), float("nan"),
+                                                        device="cuda"))
     plain = torch.full_like(q, 3.0)
     pkv.paged_attn_prefill(plain, *args)
     assert torch.equal(out, plain)                  # the same attention, bit for bit
@@ -637,6 +643,34 @@ def test_a_run_that_evicts(cuda_device, dtype, hq, hkv, D, B):
     for s in ids:
         alloc.free_seq(s)
     assert alloc.stats()["free_blocks"] == 60
+
+
+def test_two_calls_at_once(cuda_device):
+    """The same operators on two streams at a time, each with its own batch."""
+    cases = [W.make_decode_case(20 + i, 6, 16, 4, 128, 16, "bf16", [2000, 1, 700, 129, 0, 1500],
+                                pool_factor=1.1, device=cuda_device) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(c.q) for c in cases]
+    weights = [_old_weights(6, 4, 2000, i) for i in range(2)]
+    olds = [w.clone() for w in weights]
+    keeps = [torch.empty((6, 4, 300), dtype=torch.int32, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, s, o, w, old, k in zip(cases, streams, outs, weights, olds, keeps):
+            with torch.cuda.stream(s):
+                w.copy_(old)
+                pkv.paged_attn_decode_weights(o, w, c.q, c.k_cache, c.v_cache, c.block_tables,
+                                              c.context_lens, c.scale, 2000)
+                pkv.kv_evict_select(k, w, c.context_lens, 2000, recent=20, sinks=1)
+    torch.cuda.synchronize()
+    for c, o, w, old, k in zip(cases, outs, weights, olds, keeps):
+        assert_within_tol(o, oracle_decode(c), c.q.dtype, "out")
+        _check_weights(w, old, c, c.q, [1] * 6, 1.0)
+        w_np, k_np = w.cpu().numpy(), k.cpu().numpy()
+        for s, n in enumerate(c.context_lens.tolist()):
+            for h in range(4):
+                ref = oracle.evict_select(w_np[s, h], n, 300, 20, 1)
+                assert k_np[s, h].tolist() == ref + [-1] * (300 - len(ref))
 
 
 def test_chain_captured_on_another_stream(cuda_device):
