@@ -173,6 +173,16 @@ __device__ __forceinline__ bool group_any(int kg, bool v) {
 
 __device__ __forceinline__ void group_sync(int kg) { named_barrier_sync(1 + kg, 128); }
 
+// tma_load_group with the source marked as streamed once.
+__device__ __forceinline__ void tma_load_group_once(void* dst, const CUtensorMap* map, int g,
+                                                    uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(g), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+
 // Add an unsplit item's weights from this CTA's logits in buffer b: thread t of
 // 128 in warpgroup `wg` of `wgs` that share the positions.
 template <int NH>
@@ -212,10 +222,13 @@ __device__ __forceinline__ void add_weights(const DecodeParams& p, const Item& i
 // is a whole context, one more warpgroup finishes its weights while the others
 // stream the next item: the logits of two items lie in this CTA's own scratch,
 // which is used over and over and so stays in L2.  The partitions of a split
-// context leave logits and (m, l) for decode_weights_kernel.  (64 sequences of
-// 8k over 8 KV heads, groups of 4: 388 us with that kernel after an unsplit
-// decode too, 343 us so; the last item's weights, which nothing overlaps, are
-// shared with the key warpgroups: 360 us without.)
+// context leave logits and (m, l) for decode_weights_kernel.  64 sequences of 8k
+// over 8 KV heads (groups of 4): 388 us with that kernel after an unsplit decode
+// too; 360 us so; 343 us with the key warpgroups' help for the last item, which
+// nothing overlaps; 327 us (the copy rate) with K and V marked as streamed once,
+// without which they push the logits out to HBM and back.  64 sequences of
+// lognormal lengths over 40 single heads: 152 -> 131 us, 86 % of the copy rate:
+// the CTAs' fixed walk of unequal items ends unevenly.
 template <typename T, int NH, int D, bool kWeights>
 __global__ void __launch_bounds__(TcShape<NH, D>::kThreads + (kWeights ? 128 : 0), 1)
     paged_decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
@@ -309,6 +322,8 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads + (kWeights ? 128 : 0
     const int B = p.block_size;
     prefetch_tensormap(map);
     if (is_k) prefetch_tensormap(&qmap);
+    // The logits in the CTAs' scratch are wanted again, K and V are not.
+    [[maybe_unused]] const uint64_t policy = kWeights ? policy_evict_first() : 0;
     int kt = 0, k_item = 0, issued = 0, q_issued = 0;
     bool ok = true;
     for (int j = blockIdx.x; ok && j < num_items; j += gridDim.x) {
@@ -382,9 +397,14 @@ __global__ void __launch_bounds__(TcShape<NH, D>::kThreads + (kWeights ? 128 : 0
         }
         if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)nseg * B * D * sizeof(T));
         __syncwarp();
-        if (lane < nseg)
-          tma_load_group(ring + st * kKvTile + lane * (B / 8) * kGroupKV, map,
-                         ((phys * p.num_kv_heads + it.kvh) * B) / 8, &full[st]);
+        if (lane < nseg) {
+          void* dst = ring + st * kKvTile + lane * (B / 8) * kGroupKV;
+          const int g8 = ((phys * p.num_kv_heads + it.kvh) * B) / 8;
+          if constexpr (kWeights)
+            tma_load_group_once(dst, map, g8, &full[st], policy);
+          else
+            tma_load_group(dst, map, g8, &full[st]);
+        }
         issued = kt + 1;
       }
       ++k_item;
