@@ -30,7 +30,8 @@
  *     Argument checks happen on the host before anything is enqueued; a call
  *     that returns an error has enqueued nothing.
  *   - Stream order is kept as for any kernel.  The decode, append and copy
- *     kernels are launched with programmatic stream serialization: their
+ *     kernels, and those of the calls for a cache smaller than the history
+ *     (pkv_paged_attn_prefill_weights' attention excepted), are launched with programmatic stream serialization: their
  *     blocks may be placed on the GPU while the previous kernel on the stream
  *     is still running, but each waits for that kernel to finish (and for its
  *     writes to be visible) before it reads or writes memory.  A kernel the
@@ -48,7 +49,9 @@
  *   - The kernels never spin on another block or another launch.  Apart from
  *     the wait for the previous kernel on the stream described above, the
  *     only waits are on their own copies into shared memory, each bounded in
- *     time (PKV_DEV_WAIT_TIMEOUT).
+ *     time (PKV_DEV_WAIT_TIMEOUT).  (The blocks of a thread-block cluster,
+ *     which the hardware places together, meet at cluster barriers:
+ *     pkv_kv_evict_select.)
  */
 #ifndef PAGEDKV_H_
 #define PAGEDKV_H_
@@ -428,8 +431,8 @@ pkv_status_t pkv_rope_kv_append(
  * otherwise; pkv_paged_attn_prefill_weights takes larger groups, one query per
  * sequence), whatever pkv_set_decode_path says.
  *   weights_stride  >= max_context_len
- *   workspace       pkv_decode_weights_workspace_size(...) bytes, which is
- *                   never 0: the step's logits are kept there
+ *   workspace       pkv_decode_weights_workspace_size(...) bytes, split
+ *                   context or not: the step's logits are kept there
  * Everything else as pkv_paged_attn_decode. */
 pkv_status_t pkv_paged_attn_decode_weights(
     void* out, float* weights, int64_t weights_stride, float decay,

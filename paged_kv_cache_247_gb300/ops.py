@@ -20,6 +20,14 @@ def _stream_handle(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _c_int(value, name):
+    """``value`` as the int the C call takes (ctypes would drop higher bits)."""
+    value = int(value)
+    if not -2**31 <= value < 2**31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
+
+
 def _launch(name, index, *args):
     """Call the library with the current stream of CUDA device ``index`` as the
     last argument and that device current (the calls plan, and launch, on the
@@ -233,8 +241,9 @@ def _weights(weights, num_seqs, num_kv_heads, max_context_len):
 def decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
                                   partition_size=0):
     """Bytes of scratch :func:`paged_attn_decode_weights` needs."""
-    n = _lib.load().pkv_decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads,
-                                                      head_dim, max_context_len, partition_size)
+    n = _lib.load().pkv_decode_weights_workspace_size(
+        num_seqs, num_q_heads, num_kv_heads, head_dim,
+        _c_int(max_context_len, "max_context_len"), _c_int(partition_size, "partition_size"))
     if n == _SIZE_T_MAX:
         raise ValueError("invalid decode sizes")
     return n
@@ -269,8 +278,9 @@ def paged_attn_decode_weights(out, weights, q, k_cache, v_cache, block_tables, c
     _launch("pkv_paged_attn_decode_weights", dev, out.data_ptr(), weights.data_ptr(),
             weights.shape[2], float(decay), q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-            context_lens.data_ptr(), int(max_context_len), S, Hq, Hkv, D, B, NB, float(scale),
-            _DTYPE_CODE[q.dtype], int(partition_size), ws_ptr, ws_len)
+            context_lens.data_ptr(), _c_int(max_context_len, "max_context_len"), S, Hq, Hkv, D, B,
+            NB, float(scale), _DTYPE_CODE[q.dtype], _c_int(partition_size, "partition_size"),
+            ws_ptr, ws_len)
     return out
 
 
@@ -298,11 +308,11 @@ def paged_attn_prefill_weights(out, weights, q, query_start, k_cache, v_cache, b
     workspace, ws_ptr, ws_len = _workspace(
         workspace, lambda: _lib.load().pkv_prefill_weights_workspace_size(T, Hq), weights)
     _launch("pkv_paged_attn_prefill_weights", dev, out.data_ptr(), weights.data_ptr(),
-            weights.shape[2], float(decay), int(window), q.data_ptr(), T,
-            query_start.data_ptr(), int(max_query_len), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
-            int(max_context_len), S, Hq, Hkv, D, B, NB, float(scale), _DTYPE_CODE[q.dtype],
-            ws_ptr, ws_len)
+            weights.shape[2], float(decay), _c_int(window, "window"), q.data_ptr(), T,
+            query_start.data_ptr(), _c_int(max_query_len, "max_query_len"), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), _c_int(max_context_len, "max_context_len"), S, Hq, Hkv, D, B,
+            NB, float(scale), _DTYPE_CODE[q.dtype], ws_ptr, ws_len)
     return out
 
 
@@ -477,8 +487,9 @@ def kv_evict_select(keep, weights, context_lens, max_context_len, recent=0, sink
     dev = _same_device(keep, weights, context_lens, new_lens)
     _launch("pkv_kv_evict_select", dev, keep.data_ptr(),
             None if new_lens is None else new_lens.data_ptr(), weights.data_ptr(),
-            weights.shape[2], context_lens.data_ptr(), int(max_context_len), S, Hkv, budget,
-            int(recent), int(sinks))
+            weights.shape[2], context_lens.data_ptr(),
+            _c_int(max_context_len, "max_context_len"), S, Hkv, budget,
+            _c_int(recent, "recent"), _c_int(sinks, "sinks"))
     return keep
 
 
@@ -519,8 +530,8 @@ def kv_compact(k_cache, v_cache, block_tables, keep, context_lens, weights=None,
             None if weights is None else weights.data_ptr(),
             0 if weights is None else weights.shape[2], block_tables.data_ptr(),
             block_tables.shape[1], dst_tables.data_ptr(), dst_tables.shape[1], keep.data_ptr(),
-            budget, context_lens.data_ptr(), int(max_context_len), S, Hkv, D, B, NB,
-            _DTYPE_CODE[dtype])
+            budget, context_lens.data_ptr(), _c_int(max_context_len, "max_context_len"), S, Hkv,
+            D, B, NB, _DTYPE_CODE[dtype])
 
 
 def check_copy_pairs(pairs, num_blocks):

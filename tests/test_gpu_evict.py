@@ -389,6 +389,18 @@ def test_select_row_longer_than_shared_memory(cuda_device):
     _check_select(w, [419999], 100000, 7, 0)
 
 
+@pytest.mark.parametrize("S,H,n", [
+    (1, 1, 780000),      # 16 CTAs a row, each with close to all of an SM's shared memory
+    (1, 2, 1000003),     # 16 CTAs a row, keys read again in every pass
+    (40, 8, 60001),      # one CTA a row, keys read again
+])
+def test_select_keys_per_cta(cuda_device, S, H, n):
+    """Shares of a row up to and beyond what a CTA holds in shared memory."""
+    w = torch.exp(2 * torch.randn((S, H, n + 1), generator=_gen(n), device="cuda"))
+    w[0, 0, ::3] = 1.5                               # ties on both sides of the CTAs' bounds
+    _check_select(w, [n] + [max(1, n - 977 * s) for s in range(1, S)], n // 3, 500, 4)
+
+
 @pytest.mark.parametrize("S,H", [(1, 3), (20, 8), (40, 8), (90, 8)])
 def test_select_rows_per_launch(cuda_device, S, H):
     """Every number of CTAs per row, sequences below and above the budget."""
@@ -643,6 +655,30 @@ def test_a_run_that_evicts(cuda_device, dtype, hq, hkv, D, B):
     for s in ids:
         alloc.free_seq(s)
     assert alloc.stats()["free_blocks"] == 60
+
+
+def test_arguments_beyond_32_bits(cuda_device):
+    """Not cut down to their low bits: 2**32 recent positions are not none."""
+    big = 2**32
+    keep = torch.zeros((1, 2, 4), dtype=torch.int32, device="cuda")
+    w = torch.ones((1, 2, 64), device="cuda")
+    lens = torch.tensor([40], dtype=torch.int32, device="cuda")
+    kc = torch.zeros((4, 2, 16, 64), dtype=torch.float16, device="cuda")
+    q = torch.zeros((1, 2, 64), dtype=torch.float16, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    start = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for call in (
+            lambda: pkv.kv_evict_select(keep, w, lens, 64, recent=big),
+            lambda: pkv.kv_evict_select(keep, w, lens, 64, sinks=-big),
+            lambda: pkv.kv_compact(kc, kc.clone(), table, keep, lens, max_context_len=big + 64),
+            lambda: pkv.paged_attn_decode_weights(torch.empty_like(q), w, q, kc, kc, table, lens,
+                                                  0.1, 64, partition_size=big),
+            lambda: pkv.paged_attn_prefill_weights(torch.empty_like(q), w, q, start, kc, kc,
+                                                   table, lens, 0.1, 64, 1, window=-big),
+            lambda: pkv.paged_attn_prefill_weights(torch.empty_like(q), w, q, start, kc, kc,
+                                                   table, lens, 0.1, 64, big)):
+        with pytest.raises(ValueError):
+            call()
 
 
 def test_two_calls_at_once(cuda_device):
