@@ -43,6 +43,22 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return x != x ? 0u : k;
 }
 
+// Steps for single lanes without a branch around each, which would keep several
+// of them from being in flight.
+__device__ __forceinline__ void count_if(bool go, uint32_t* bin) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], 1;\n\t}" ::"r"(
+          (uint32_t)go),
+      "r"(smem_addr(bin))
+      : "memory");
+}
+__device__ __forceinline__ void store_if(uint32_t go, int32_t* to, int32_t x) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}" ::"r"(go),
+      "l"(to), "r"(x)
+      : "memory");
+}
+
 // Inclusive prefix sum over a warp.
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
   const int lane = threadIdx.x & 31;
@@ -120,7 +136,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     // The digit of a key that has the prefix: k ^ prefix has zeros above it.
     auto count = [&](uint32_t k) {
       const uint32_t d = k ^ prefix;
-      if (d <= span) atomicAdd(&hb[d >> shift], 1u);
+      count_if(d <= span, hb + (d <= span ? d >> shift : 0u));
     };
     if (pass == 0 || !kCached) {
       // Four loads per thread are issued before any is used.
@@ -143,12 +159,21 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
       }
     } else {
       const int m4 = m & ~3;
-      for (int i = 4 * tid; i < m4; i += 4 * kSelThreads) {
-        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
-        count(k.x);
-        count(k.y);
-        count(k.z);
-        count(k.w);
+#pragma unroll 1
+      for (int i = 4 * tid; i < m4; i += 8 * kSelThreads) {
+        const uint4 a = *reinterpret_cast<const uint4*>(keys + i);
+        // (a key that differs from the prefix above the digit is not counted)
+        uint4 b = make_uint4(~prefix, ~prefix, ~prefix, ~prefix);
+        if (i + 4 * kSelThreads < m4)
+          b = *reinterpret_cast<const uint4*>(keys + i + 4 * kSelThreads);
+        count(a.x);
+        count(a.y);
+        count(a.z);
+        count(a.w);
+        count(b.x);
+        count(b.y);
+        count(b.z);
+        count(b.w);
       }
       if (tid < m - m4) count(keys[m4 + tid]);
     }
@@ -224,12 +249,18 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
   auto masks = [&](int base, uint32_t least) {  // of keys of at least this value
     uint32_t mine = 0;
     const int groups = min(32, (w1 - base + 31) / 32);
-#pragma unroll 4
-    for (int g = 0; g < groups; ++g) {
-      const int i = base + 32 * g + lane;
-      const uint32_t k = i >= w1 ? 0u : (kCached ? keys[i] : weight_key(w[i]));
-      const uint32_t a = __ballot_sync(kFull, k >= least);
-      if (lane == g) mine = a;
+    for (int g = 0; g < groups; g += 8) {
+      uint32_t k[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = base + 32 * (g + j) + lane;
+        k[j] = i >= w1 ? 0u : (kCached ? keys[i] : weight_key(w[i]));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t a = __ballot_sync(kFull, k[j] >= least);
+        if (lane == g + j) mine = a;
+      }
     }
     // (a key past the part's end reads as 0, which `least` may be)
     const int left = w1 - base - 32 * lane;
@@ -274,6 +305,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     }
     above += __reduce_add_sync(kFull, g);
     equal += __reduce_add_sync(kFull, e);
+    cluster.barrier_arrive();  // done with the other CTAs' shared memory
   }
   const uint32_t below = (1u << lane) - 1u;
   int32_t* to = keep + lo;
@@ -294,15 +326,21 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     const uint32_t incl = warp_scan(kept);
     const uint32_t first = at + incl - kept;
     const int groups = min(32, (w1 - base + 31) / 32);
-#pragma unroll 4
-    for (int g = 0; g < groups; ++g) {
-      const uint32_t k = __shfl_sync(kFull, gm, g);
-      const uint32_t f = __shfl_sync(kFull, first, g);
-      if (k >> lane & 1u) to[f + __popc(k & below)] = c0 + base + 32 * g + lane;
+    for (int g = 0; g < groups; g += 8) {  // (the mask of a group past the last is 0)
+      uint32_t k[8], f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        k[j] = __shfl_sync(kFull, gm, g + j);
+        f[j] = __shfl_sync(kFull, first, g + j);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        store_if(k[j] >> lane & 1u, to + f[j] + __popc(k[j] & below),
+                 c0 + base + 32 * (g + j) + lane);
     }
     at += __shfl_sync(kFull, incl, 31);
   }
-  if (C > 1) cluster.sync();  // no CTA leaves while another may read its counts
+  if (C > 1) cluster.barrier_wait();  // no CTA leaves while another may read its counts
 }
 
 // ---- compaction ------------------------------------------------------------
