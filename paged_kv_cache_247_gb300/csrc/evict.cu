@@ -82,6 +82,15 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
 // Then each warp marks the kept keys of its contiguous part, one bit mask per
 // 32 keys, and after a prefix sum over warps and CTAs writes their positions:
 // ascending, and of the keys that equal the threshold the lowest positions.
+//
+// Bound by instruction issue and the shared-memory additions with many rows
+// (512 rows of 6-8k: 13.7 us), by the chain of phases with few (8 rows of
+// 131,072 on 16 CTAs each: 14.4 us, 12.5 of them in the kernel; 5.2 go to the
+// three exchanges over the cluster).  A branch per key or group in place of the
+// predicated steps cost 1.4 and 2.7 us.  No better: more loads in flight (15.1
+// against 15.5 us with 8 and 16.2 with 16, before the predicated steps), marking
+// the keys that have the prefix first (14.0 and 14.4), 512 or 1,024 threads per
+// CTA for few rows (15.3 and 23.6: they keep the next launch off the SM).
 template <bool kCached>
 __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     kv_evict_select_kernel(const SelectParams p) {
@@ -591,7 +600,7 @@ cudaError_t launch_kv_evict_select(SelectParams p, int num_seqs, int sm_count,
                                    cudaStream_t stream) {
   // CTAs per row: as many as keep the whole launch within one wave, each with
   // 1,024 keys or more.  (8 rows of 131,072: 95 us on one CTA each with 1,024
-  // threads, 33 us on 8, 17 us on 16.)
+  // threads, 33 us on 8, 14 us on 16.)
   const long long rows = (long long)num_seqs * p.num_kv_heads;
   int cluster = 1;
   while (cluster < kSelMaxCluster && rows * cluster * 2 <= (long long)kSelPerSm * sm_count &&
