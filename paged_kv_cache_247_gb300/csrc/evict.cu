@@ -77,28 +77,33 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
 // 10 bits, from the top).  Each CTA counts the digits of its keys in shared
 // memory and sums them by 64; one warp per CTA adds up the cluster's 32 coarse
 // counts, then the 64 bins of the coarse one that holds the wanted rank (all
-// CTAs find the same digit; distributed shared memory carries 96 words per CTA
-// and pass).  The keys stay in shared memory, so the row is read from HBM once.
-// Then each warp marks the kept keys of its contiguous part, one bit mask per
-// 32 keys, and after a prefix sum over warps and CTAs writes their positions:
-// ascending, and of the keys that equal the threshold the lowest positions.
+// CTAs find the same digit; the coarse counts are written into every CTA's shared
+// memory before the barrier, the 64 bins read from the others after it).  The keys
+// stay in shared memory, so the row is read from HBM once.  Then each warp marks
+// the kept keys of its contiguous part, one bit mask per 32 keys, and after a
+// prefix sum over warps and CTAs writes their positions: ascending, and of the
+// keys that equal the threshold the lowest positions.
 //
 // Bound by instruction issue and the shared-memory additions with many rows
-// (512 rows of 6-8k: 13.7 us), by the chain of phases with few (8 rows of
-// 131,072 on 16 CTAs each: 14.4 us, 12.5 of them in the kernel; 5.2 go to the
-// three exchanges over the cluster).  A branch per key or group in place of the
-// predicated steps cost 1.4 and 2.7 us.  No better: more loads in flight (15.1
-// against 15.5 us with 8 and 16.2 with 16, before the predicated steps), marking
-// the keys that have the prefix first (14.0 and 14.4), 512 or 1,024 threads per
-// CTA for few rows (15.3 and 23.6: they keep the next launch off the SM).
+// (512 rows of 6-8k: 13.9 us), by the chain of phases with few (8 rows of
+// 131,072 on 16 CTAs each: 13.8 us; 14.5 with every count read from the others
+// after a barrier, of which the three exchanges took 5.2).  A branch per key or
+// group in place of the predicated steps cost 1.4 and 2.7 us.  No better: more
+// loads in flight (15.1 against 15.5 us with 8 and 16.2 with 16, before the
+// predicated steps), marking the keys that have the prefix first (14.0 and 14.4),
+// 512 or 1,024 threads per CTA for few rows (15.3 and 23.6: they keep the next
+// launch off the SM).
 template <bool kCached>
 __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     kv_evict_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) uint32_t hist[2 * kSelBins];
-  __shared__ uint32_t coarse[2][kSelBins / kSelCoarse];  // (passes alternate, as in hist)
+  // Coarse counts of every CTA of the cluster (passes alternate, as in hist), and
+  // how many keys above and at the threshold each holds: written by their owners.
+  __shared__ uint32_t coarse[2][kSelMaxCluster][kSelBins / kSelCoarse];
+  __shared__ uint2 kept_in[kSelMaxCluster];
   __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
-  __shared__ uint32_t s_digit, s_need, s_count, cta_gt, cta_eq;
+  __shared__ uint32_t s_digit, s_need, s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < 2 * kSelBins / 4; i += kSelThreads)
     reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
@@ -131,7 +136,8 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
   const int c0 = lo + min(rank * share, hi - lo);
   const int m = min(share, hi - c0);
   const float* w = p.weights + row * p.weights_stride + c0;
-  __syncthreads();  // the cleared histograms
+  if (C > 1) cluster.barrier_arrive();  // this CTA runs: the others may write to it
+  __syncthreads();                      // the cleared histograms
 
   // The need-th largest among the keys that share the prefix.  Once exactly
   // that many do, all of them are kept: every key from the prefix on.
@@ -193,32 +199,30 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
       uint32_t sum = (b.x + b.y) + (b.z + b.w);
 #pragma unroll
       for (int d = 1; d < kSelCoarse / 4; d <<= 1) sum += __shfl_xor_sync(kFull, sum, d);
-      if (i % (kSelCoarse / 4) == 0) coarse[pass & 1][i / (kSelCoarse / 4)] = sum;
+      if (i % (kSelCoarse / 4) == 0) coarse[pass & 1][rank][i / (kSelCoarse / 4)] = sum;
     }
-    if (C > 1)
+    __syncthreads();
+    if (C > 1) {
+      if (pass == 0) cluster.barrier_wait();
+      uint32_t* mine = &coarse[pass & 1][rank][lane];
+      for (int q = warp; q < C; q += kSelWarps)
+        if (q != rank) *cluster.map_shared_rank(mine, q) = *mine;
       cluster.sync();
-    else
-      __syncthreads();
+    }
     if (warp == 0) {
       // Lane l holds coarse count 31 - l, then bins 2 (31 - l) + 1 and
       // 2 (31 - l) of the one found: prefix sums run from the largest digit.
-      // (The loads from all CTAs are in flight together: one after another
-      // they took 1.6 us with 16 CTAs.)
-      uint32_t c = coarse[pass & 1][31 - lane];
-      if (C > 1) {
-        uint32_t x[kSelMaxCluster];
+      uint32_t c = 0;
 #pragma unroll
-        for (int q = 0; q < kSelMaxCluster; ++q)
-          x[q] = q < C && q != rank ? cluster.map_shared_rank(coarse[pass & 1], q)[31 - lane] : 0u;
-#pragma unroll
-        for (int q = 0; q < kSelMaxCluster; ++q) c += x[q];
-      }
+      for (int q = 0; q < kSelMaxCluster; ++q)
+        if (q < C) c += coarse[pass & 1][q][31 - lane];
       uint32_t incl = warp_scan(c);
       const int hit = __ffs(__ballot_sync(kFull, incl >= need)) - 1;
       const uint32_t rest = need - __shfl_sync(kFull, incl - c, hit);  // wanted within the 64 bins
       const int bin = (31 - hit) * kSelCoarse + 2 * (31 - lane);
       uint32_t b1 = hb[bin + 1], b0 = hb[bin];
       if (C > 1) {
+        // (All loads in flight together: one after another they took 0.8 us.)
         uint2 x[kSelMaxCluster];
 #pragma unroll
         for (int q = 0; q < kSelMaxCluster; ++q)
@@ -302,19 +306,11 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
   uint32_t equal = warp > 0 ? __shfl_sync(kFull, se, warp - 1) : 0u;
   if (C > 1) {
     const uint32_t tg = __shfl_sync(kFull, sg, 31), te = __shfl_sync(kFull, se, 31);
-    if (tid == 0) {
-      cta_gt = tg;
-      cta_eq = te;
-    }
-    cluster.sync();
-    uint32_t g = 0, e = 0;
-    if (lane < rank) {
-      g = *cluster.map_shared_rank(&cta_gt, lane);
-      e = *cluster.map_shared_rank(&cta_eq, lane);
-    }
-    above += __reduce_add_sync(kFull, g);
-    equal += __reduce_add_sync(kFull, e);
-    cluster.barrier_arrive();  // done with the other CTAs' shared memory
+    if (warp == 0 && lane < C) *cluster.map_shared_rank(&kept_in[rank], lane) = make_uint2(tg, te);
+    cluster.sync();  // (no CTA reads another's memory from here on)
+    const uint2 x = lane < rank ? kept_in[lane] : make_uint2(0, 0);
+    above += __reduce_add_sync(kFull, x.x);
+    equal += __reduce_add_sync(kFull, x.y);
   }
   const uint32_t below = (1u << lane) - 1u;
   int32_t* to = keep + lo;
@@ -349,7 +345,6 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm)
     }
     at += __shfl_sync(kFull, incl, 31);
   }
-  if (C > 1) cluster.barrier_wait();  // no CTA leaves while another may read its counts
 }
 
 // ---- compaction ------------------------------------------------------------
