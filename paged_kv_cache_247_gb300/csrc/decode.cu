@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(SmemLayout<T, D, GT>::kThreads, LayoutFor<D, G
     ctx = ctx < 0 ? 0 : ctx_cap;
   }
   const int t_begin = part * p.partition_size;
-  const int t_end = min(ctx, t_begin + p.partition_size);
-  const int nparts_seq = (ctx + p.partition_size - 1) / p.partition_size;
+  const int t_end = partition_end(ctx, t_begin, p.partition_size);
+  const int nparts_seq = context_partitions(ctx, p.partition_size);
   if (t_begin >= t_end) {
     if (ctx == 0 && part == 0) {  // empty context: the output is zero
       uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + ((size_t)s * p.num_q_heads + h0) * D;
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(128) paged_decode_reduce_kernel(const DecodePa
   const long long cap_ll = min((long long)p.max_context_len,
                                (long long)p.max_blocks_per_seq * p.block_size);
   ctx = ctx < 0 ? 0 : (ctx > cap_ll ? (int)cap_ll : ctx);
-  const int np = (ctx + p.partition_size - 1) / p.partition_size;
+  const int np = context_partitions(ctx, p.partition_size);
   if (np <= 1) return;  // written directly by the decode kernel
   const float* mrow = p.ws_m + (size_t)pair * p.num_parts;
   const float* lrow = p.ws_l + (size_t)pair * p.num_parts;

@@ -148,9 +148,9 @@ __device__ __forceinline__ Item item_from(const DecodeParams& p, int j, int ctx)
   if (ctx > cap) ctx = (int)cap;
   it.ctx = ctx;
   it.t_begin = it.part * p.partition_size;
-  it.t_end = min(ctx, it.t_begin + p.partition_size);
+  it.t_end = partition_end(ctx, it.t_begin, p.partition_size);
   it.n_tiles = it.t_begin < it.t_end ? (it.t_end - it.t_begin + kKeys - 1) / kKeys : 0;
-  it.nparts_seq = (ctx + p.partition_size - 1) / p.partition_size;
+  it.nparts_seq = context_partitions(ctx, p.partition_size);
   return it;
 }
 

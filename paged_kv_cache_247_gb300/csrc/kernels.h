@@ -7,6 +7,19 @@
 
 namespace pkv {
 
+// The partitions of a context, in 32 bits: any int32 partition size is taken, so
+// that ctx + partition and t_begin + partition may pass 2^31 (not 2^32).
+__host__ __device__ inline int context_partitions(int ctx, int partition) {
+  return (int)(((unsigned)ctx + (unsigned)partition - 1u) / (unsigned)partition);
+}
+
+// End of the partition that starts at t_begin (the context's, where that is
+// earlier).
+__host__ __device__ inline int partition_end(int ctx, int t_begin, int partition) {
+  const unsigned end = (unsigned)t_begin + (unsigned)partition;
+  return (unsigned)ctx < end ? ctx : (int)end;
+}
+
 // Everything one paged decode launch needs.  Filled and checked by the API
 // layer; the kernels trust it.
 struct DecodeParams {

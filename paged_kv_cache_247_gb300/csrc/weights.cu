@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kDwThreads) decode_weights_kernel(const Decode
   int ctx = p.context_lens[s];
   ctx = ctx < 0 ? 0 : (ctx > cap ? (int)cap : ctx);
   if (t0 >= ctx) return;
-  const int np = (ctx + p.partition_size - 1) / p.partition_size;
+  const int np = context_partitions(ctx, p.partition_size);
   if (np <= 1) return;  // done by the decode kernel
   const size_t row0 = (size_t)s * p.num_q_heads + (size_t)kvh * p.group;
   const int lane = threadIdx.x & 31;
