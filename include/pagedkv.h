@@ -129,6 +129,7 @@ int pkv_version(void);
  *                 <= max_blocks_per_seq * block_size
  *   max_context_len  host-side upper bound on context_lens (sizes the grid)
  *   head_dim      64 or 128;  block_size 8, 16, 32, 64 or 128
+ *   scale         finite, of either sign or zero
  *   partition_size   tokens per split-context partition: 0 lets the library
  *                 choose (pkv_decode_partition_size); otherwise a positive
  *                 multiple of 32.  When ceil(max_context_len / partition_size)

@@ -53,6 +53,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
@@ -115,13 +116,14 @@ struct PrefillParams {
   int group_pow2;   // rows per query in a tile (group rounded up to a power of two)
   int block_size;
   int num_blocks;
-  float qscale;     // scale * log2(e)
+  float qscale;     // |scale| * log2(e), a scale of 0 counting as 1: always above 0
   int num_seqs;
   int q_tiles;          // CTAs per (sequence, KV head)
   int pairs_per_group;  // (sequence, KV head) pairs whose items are launched together
   int total_queries;    // rows of q and out
   float* lse;           // kLse: base-2 log-sum of each row [total_queries, Hq]
   int prefetch_stride;  // work items between a CTA and the one likely to follow it on its SM
+  float q_factor;       // -1, 0 or 1: the sign of scale
 };
 
 // A Q box (as tma_load_token_heads copies it) fetched into L2 only: no
@@ -144,7 +146,9 @@ __device__ __forceinline__ uint32_t tile_chunk_offset(int r, int c) {
 // ---- the kernel -----------------------------------------------------------
 
 // kLse: each row's log-sum is written for the accumulated attention weights.
-template <typename T, int D, bool kLse>
+// kFactor: the query rows are multiplied by q_factor (scales of zero and below;
+// a branch in the one kernel cost 1 % at scales above it).
+template <typename T, int D, bool kLse, bool kFactor>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
     paged_prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap,
@@ -346,11 +350,33 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       }
       mma_commit_warp(&s_full[t]);
     };
+    // The softmax takes its maxima before it scales and masks with -inf, both of
+    // which need qscale > 0: a scale of zero or below multiplies the query rows
+    // by 0 or -1 instead (exact; NaN and infinities times 0 stay NaN).
+    [[maybe_unused]] auto apply_factor = [&](int t) {
+      uint4* rows = reinterpret_cast<uint4*>(sQ + t * L::kQTile);
+#pragma unroll 1
+      for (int i = lane; i < L::kQTile / 16; i += 32) {
+        uint4 w = rows[i];
+        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = Cvt<T>::to_float2(u[k]);
+          u[k] = Cvt<T>::from_float2(x.x * p.q_factor, x.y * p.q_factor);
+        }
+        rows[i] = w;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
     bool ok = mbar_wait_warp(&k_full[0], 0, p.status);
 #pragma unroll
     for (int t = 0; t < kRowTiles; ++t) {
       if (!ok || n_t[t] == 0) continue;
       ok = mbar_wait_warp(&q_full[t], 0, p.status);
+      if constexpr (kFactor) {
+        if (ok) apply_factor(t);
+      }
       tc_fence_after();
       if (ok) issue_s(t, 0);
     }
@@ -478,8 +504,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 #pragma unroll
         for (int c = 0; c < kBN; ++c)
           if (key0 + c > pos) sv[c] = -CUDART_INF_F;
-        // Row max with 8 independent chains (scaling by qscale > 0 commutes
-        // with the max).
+        // Row max with 8 independent chains (scaling by qscale, which is above
+        // 0, commutes with the max).
         float mx[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx[k] = sv[k];
@@ -599,23 +625,24 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 
 // ---- host side ------------------------------------------------------------
 
-template <typename T, int D, bool kLse>
-cudaError_t launch_prefill_lse(const PrefillParams& p, const CUtensorMap& qm,
-                                 const CUtensorMap& km, const CUtensorMap& vm, int q_tiles,
-                                 int num_seqs, cudaStream_t stream) {
+template <typename T, int D, bool kLse, bool kFactor>
+cudaError_t launch_prefill_variant(const PrefillParams& p, const CUtensorMap& qm,
+                                   const CUtensorMap& km, const CUtensorMap& vm, int q_tiles,
+                                   int num_seqs, cudaStream_t stream) {
   using L = PrefillSmem<D>;
   static unsigned long long configured = 0;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    err = cudaFuncSetAttribute(paged_prefill_kernel<T, D, kLse>,
+    err = cudaFuncSetAttribute(paged_prefill_kernel<T, D, kLse, kFactor>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
     if (err != cudaSuccess) return err;
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
   const dim3 grid((unsigned)((long long)q_tiles * p.num_kv_heads * num_seqs));
-  paged_prefill_kernel<T, D, kLse><<<grid, kPrefillThreads, L::kBytes, stream>>>(p, qm, km, vm);
+  paged_prefill_kernel<T, D, kLse, kFactor>
+      <<<grid, kPrefillThreads, L::kBytes, stream>>>(p, qm, km, vm);
   return cudaGetLastError();
 }
 
@@ -623,8 +650,13 @@ template <typename T, int D>
 cudaError_t launch_prefill_typed(const PrefillParams& p, const CUtensorMap& qm,
                                  const CUtensorMap& km, const CUtensorMap& vm, int q_tiles,
                                  int num_seqs, cudaStream_t stream) {
-  return p.lse ? launch_prefill_lse<T, D, true>(p, qm, km, vm, q_tiles, num_seqs, stream)
-               : launch_prefill_lse<T, D, false>(p, qm, km, vm, q_tiles, num_seqs, stream);
+  if (p.q_factor != 1.f)
+    return p.lse
+               ? launch_prefill_variant<T, D, true, true>(p, qm, km, vm, q_tiles, num_seqs, stream)
+               : launch_prefill_variant<T, D, false, true>(p, qm, km, vm, q_tiles, num_seqs, stream);
+  return p.lse
+             ? launch_prefill_variant<T, D, true, false>(p, qm, km, vm, q_tiles, num_seqs, stream)
+             : launch_prefill_variant<T, D, false, false>(p, qm, km, vm, q_tiles, num_seqs, stream);
 }
 
 }  // namespace
@@ -662,7 +694,8 @@ cudaError_t launch_paged_prefill(const PrefillArgs& a, cudaStream_t stream, bool
   p.group_pow2 = gp;
   p.block_size = a.block_size;
   p.num_blocks = a.num_blocks;
-  p.qscale = a.scale * 1.4426950408889634f;
+  p.q_factor = a.scale > 0.f ? 1.f : (a.scale < 0.f ? -1.f : 0.f);
+  p.qscale = (a.scale == 0.f ? 1.f : std::fabs(a.scale)) * 1.4426950408889634f;
   const int rows_q = kRowTiles * (kBM / gp);  // queries per CTA
   const int q_tiles = (a.max_query_len + rows_q - 1) / rows_q;
   if ((long long)q_tiles * a.num_kv_heads * a.num_seqs > 0x7fffffffLL) {
