@@ -45,7 +45,8 @@
  *   - Strides given as int64_t count elements.  Accumulated attention weights
  *     are fp32 [num_seqs, num_kv_heads, >= the contexts] with weights_stride
  *     elements between rows: weights[s][h][t] belongs to position t of batch
- *     row s, whatever blocks the position lives in.
+ *     row s, whatever blocks the position lives in.  (They may be NULL where
+ *     max_context_len is 0.)
  *   - The kernels never spin on another block or another launch.  Apart from
  *     the wait for the previous kernel on the stream described above, the
  *     only waits are on their own copies into shared memory, each bounded in

@@ -332,8 +332,9 @@ constexpr int kMaxPositions = 1 << 30;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// (No position, no weight: a tensor without elements has no address.)
 pkv_status_t check_weights(const WeightsArgs& w, int max_context_len) {
-  if (!w.weights || !aligned4(w.weights) || w.stride < max_context_len || !isfinite(w.decay))
+  if ((!w.weights && max_context_len > 0) || !aligned4(w.weights) || w.stride < max_context_len || !isfinite(w.decay))
     return PKV_ERR_INVALID_ARG;
   return max_context_len > kMaxPositions ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
@@ -802,7 +803,7 @@ pkv_status_t pkv_kv_evict_select(int32_t* keep, int32_t* new_lens, const float* 
       budget > kMaxPositions)
     return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
-  if (!keep || !weights || !context_lens) return PKV_ERR_INVALID_ARG;
+  if (!keep || (!weights && max_context_len > 0) || !context_lens) return PKV_ERR_INVALID_ARG;
   if (new_lens == context_lens) return PKV_ERR_INVALID_ARG;  // other heads still read it
   if (!aligned4(keep) || !aligned4(new_lens) || !aligned4(weights) || !aligned4(context_lens))
     return PKV_ERR_INVALID_ARG;

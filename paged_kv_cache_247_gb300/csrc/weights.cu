@@ -506,6 +506,7 @@ cudaError_t launch_prefill_weights(const PrefillArgs& a, cudaStream_t stream, bo
   const int nr = most * p.group_pow2 <= 32 ? 32 : 128;  // query rows per tile
   const int keys = kKeys * (nr == 128 ? PwShape<128, 128>::KT : PwShape<128, 32>::KT);
   p.key_tiles = (a.max_context_len + keys - 1) / keys;  // CTAs per (sequence, KV head)
+  if (p.key_tiles == 0) return cudaSuccess;  // no sequence holds a position
   const long long ctas = (long long)p.key_tiles * a.num_kv_heads * a.num_seqs;
   CUtensorMap qm, km;
   const long long rows = (long long)a.num_blocks * a.num_kv_heads * a.block_size;
