@@ -688,6 +688,7 @@ pkv_status_t paged_prefill_impl(void* out, const void* q, int total_queries,
   a.num_blocks = num_blocks;
   a.scale = scale;
   a.dtype = dtype;
+  if (wa && pkv::prefill_weights_ctas(a) > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   cudaError_t err = status_word(&a.status);
   if (err != cudaSuccess) return cuda_fail(err);
   a.sm_count = sm_count() > 0 ? sm_count() : kAssumedSms;

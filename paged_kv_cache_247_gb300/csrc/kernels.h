@@ -155,6 +155,10 @@ struct PrefillWeightsParams {
   int key_tiles;
 };
 
+// CTAs of launch_prefill_weights: a call of more than 2^31 - 1 has to be refused
+// before its attention is launched.
+long long prefill_weights_ctas(const PrefillArgs& a);
+
 // Accumulated attention weights of a prompt chunk, after launch_paged_prefill
 // with a.lse set.
 cudaError_t launch_prefill_weights(const PrefillArgs& a, cudaStream_t stream, bool* unsupported);

@@ -479,6 +479,32 @@ cudaError_t launch_decode_weights(const DecodeParams& p, cudaStream_t stream) {
   return launch_overlapped(decode_weights_kernel, grid, dim3(kDwThreads), 0, stream, p);
 }
 
+namespace {
+
+int pow2_group(const PrefillArgs& a) {
+  int g = 1;
+  while (g < a.num_q_heads / a.num_kv_heads) g <<= 1;
+  return g;
+}
+
+// Query rows per tile.
+int tile_rows(const PrefillArgs& a) {
+  const long long most = a.window > 0 ? std::min(a.window, a.max_query_len) : a.max_query_len;
+  return most * pow2_group(a) <= 32 ? 32 : 128;
+}
+
+// CTAs per (sequence, KV head).
+int key_tiles(const PrefillArgs& a) {
+  const int keys = kKeys * (tile_rows(a) == 128 ? PwShape<128, 128>::KT : PwShape<128, 32>::KT);
+  return (a.max_context_len + keys - 1) / keys;
+}
+
+}  // namespace
+
+long long prefill_weights_ctas(const PrefillArgs& a) {
+  return (long long)key_tiles(a) * a.num_kv_heads * a.num_seqs;
+}
+
 cudaError_t launch_prefill_weights(const PrefillArgs& a, cudaStream_t stream, bool* unsupported) {
   *unsupported = false;
   PrefillWeightsParams p{};
@@ -496,22 +522,18 @@ cudaError_t launch_prefill_weights(const PrefillArgs& a, cudaStream_t stream, bo
   p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = a.num_kv_heads;
   p.group = a.num_q_heads / a.num_kv_heads;
-  p.group_pow2 = 1;
-  while (p.group_pow2 < p.group) p.group_pow2 <<= 1;
+  p.group_pow2 = pow2_group(a);
   p.block_size = a.block_size;
   p.num_blocks = a.num_blocks;
   p.total_queries = a.total_queries;
   p.qscale = a.scale * 1.4426950408889634f;
-  const long long most = a.window > 0 ? std::min(a.window, a.max_query_len) : a.max_query_len;
-  const int nr = most * p.group_pow2 <= 32 ? 32 : 128;  // query rows per tile
-  const int keys = kKeys * (nr == 128 ? PwShape<128, 128>::KT : PwShape<128, 32>::KT);
-  p.key_tiles = (a.max_context_len + keys - 1) / keys;  // CTAs per (sequence, KV head)
-  if (p.key_tiles == 0) return cudaSuccess;  // no sequence holds a position
-  const long long ctas = (long long)p.key_tiles * a.num_kv_heads * a.num_seqs;
+  const int nr = tile_rows(a);
+  p.key_tiles = key_tiles(a);
+  const long long ctas = prefill_weights_ctas(a);
+  if (ctas == 0) return cudaSuccess;  // no sequence holds a position
   CUtensorMap qm, km;
   const long long rows = (long long)a.num_blocks * a.num_kv_heads * a.block_size;
-  if (ctas > 0x7fffffffLL ||
-      !make_cache_map(&km, a.k_cache, a.dtype, rows, a.head_dim, a.block_size) ||
+  if (!make_cache_map(&km, a.k_cache, a.dtype, rows, a.head_dim, a.block_size) ||
       !make_token_head_map(&qm, a.q, a.dtype, a.total_queries, a.num_q_heads, a.head_dim,
                            p.group_pow2, nr / p.group_pow2)) {
     *unsupported = true;
