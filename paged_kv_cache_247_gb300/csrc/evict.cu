@@ -591,50 +591,75 @@ __global__ void __launch_bounds__(kCmpMaxWarps * 32) kv_compact_kernel(const Com
 
 }  // namespace
 
+namespace {
+
+// A launch of kv_evict_select_kernel as clusters of `cluster` CTAs.
+struct SelectLaunch {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg;
+  SelectLaunch(int rows_x, int rows_y, int cluster, size_t smem, cudaStream_t stream) : cfg{} {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(rows_x * cluster, rows_y);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+// The largest cluster that the device (or the part of it this process may use)
+// places with the most shared memory a CTA asks for.
+int largest_cluster(cudaStream_t stream) {
+  for (int c = kSelMaxCluster; c > 1; c /= 2) {
+    SelectLaunch l(1, 1, c, (size_t)kSelMaxKeys * 4, stream);
+    int fit = 0;
+    const cudaError_t err =
+        cudaOccupancyMaxActiveClusters(&fit, kv_evict_select_kernel<true>, &l.cfg);
+    if (err != cudaSuccess) (void)cudaGetLastError();
+    if (err == cudaSuccess && fit > 0) return c;
+  }
+  return 1;
+}
+
+}  // namespace
+
 cudaError_t launch_kv_evict_select(SelectParams p, int num_seqs, int sm_count,
                                    cudaStream_t stream) {
-  // CTAs per row: as many as keep the whole launch within one wave, each with
-  // 1,024 keys or more.  (8 rows of 131,072: 95 us on one CTA each with 1,024
-  // threads, 33 us on 8, 14 us on 16.)
-  const long long rows = (long long)num_seqs * p.num_kv_heads;
-  int cluster = 1;
-  while (cluster < kSelMaxCluster && rows * cluster * 2 <= (long long)kSelPerSm * sm_count &&
-         p.max_context_len / (cluster * 2) >= 1024)
-    cluster *= 2;
-  p.cluster = cluster;
-  const int share = (std::max(1, (p.max_context_len + cluster - 1) / cluster) + 31) / 32 * 32;
-  const bool cached = share <= kSelMaxKeys;
-  const size_t smem = cached ? (size_t)share * 4 : 0;
-
-  auto kernel = cached ? kv_evict_select_kernel<true> : kv_evict_select_kernel<false>;
-  static unsigned long long configured = 0;  // bit per device ordinal (< 64)
+  static int largest[64] = {};  // largest_cluster of a device; 0: not asked yet
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+  int most = dev < 64 ? __atomic_load_n(&largest[dev], __ATOMIC_ACQUIRE) : 0;
+  if (most == 0) {
     err = cudaFuncSetAttribute(kv_evict_select_kernel<true>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4);
     for (auto k : {kv_evict_select_kernel<true>, kv_evict_select_kernel<false>})
       if (err == cudaSuccess)
         err = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err != cudaSuccess) return err;
-    if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
+    most = largest_cluster(stream);
+    if (dev < 64) __atomic_store_n(&largest[dev], most, __ATOMIC_RELEASE);
   }
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.num_kv_heads * cluster, num_seqs);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, kernel, p);
+  // CTAs per row: as many as keep the whole launch within one wave, each with
+  // 1,024 keys or more.  (8 rows of 131,072: 95 us on one CTA each with 1,024
+  // threads, 33 us on 8, 14 us on 16.)
+  const long long rows = (long long)num_seqs * p.num_kv_heads;
+  int cluster = 1;
+  while (cluster < most && rows * cluster * 2 <= (long long)kSelPerSm * sm_count &&
+         p.max_context_len / (cluster * 2) >= 1024)
+    cluster *= 2;
+  p.cluster = cluster;
+  const int share = (std::max(1, (p.max_context_len + cluster - 1) / cluster) + 31) / 32 * 32;
+  const bool cached = share <= kSelMaxKeys;
+  auto kernel = cached ? kv_evict_select_kernel<true> : kv_evict_select_kernel<false>;
+  SelectLaunch l(p.num_kv_heads, num_seqs, cluster, cached ? (size_t)share * 4 : 0, stream);
+  err = cudaLaunchKernelEx(&l.cfg, kernel, p);
   const cudaError_t last = cudaGetLastError();  // clears the error, as after <<<>>>
   return err != cudaSuccess ? err : last;
 }
