@@ -431,10 +431,19 @@ pkv_status_t pkv_rope_kv_append(
  * their values.  Runs the tensor-core kernel: groups of at most 32 query
  * heads, partition_size 0 or a multiple of 128 (PKV_ERR_UNSUPPORTED
  * otherwise; pkv_paged_attn_prefill_weights takes larger groups, one query per
- * sequence), whatever pkv_set_decode_path says.
+ * sequence, with its tiles mostly empty: 120 us for 16 sequences of 4,096 over
+ * 4 KV heads of 128 with groups of 33, whose bytes take 20), whatever
+ * pkv_set_decode_path says.
  *   weights_stride  >= max_context_len
  *   workspace       pkv_decode_weights_workspace_size(...) bytes, split
- *                   context or not: the step's logits are kept there
+ *                   context or not: the step's logits are kept there.  It grows
+ *                   with max_context_len, not with the contexts: unsplit, two
+ *                   rows of logits per query head of a group and CTA, 4 *
+ *                   2 * CTAs * G * max_context_len bytes (at most one CTA per
+ *                   SM; 67 MB for 64 sequences over 8 KV heads with groups of 8
+ *                   and a bound of 8,192, 1.07 GB at 131,072); split, every
+ *                   logit of the call besides.  So pass a bound near the longest
+ *                   context, and keep the workspace between steps.
  * Everything else as pkv_paged_attn_decode. */
 pkv_status_t pkv_paged_attn_decode_weights(
     void* out, float* weights, int64_t weights_stride, float decay,
@@ -446,7 +455,8 @@ pkv_status_t pkv_paged_attn_decode_weights(
     int partition_size, void* workspace, size_t workspace_bytes,
     pkv_stream_t stream);
 
-/* (size_t)-1 for invalid arguments or sizes the call does not support. */
+/* Depends on the SM count of the current device.  (size_t)-1 for invalid
+ * arguments or sizes the call does not support. */
 size_t pkv_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
                                          int head_dim, int max_context_len, int partition_size);
 

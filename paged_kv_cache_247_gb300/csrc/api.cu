@@ -334,7 +334,8 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 // (No position, no weight: a tensor without elements has no address.)
 pkv_status_t check_weights(const WeightsArgs& w, int max_context_len) {
-  if ((!w.weights && max_context_len > 0) || !aligned4(w.weights) || w.stride < max_context_len || !isfinite(w.decay))
+  if ((!w.weights && max_context_len > 0) || !aligned4(w.weights) ||
+      w.stride < max_context_len || !isfinite(w.decay))
     return PKV_ERR_INVALID_ARG;
   return max_context_len > kMaxPositions ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }

@@ -221,14 +221,22 @@ __device__ __forceinline__ void add_weights(const DecodeParams& p, const Item& i
 // at the end of the context, so the base-2 logits x are kept.  Where a work item
 // is a whole context, one more warpgroup finishes its weights while the others
 // stream the next item: the logits of two items lie in this CTA's own scratch,
-// which is used over and over and so stays in L2.  The partitions of a split
-// context leave logits and (m, l) for decode_weights_kernel.  64 sequences of 8k
-// over 8 KV heads (groups of 4): 388 us with that kernel after an unsplit decode
-// too; 360 us so; 343 us with the key warpgroups' help for the last item, which
-// nothing overlaps; 327 us (the copy rate) with K and V marked as streamed once,
-// without which they push the logits out to HBM and back.  64 sequences of
-// lognormal lengths over 40 single heads: 152 -> 131 us, 86 % of the copy rate:
-// the CTAs' fixed walk of unequal items ends unevenly.
+// which is used over and over and so stays in L2 while 2 x CTAs x group x context
+// floats fit there (below).  The partitions of a split context leave logits and
+// (m, l) for decode_weights_kernel.  64 sequences of 8k over 8 KV heads (groups
+// of 4): 388 us with that kernel after an unsplit decode too; 360 us so; 343 us
+// with the key warpgroups' help for the last item, which nothing overlaps; 327 us
+// (the copy rate) with K and V marked as streamed once, without which they push the
+// logits out to HBM and back.  64 sequences of lognormal lengths over 40 single
+// heads: 152 -> 131 us, 86 % of the copy rate: the CTAs' fixed walk of unequal items
+// ends unevenly.  Split: 8 sequences of 32k 191 us (floor 163), one of 131,072 98
+// (floor 82).
+//
+// Scratch against the 129 MB of L2, 64 sequences over 8 KV heads: groups of 4 and 8
+// at 8k (34 and 67 MB) take 329 and 348 us, the copy rate and 94 % of it, of 326 us
+// for K, V and weights.  From about its size on, the logits go to HBM and back:
+// group 8 at 16k (134 MB) 707 us (floor 652) with 0.40 GB more traffic, group 16 at
+// 8k (134 MB) 442 us with 0.48 GB more, group 32 (268 MB) 617 us with 1.09 GB more.
 template <typename T, int NH, int D, bool kWeights>
 __global__ void __launch_bounds__(TcShape<NH, D>::kThreads + (kWeights ? 128 : 0), 1)
     paged_decode_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,

@@ -84,10 +84,14 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
 // prefix sum over warps and CTAs writes their positions: ascending, and of the
 // keys that equal the threshold the lowest positions.
 //
-// Bound by instruction issue and the shared-memory additions with many rows
-// (512 rows of 6-8k: 13.9 us), by the chain of phases with few (8 rows of
-// 131,072 on 16 CTAs each: 13.8 us; 14.5 with every count read from the others
-// after a barrier, of which the three exchanges took 5.2).  A branch per key or
+// Bound by the chain of phases within a CTA.  With many rows (512 rows of 6-8k,
+// 3.4 CTAs per SM: 14.0 us) an SM issues in 54 % of its cycles and uses 23 % of
+// its shared-memory wavefronts, a fifth of them the additions (of which 39 %
+// are lanes that met on a bank); of 11.1 cycles between a warp's instructions it
+// waits 3.1 for weights from HBM, 1.7 for fixed latencies, 1.4 at barriers and
+// 1.0 for shared memory.  With few rows (8 of 131,072 on 16 CTAs each: 13.8 us)
+// the exchanges between the CTAs come on top (14.5 us with every count read from
+// the others after a barrier, of which the three exchanges took 5.2).  A branch per key or
 // group in place of the predicated steps cost 1.4 and 2.7 us.  No better: more
 // loads in flight (15.1 against 15.5 us with 8 and 16.2 with 16, before the
 // predicated steps), marking the keys that have the prefix first (14.0 and 14.4),

@@ -117,8 +117,9 @@ __device__ __forceinline__ void prepare_tokens(const RopeParams& p, RopeTokens& 
 // A CTA takes as many tokens as give each thread kRopeUnits units, and issues
 // those loads before it looks at positions and slots: the angles (64-bit
 // arithmetic at a low rate, and a barrier) then overlap them.  (16,384 tokens,
-// 32 + 2 x 8 heads of 128: 88 us with the angles first and a CTA per token,
-// 68 us so.)
+// 32 + 2 x 8 heads of 128, whose units fill a CTA for each token: 78 us with the
+// angles first, 68 us so.  4 + 2 heads of 64, eight tokens a CTA: 11.1 us, 17.1
+// with one token; 48 heads of 64, two tokens a CTA: 40.9 us, 37.0 with one.)
 template <typename T, int LAYOUT>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kv_append_kernel(const RopeParams p, int num_tokens, int tokens_per_cta) {
@@ -199,7 +200,10 @@ __global__ void __launch_bounds__(kRopeThreads)
 
 // The half layout where R is not a multiple of 16, so that a pair's halves lie
 // in chunks at different offsets: one pair of elements per thread.  One CTA per
-// token.
+// token.  Bound by its 2-byte accesses and the angles ahead of them: 16,384 tokens
+// of 32 + 2 x 8 heads of 128 with R = 100 take 192 us (R = 96: 68), with heads of 64
+// and R = 46 125 us (R = 48: 41); 64 tokens 4.8 us (2.9).  Kept simple: models rotate
+// multiples of 16 in this layout, and the other layout takes any R at full speed.
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kv_append_scalar_kernel(const RopeParams p) {

@@ -103,7 +103,9 @@ __global__ void __launch_bounds__(kDwThreads) decode_weights_kernel(const Decode
 // What bounds it is the chain from one product to the next through four S^T
 // buffers: a wait on a ready barrier takes a warp about 150 cycles, eight MMAs
 // and their commit 700, the sums of 128 columns 1,900 with four warps per
-// scheduler.  On 8 chunks of 2,048 queries over contexts of 4,096 (32 heads over
+// scheduler.  That is the price of one buffer per warpgroup (the four fill tensor
+// memory): a warpgroup's sums and the product that refills its buffer alternate.
+// On 8 chunks of 2,048 queries over contexts of 4,096 (32 heads over
 // 8 of 128) the products alone would take 187 us (64 cycles per 128 x 128 x 16)
 // and the exponentials 174 (32 a cycle and SM).  Measured: 628 us with KT = 1 and
 // every product masked, 423 with masks only where some row does not see some key,
@@ -114,6 +116,8 @@ __global__ void __launch_bounds__(kDwThreads) decode_weights_kernel(const Decode
 // (408).  Where a sequence has at most 32 rows per KV head (a short window),
 // NR = 32, KT = 1 and one warpgroup leave room for four CTAs per SM, which hide
 // each other's chain of latencies (16 prompts, 40 heads, window 32: 47 -> 27 us).
+// A group that is no power of two masks every tile: the same 8 chunks with groups
+// of 3 and 7 spend 532 and 1,022 us here, with groups of 4 and 8 383 and 727.
 
 constexpr int kKeys = kTileKeys;
 

@@ -255,8 +255,10 @@ def paged_attn_decode_weights(out, weights, q, k_cache, v_cache, block_tables, c
     """:func:`paged_attn_decode` that also accumulates attention weights:
     ``weights`` (fp32 [S, Hkv, >= max_context_len]) becomes ``decay * weights``
     plus each held position's softmax weight, summed over the query heads of
-    the KV head's group.  Groups of at most 32 query heads.  Writes ``out``
-    and returns it."""
+    the KV head's group.  Groups of at most 32 query heads.  ``workspace`` (any
+    CUDA tensor of at least :func:`decode_weights_workspace_size` bytes, which
+    grow with ``max_context_len``, not with the contexts) is allocated here
+    with torch if omitted.  Writes ``out`` and returns it."""
     _attn_shapes(q, out, k_cache, v_cache)
     _cuda(block_tables, "block_tables", torch.int32, 2)
     _cuda(context_lens, "context_lens", torch.int32, 1)
@@ -291,7 +293,8 @@ def paged_attn_prefill_weights(out, weights, q, query_start, k_cache, v_cache, b
     ``weights`` (fp32 [S, Hkv, >= max_context_len]) becomes ``decay * weights``
     plus each position's softmax weights, summed over the last ``window``
     queries of its sequence's chunk (0: all) and the query heads of the KV
-    head's group.  ``workspace``: uint8, 4 bytes per query row and head.
+    head's group.  ``workspace``: 4 bytes per query row and head (allocated
+    here with torch if omitted).
     Writes ``out`` and returns it."""
     _attn_shapes(q, out, k_cache, v_cache)
     _cuda(block_tables, "block_tables", torch.int32, 2)
