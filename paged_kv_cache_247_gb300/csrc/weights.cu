@@ -115,7 +115,10 @@ __global__ void __launch_bounds__(kDwThreads) decode_weights_kernel(const Decode
 // log-sums (395), a buffer given back once its last 64 columns are in registers
 // (408).  Where a sequence has at most 32 rows per KV head (a short window),
 // NR = 32, KT = 1 and one warpgroup leave room for four CTAs per SM, which hide
-// each other's chain of latencies (16 prompts, 40 heads, window 32: 47 -> 27 us).
+// each other's chain of latencies (16 prompts, 40 heads, window 32: 47 -> 27 us;
+// 16 contexts of 4,096 over 8 KV heads, window 32: 43 us with single heads, 85 on
+// 128-row tiles.  With groups of 2 and 4, above the limit, the 128-row tiles take
+// 105 and 123 us and 32-row tiles would take 65 and 78; from 8 on the two tie).
 // A group that is no power of two masks every tile: the same 8 chunks with groups
 // of 3 and 7 spend 532 and 1,022 us here, with groups of 4 and 8 383 and 727.
 
