@@ -531,6 +531,136 @@ pkv_status_t pkv_kv_compact(
     int num_seqs, int num_kv_heads, int head_dim, int block_size, int num_blocks,
     pkv_dtype_t dtype, pkv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A cache held in 8 bits.
+ *
+ * [P2] "Why the KV cache is the thing that limits your batch": a decode step's
+ * time and the pool's size are the cache's bytes.  The calls below keep K and V
+ * as e4m3 codes, [num_blocks, num_kv_heads, block_size, head_dim] bytes as the
+ * 16-bit caches are laid out, with one scale per row (position and KV head),
+ * bfloat16 [num_blocks, num_kv_heads, block_size]:
+ *   element = code * scale,  scale = 2^e,
+ *   e the smallest integer >= -126 with max |element of the row| <= 448 * 2^e.
+ * The division by a power of two is exact, so each element is rounded once, to
+ * nearest even, and a row gives the same bits wherever it is written; read back
+ * and appended again it keeps its values.  A row with a NaN or an infinity is
+ * held as NaN as a whole (scale NaN, codes 0).
+ *
+ * pkv_block_copy copies the codes (block_bytes = num_kv_heads * block_size *
+ * head_dim) and, in a call of its own, the scales (num_kv_heads * block_size *
+ * 2).  Prompt chunks attend over cached blocks read back by pkv_block_read_fp8
+ * (pkv_paged_attn_prefill).  Codes must be 16-byte aligned, scales 16-byte
+ * aligned.
+ * ---------------------------------------------------------------------- */
+
+/* Quantise new tokens' K and V rows into their slots: pkv_kv_append for an
+ * 8-bit cache, with the same slot_mapping (distinct; negative skips a token;
+ * beyond the pool flags PKV_DEV_BAD_SLOT).
+ *
+ *   k, v          [num_tokens, num_kv_heads, head_dim] dtype, tokens *_stride
+ *                 elements apart (a multiple of 8, at least a token's row)
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (head_dim or block_size not
+ * built, 2^31 or more 16-element parts of rows in one call), PKV_ERR_CUDA. */
+pkv_status_t pkv_kv_append_fp8(
+    const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+    void* k_cache, void* v_cache, void* k_scales, void* v_scales,
+    const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, pkv_dtype_t dtype, pkv_stream_t stream);
+
+/* Read blocks back into 16 bits: for each pair i, block src_dst_pairs[2i] of
+ * the 8-bit caches, every row of it, into block src_dst_pairs[2i + 1] of k_out
+ * and v_out [num_out_blocks, num_kv_heads, block_size, head_dim].  bf16 holds
+ * the products exactly (down to its smallest normal number), fp16 rounds them
+ * once.  A source may be read into several blocks; destinations must be
+ * distinct.  Ids outside the pools skip the pair and flag PKV_DEV_BAD_BLOCK_ID.
+ * Errors as pkv_kv_append_fp8. */
+pkv_status_t pkv_block_read_fp8(
+    void* k_out, void* v_out, int num_out_blocks, const void* k_cache, const void* v_cache,
+    const void* k_scales, const void* v_scales, const int64_t* src_dst_pairs, int num_pairs,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, pkv_dtype_t dtype,
+    pkv_stream_t stream);
+
+/* Norms of the query and key heads with rotary positions, in one launch: what
+ * pkv_rope_kv_append does to q and k, for a cache that takes k from elsewhere,
+ * with each head row first normalised,
+ *   y = x * weight / sqrt(mean x^2 + eps),
+ * where q_weight / k_weight is not NULL, and with a position per axis: pair i
+ * is turned by positions[pair_axes[i]][t] * inv_freq[i] (a picture's tokens
+ * have a height and a width, a film's a time besides).  attn_factor multiplies
+ * the turned elements.  Each element is rounded once.  A token whose position
+ * on axis 0 is negative is padding: nothing is written for it.
+ *
+ *   q_out, q, k_out, k  as q_out and q of pkv_rope_kv_append: an output may be
+ *                 its input with the same stride, and must overlap neither
+ *                 input otherwise
+ *   q_weight, k_weight  [head_dim] dtype, or NULL
+ *   eps           finite, >= 0
+ *   positions     int32 [num_axes][positions_stride >= num_tokens]
+ *   pair_axes     HOST array of rot_dim / 2 axis numbers below num_axes, read
+ *                 before the call returns (NULL: axis 0 turns every pair)
+ *   inv_freq      double [rot_dim / 2]
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (head_dim not built, 65,536
+ * heads or more), PKV_ERR_CUDA. */
+pkv_status_t pkv_qk_norm_rope(
+    void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+    const void* q_weight, const void* k_weight, float eps,
+    const int32_t* positions, int64_t positions_stride, int num_axes, const uint8_t* pair_axes,
+    const double* inv_freq, int rot_dim, int interleaved, float attn_factor,
+    int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, pkv_dtype_t dtype,
+    pkv_stream_t stream);
+
+/* pkv_paged_attn_decode over an 8-bit cache.  q and out are dtype; any group
+ * size.  partition_size 0 or a multiple of 128; workspace of
+ * pkv_decode_fp8_workspace_size(...) bytes.  Everything else as there. */
+pkv_status_t pkv_paged_attn_decode_fp8(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const void* k_scales, const void* v_scales,
+    const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len,
+    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, pkv_dtype_t dtype,
+    int partition_size, void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* (size_t)-1 for invalid arguments or sizes the call does not support. */
+size_t pkv_decode_fp8_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                     int head_dim, int max_context_len, int partition_size);
+
+/* Attention of a tree of drafted tokens over an 8-bit cache: several guesses of
+ * a sequence's next tokens are checked in one pass over its cache.
+ *
+ * Sequence s brings L_s = query_start[s+1] - query_start[s] <= 64 drafted
+ * tokens, the last L_s positions of its context (as pkv_paged_attn_prefill;
+ * their rows are already in the cache).  Query j sees every position before
+ * the drafted ones, and of those the i-th where bit i of
+ * tree_masks[query_start[s] + j] is set (bits from L_s on are ignored): its
+ * ancestors and itself, for a tree.  A query that sees nothing gets zeros;
+ * what a query does not see does not reach it, NaN included.
+ *
+ *   q, out        [total_queries, num_q_heads, head_dim] dtype, total_queries
+ *                 >= query_start[num_seqs]; rows of out from
+ *                 query_start[num_seqs] on are not written
+ *   tree_masks    int64 [total_queries]
+ *   max_query_len bound on L_s (at most 64; a sequence with more flags
+ *                 PKV_DEV_BAD_CONTEXT_LEN, as does one whose context is
+ *                 shorter than L_s)
+ *   workspace     pkv_tree_fp8_workspace_size(...) bytes
+ * Everything else as pkv_paged_attn_decode_fp8. */
+pkv_status_t pkv_paged_attn_tree_fp8(
+    void* out, const void* q, int total_queries, const int32_t* query_start, int max_query_len,
+    const int64_t* tree_masks, const void* k_cache, const void* v_cache,
+    const void* k_scales, const void* v_scales,
+    const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len,
+    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, pkv_dtype_t dtype,
+    int partition_size, void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* (size_t)-1 for invalid arguments or sizes the call does not support. */
+size_t pkv_tree_fp8_workspace_size(int total_queries, int max_query_len, int num_seqs,
+                                   int num_q_heads, int num_kv_heads, int head_dim,
+                                   int max_context_len, int partition_size);
+
 /* Read (and optionally clear) the status word of the current device.
  * Synchronises `stream` first so that flags from work already enqueued on it
  * are visible.  flags may be NULL when only clearing. */

@@ -26,10 +26,13 @@ Modules:
 * :mod:`oracle.cache_ops` — the slot scatter (append) and block copy.
 * :mod:`oracle.evict` — rotary positions, accumulated attention weights, the
   choice of the positions to keep and the compaction of a cache to them.
+* :mod:`oracle.fp8` — e4m3 rows with power-of-two scales, head norms, and the
+  attention of a tree of drafted tokens.
 * :mod:`oracle.allocator` — a pure-Python refcounted block allocator model.
 
 Every function here is pinned by ``tests/test_oracle_pins.py``,
-``tests/test_oracle_evict.py`` and ``tests/test_oracle_allocator.py`` to facts and invariants that do not come
+``tests/test_oracle_evict.py``, ``tests/test_oracle_fp8.py`` and
+``tests/test_oracle_allocator.py`` to facts and invariants that do not come
 from the oracle itself; no function is "parity unpinned".
 """
 
@@ -43,4 +46,5 @@ from .attention import (  # noqa: F401
 from .cache_ops import kv_append, block_copy  # noqa: F401
 from .evict import (  # noqa: F401
     rope, attention_weights, evict_select, compact, compact_weights)
+from .fp8 import e4m3_values, quantise, norm, tree_attention  # noqa: F401
 from .allocator import OracleAllocator, OracleOutOfBlocks  # noqa: F401

@@ -17,7 +17,13 @@ Device calls (hand-written CUDA behind the C ABI of ``libpagedkv.so``):
 * :func:`paged_attn_decode_weights`, :func:`paged_attn_prefill_weights` — the
   two attentions with accumulated attention weights per cached position;
 * :func:`kv_evict_select`, :func:`kv_compact` — which positions a sequence
-  keeps, and the move of their rows to the front of its blocks.
+  keeps, and the move of their rows to the front of its blocks;
+* :func:`kv_append_fp8`, :func:`block_read_fp8` — a cache held in 8 bits: rows
+  quantised as they are appended, and blocks read back;
+* :func:`paged_attn_decode_fp8`, :func:`paged_attn_tree_fp8` — attention over
+  it, of one query per sequence or of a tree of drafted tokens;
+* :func:`qk_norm_rope` — norms and rotary positions of the query and key heads
+  in one launch.
 
 Host: :class:`BlockAllocator`, the refcounted block allocator that decides
 slots and copy-on-write pairs.  The library is loaded on first use and there
@@ -36,6 +42,11 @@ from .ops import (  # noqa: F401
     rope_kv_append,
     kv_evict_select,
     kv_compact,
+    kv_append_fp8,
+    block_read_fp8,
+    qk_norm_rope,
+    paged_attn_decode_fp8,
+    paged_attn_tree_fp8,
     kv_append,
     block_copy,
     check_copy_pairs,
@@ -43,6 +54,8 @@ from .ops import (  # noqa: F401
     debug_wait_timeout,
     decode_workspace_size,
     decode_weights_workspace_size,
+    decode_fp8_workspace_size,
+    tree_fp8_workspace_size,
     decode_partition_size,
     decode_uses_tensor_cores,
     set_decode_path,

@@ -84,6 +84,27 @@ SIGNATURES = {
     "pkv_kv_compact": (c_int, [
         c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
         c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),
+    "pkv_kv_append_fp8": (c_int, [
+        c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),
+    "pkv_block_read_fp8": (c_int, [
+        c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
+        c_int, c_int, c_int, c_int, c_void_p]),
+    "pkv_qk_norm_rope": (c_int, [
+        c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+        c_void_p, c_float, c_void_p, c_int64, c_int, ctypes.c_char_p, c_void_p, c_int, c_int,
+        c_float, c_int, c_int, c_int, c_int, c_int, c_void_p]),
+    "pkv_paged_attn_decode_fp8": (c_int, [
+        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p,
+        c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_int, c_int, c_void_p, c_size_t,
+        c_void_p]),
+    "pkv_decode_fp8_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "pkv_paged_attn_tree_fp8": (c_int, [
+        c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+        c_void_p, c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+        c_float, c_int, c_int, c_void_p, c_size_t, c_void_p]),
+    "pkv_tree_fp8_workspace_size": (c_size_t, [
+        c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
     "pkv_device_status": (c_int, [P_u32, c_int, c_void_p]),
     "pkv_debug_wait_timeout": (c_int, [c_void_p]),
     "pkv_alloc_create": (c_int, [c_int, c_int, ctypes.POINTER(c_void_p)]),

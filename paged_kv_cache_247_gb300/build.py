@@ -21,9 +21,10 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
 
 SOURCES = ["api.cu", "decode.cu", "decode_tc.cu", "prefill.cu", "cache_ops.cu", "rope.cu",
-           "weights.cu", "evict.cu", "allocator.cpp"]
+           "weights.cu", "evict.cu", "fp8_cache.cu", "norm_rope.cu", "attn_fp8.cu",
+           "allocator.cpp"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "overlap.cuh"),
-           os.path.join(CSRC, "tcgen05.cuh"),
+           os.path.join(CSRC, "tcgen05.cuh"), os.path.join(CSRC, "fp8.cuh"),
            os.path.join(CSRC, "kernels.h"),
            os.path.join(INCLUDE, "pagedkv.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -877,6 +877,294 @@ pkv_status_t pkv_kv_compact(void* k_cache, void* v_cache, float* weights, int64_
   return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
 }
 
+namespace {
+
+// The caches of a call over 8-bit rows.
+bool fp8_cache_ok(const void* k_cache, const void* v_cache, const void* k_scales,
+                  const void* v_scales) {
+  return k_cache && v_cache && k_scales && v_scales && aligned16(k_cache) && aligned16(v_cache) &&
+         aligned16(k_scales) && aligned16(v_scales);
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+}  // namespace
+
+pkv_status_t pkv_kv_append_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               void* k_cache, void* v_cache, void* k_scales, void* v_scales,
+                               const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                               int head_dim, int block_size, int num_blocks, pkv_dtype_t dtype,
+                               pkv_stream_t stream) {
+  if (num_tokens < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (!supported_block_size(block_size)) return PKV_ERR_UNSUPPORTED;
+  const int64_t row = (int64_t)num_kv_heads * head_dim;
+  if ((k_stride | v_stride) % 8 || k_stride < row || v_stride < row) return PKV_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PKV_OK;
+  if (!k || !v || !slot_mapping || !aligned16(k) || !aligned16(v) || !aligned8(slot_mapping) ||
+      !fp8_cache_ok(k_cache, v_cache, k_scales, v_scales))
+    return PKV_ERR_INVALID_ARG;
+  if (row / 16 > pkv::kMaxFp8Parts / num_tokens) return PKV_ERR_UNSUPPORTED;
+  pkv::AppendFp8Params p{};
+  p.k = k;
+  p.v = v;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = static_cast<uint16_t*>(k_scales);
+  p.v_scales = static_cast<uint16_t*>(v_scales);
+  p.slot_mapping = slot_mapping;
+  p.num_slots = (long long)num_blocks * block_size;
+  p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  cudaError_t err = status_word(&p.status);
+  if (err != cudaSuccess) return cuda_fail(err);
+  err = pkv::launch_kv_append_fp8(p, num_tokens, head_dim, dtype,
+                                  reinterpret_cast<cudaStream_t>(stream));
+  return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
+}
+
+pkv_status_t pkv_block_read_fp8(void* k_out, void* v_out, int num_out_blocks, const void* k_cache,
+                                const void* v_cache, const void* k_scales, const void* v_scales,
+                                const int64_t* src_dst_pairs, int num_pairs, int num_kv_heads,
+                                int head_dim, int block_size, int num_blocks, pkv_dtype_t dtype,
+                                pkv_stream_t stream) {
+  if (num_pairs < 0 || num_kv_heads <= 0 || num_blocks <= 0 || num_out_blocks <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (!supported_block_size(block_size)) return PKV_ERR_UNSUPPORTED;
+  if (num_pairs == 0) return PKV_OK;
+  if (!k_out || !v_out || !src_dst_pairs || !aligned16(k_out) || !aligned16(v_out) ||
+      !aligned8(src_dst_pairs) || !fp8_cache_ok(k_cache, v_cache, k_scales, v_scales))
+    return PKV_ERR_INVALID_ARG;
+  if ((long long)num_kv_heads * block_size * head_dim / 16 > pkv::kMaxFp8Parts / num_pairs)
+    return PKV_ERR_UNSUPPORTED;
+  pkv::ReadFp8Params p{};
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = static_cast<const uint16_t*>(k_scales);
+  p.v_scales = static_cast<const uint16_t*>(v_scales);
+  p.pairs = src_dst_pairs;
+  p.num_blocks = num_blocks;
+  p.num_out_blocks = num_out_blocks;
+  p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  cudaError_t err = status_word(&p.status);
+  if (err != cudaSuccess) return cuda_fail(err);
+  err = pkv::launch_block_read_fp8(p, num_pairs, head_dim, dtype,
+                                   reinterpret_cast<cudaStream_t>(stream));
+  return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
+}
+
+pkv_status_t pkv_qk_norm_rope(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                              const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* q_weight, const void* k_weight, float eps,
+                              const int32_t* positions, int64_t positions_stride, int num_axes,
+                              const uint8_t* pair_axes, const double* inv_freq, int rot_dim,
+                              int interleaved, float attn_factor, int num_tokens, int num_q_heads,
+                              int num_kv_heads, int head_dim, pkv_dtype_t dtype,
+                              pkv_stream_t stream) {
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0) return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (!isfinite(attn_factor) || !isfinite(eps) || eps < 0.f) return PKV_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (num_q_heads > 65535 || num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2) return PKV_ERR_INVALID_ARG;
+  if (num_axes < 1 || num_axes > 255 || positions_stride < num_tokens) return PKV_ERR_INVALID_ARG;
+  pkv::NormRopeParams p{};
+  static_assert(pkv::kMaxRopePairs == 64, "pairs of a head of 128");
+  for (int i = 0; pair_axes && i < rot_dim / 2; ++i) {
+    if (pair_axes[i] >= num_axes) return PKV_ERR_INVALID_ARG;
+    p.pair_axes[i] = pair_axes[i];
+  }
+  if (num_tokens == 0) return PKV_OK;
+  if (!q_out || !k_out || !q || !k || !positions || !inv_freq) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(q) || !aligned16(k) ||
+      !aligned16(q_weight) || !aligned16(k_weight) || !aligned4(positions) || !aligned8(inv_freq))
+    return PKV_ERR_INVALID_ARG;
+  if ((q_out_stride | k_out_stride | q_stride | k_stride) % 8) return PKV_ERR_INVALID_ARG;
+  const int64_t q_row = (int64_t)num_q_heads * head_dim, k_row = (int64_t)num_kv_heads * head_dim;
+  if (q_out_stride < q_row || q_stride < q_row || k_out_stride < k_row || k_stride < k_row)
+    return PKV_ERR_INVALID_ARG;
+  if ((q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride))
+    return PKV_ERR_INVALID_ARG;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q = q;
+  p.k = k;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.positions = positions;
+  p.positions_stride = positions_stride;
+  p.inv_freq = inv_freq;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.rot_dim = rot_dim;
+  p.interleaved = interleaved != 0;
+  p.eps = eps;
+  p.factor = attn_factor;
+  const cudaError_t err = pkv::launch_qk_norm_rope(p, num_tokens, head_dim, dtype,
+                                                   reinterpret_cast<cudaStream_t>(stream));
+  return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
+}
+
+namespace {
+
+struct Fp8Plan {
+  int chunks;     // work items of up to pkv::kFp8Rows query rows per (sequence, KV head, partition)
+  int partition;
+  long long parts;
+};
+
+// The split of a call over an 8-bit cache; false for sizes it does not take.
+bool fp8_plan(int total_queries, int max_query_len, int num_seqs, int num_q_heads,
+              int num_kv_heads, int head_dim, int max_context_len, int partition_size,
+              Fp8Plan* plan) {
+  if (head_dim != 64 && head_dim != 128) return false;
+  if (max_query_len > pkv::kMaxDrafts || max_context_len > kMaxPositions) return false;
+  if ((long long)total_queries * num_q_heads > 0x7fffffffLL) return false;
+  const long long rows = (long long)std::max(max_query_len, 1) * (num_q_heads / num_kv_heads);
+  const long long chunks = (rows + pkv::kFp8Rows - 1) / pkv::kFp8Rows;
+  if (num_kv_heads > 65535 || num_seqs > 65535 || chunks > 65535) return false;
+  const long long units = chunks * num_kv_heads * std::max(num_seqs, 1);
+  if (units > 0x7fffffffLL) return false;
+  plan->chunks = (int)chunks;
+  plan->partition = partition_size ? partition_size : tc_partition(1, (int)units, max_context_len);
+  plan->parts = num_parts_for(max_context_len, plan->partition);
+  return plan->parts <= 0x7fffffffLL / units;
+}
+
+size_t fp8_workspace(int total_queries, int num_q_heads, int head_dim, const Fp8Plan& plan) {
+  return plan.parts > 1 ? (size_t)total_queries * num_q_heads * plan.parts * (head_dim + 2) *
+                              sizeof(float)
+                        : 0;
+}
+
+// Shared body of the attention calls over an 8-bit cache; query_start is
+// nullptr for one query per sequence.
+pkv_status_t attn_fp8_impl(void* out, const void* q, int total_queries, const int32_t* query_start,
+                           int max_query_len, const int64_t* tree_masks, const void* k_cache,
+                           const void* v_cache, const void* k_scales, const void* v_scales,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int max_context_len, int num_seqs,
+                           int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                           int num_blocks, float scale, pkv_dtype_t dtype, int partition_size,
+                           void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (!decode_shape_ok(num_seqs, num_q_heads, num_kv_heads, max_context_len) ||
+      total_queries < 0 || max_query_len < 0)
+    return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (!isfinite(scale)) return PKV_ERR_INVALID_ARG;
+  if (partition_size < 0 || partition_size % pkv::kTcPartitionQuantum) return PKV_ERR_INVALID_ARG;
+  if (!supported_block_size(block_size)) return PKV_ERR_UNSUPPORTED;
+  Fp8Plan plan;
+  if (!fp8_plan(total_queries, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                max_context_len, partition_size, &plan))
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || total_queries == 0 || max_query_len == 0) return PKV_OK;
+  if (!out || !q || !block_tables || !context_lens || !aligned16(out) || !aligned16(q) ||
+      !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start) ||
+      !aligned8(tree_masks) || !fp8_cache_ok(k_cache, v_cache, k_scales, v_scales))
+    return PKV_ERR_INVALID_ARG;
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0 ||
+      (long long)max_blocks_per_seq * block_size < max_context_len)
+    return PKV_ERR_INVALID_ARG;
+  if ((long long)num_blocks * num_kv_heads * block_size > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  if (workspace_bytes < fp8_workspace(total_queries, num_q_heads, head_dim, plan) ||
+      (plan.parts > 1 && !workspace))
+    return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+  pkv::AttnFp8Params p{};
+  p.out = out;
+  p.q = q;
+  p.query_start = query_start;
+  p.tree_masks = tree_masks;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = static_cast<const uint16_t*>(k_scales);
+  p.v_scales = static_cast<const uint16_t*>(v_scales);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_context_len = max_context_len;
+  p.max_query_len = max_query_len;
+  p.total_queries = total_queries;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_q_heads / num_kv_heads;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax is evaluated with exp2
+  cudaError_t err = status_word(&p.status);
+  if (err != cudaSuccess) return cuda_fail(err);
+  bool unsupported = false;
+  err = pkv::launch_attn_fp8(p, head_dim, dtype, device_sms(),
+                             reinterpret_cast<cudaStream_t>(stream), &unsupported);
+  if (unsupported) return PKV_ERR_UNSUPPORTED;
+  return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
+}
+
+}  // namespace
+
+pkv_status_t pkv_paged_attn_decode_fp8(
+    void* out, const void* q, const void* k_cache, const void* v_cache, const void* k_scales,
+    const void* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    pkv_dtype_t dtype, int partition_size, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream) {
+  return attn_fp8_impl(out, q, num_seqs, nullptr, 1, nullptr, k_cache, v_cache, k_scales, v_scales,
+                       block_tables, max_blocks_per_seq, context_lens, max_context_len, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, dtype,
+                       partition_size, workspace, workspace_bytes, stream);
+}
+
+pkv_status_t pkv_paged_attn_tree_fp8(
+    void* out, const void* q, int total_queries, const int32_t* query_start, int max_query_len,
+    const int64_t* tree_masks, const void* k_cache, const void* v_cache, const void* k_scales,
+    const void* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int max_context_len, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    pkv_dtype_t dtype, int partition_size, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream) {
+  if (num_seqs > 0 && total_queries > 0 && (!query_start || !tree_masks))
+    return PKV_ERR_INVALID_ARG;
+  return attn_fp8_impl(out, q, total_queries, query_start, max_query_len, tree_masks, k_cache,
+                       v_cache, k_scales, v_scales, block_tables, max_blocks_per_seq, context_lens,
+                       max_context_len, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                       num_blocks, scale, dtype, partition_size, workspace, workspace_bytes,
+                       stream);
+}
+
+size_t pkv_decode_fp8_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_context_len, int partition_size) {
+  return pkv_tree_fp8_workspace_size(num_seqs, 1, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                     max_context_len, partition_size);
+}
+
+size_t pkv_tree_fp8_workspace_size(int total_queries, int max_query_len, int num_seqs,
+                                   int num_q_heads, int num_kv_heads, int head_dim,
+                                   int max_context_len, int partition_size) {
+  Fp8Plan plan;
+  if (!decode_shape_ok(num_seqs, num_q_heads, num_kv_heads, max_context_len) ||
+      total_queries < 0 || max_query_len < 0 || partition_size < 0 ||
+      partition_size % pkv::kTcPartitionQuantum ||
+      !fp8_plan(total_queries, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                max_context_len, partition_size, &plan))
+    return (size_t)-1;
+  return fp8_workspace(total_queries, num_q_heads, head_dim, plan);
+}
+
 pkv_status_t pkv_kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
                            const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
                            int head_dim, int block_size, int num_blocks, pkv_dtype_t dtype,

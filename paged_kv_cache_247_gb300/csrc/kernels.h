@@ -244,6 +244,107 @@ cudaError_t launch_block_copy(void* k_cache, void* v_cache, const int64_t* pairs
                               int num_pairs, int num_blocks, size_t block_bytes,
                               unsigned int* status, cudaStream_t stream);
 
+// A cache held in 8 bits (fp8.cuh): codes [NB, Hkv, B, D] and one bfloat16
+// scale per row [NB, Hkv, B].
+struct AppendFp8Params {
+  const void* k;  // [T, Hkv, D], tokens *_stride elements apart
+  const void* v;
+  long long k_stride, v_stride;
+  void* k_cache;
+  void* v_cache;
+  uint16_t* k_scales;
+  uint16_t* v_scales;
+  const int64_t* slot_mapping;
+  unsigned int* status;
+  long long num_slots;
+  int num_kv_heads;
+  int block_size;
+};
+
+// The kernels index 16-element parts of rows with 32 bits.
+constexpr long long kMaxFp8Parts = 0x7fffffffLL;
+
+cudaError_t launch_kv_append_fp8(const AppendFp8Params& p, int num_tokens, int head_dim, int dtype,
+                                 cudaStream_t stream);
+
+struct ReadFp8Params {
+  void* k_out;  // [num_out_blocks, Hkv, B, D]
+  void* v_out;
+  const void* k_cache;
+  const void* v_cache;
+  const uint16_t* k_scales;
+  const uint16_t* v_scales;
+  const int64_t* pairs;
+  unsigned int* status;
+  int num_blocks;
+  int num_out_blocks;
+  int num_kv_heads;
+  int block_size;
+};
+
+cudaError_t launch_block_read_fp8(const ReadFp8Params& p, long long num_pairs, int head_dim,
+                                  int dtype, cudaStream_t stream);
+
+// Norms and rotary positions of q and k.
+constexpr int kMaxRopePairs = 64;
+
+struct NormRopeParams {
+  void* q_out;
+  void* k_out;
+  const void* q;
+  const void* k;
+  long long q_out_stride, k_out_stride, q_stride, k_stride;
+  const void* q_weight;  // [D] or nullptr: not normalised
+  const void* k_weight;
+  const int32_t* positions;  // [axes, positions_stride]
+  long long positions_stride;
+  const double* inv_freq;
+  int num_q_heads;
+  int num_kv_heads;
+  int rot_dim;
+  int interleaved;
+  float eps;
+  float factor;
+  uint8_t pair_axes[kMaxRopePairs];  // the axis whose position turns the pair
+};
+
+cudaError_t launch_qk_norm_rope(const NormRopeParams& p, int num_tokens, int head_dim, int dtype,
+                                cudaStream_t stream);
+
+// Attention over an 8-bit cache.  query_start == nullptr: one query per
+// sequence, the whole context seen.  Otherwise the last positions of each
+// context are drafted tokens, seen as tree_masks says.
+constexpr int kMaxDrafts = 64;
+constexpr int kFp8Rows = 32;  // query rows (query, head of the group) a work item takes at most
+
+struct AttnFp8Params {
+  void* out;      // [total_queries, Hq, D]
+  const void* q;
+  const int32_t* query_start;  // [S + 1]
+  const int64_t* tree_masks;   // [total_queries]
+  const void* k_cache;
+  const void* v_cache;
+  const uint16_t* k_scales;
+  const uint16_t* v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  unsigned int* status;
+  int max_blocks_per_seq;
+  int max_context_len;
+  int max_query_len;
+  int total_queries;
+  int num_seqs;
+  int num_q_heads;
+  int num_kv_heads;
+  int group;
+  int block_size;
+  int num_blocks;
+  float qscale;  // scale * log2(e)
+};
+
+cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, int sms,
+                            cudaStream_t stream, bool* unsupported);
+
 // Diagnostic: one bounded wait on an mbarrier that nothing completes; it
 // gives up after the wait limit and raises PKV_DEV_WAIT_TIMEOUT.
 cudaError_t launch_wait_probe(unsigned int* status, cudaStream_t stream);

@@ -537,6 +537,231 @@ def kv_compact(k_cache, v_cache, block_tables, keep, context_lens, weights=None,
             D, B, NB, _DTYPE_CODE[dtype])
 
 
+def _fp8_cache(k_cache, v_cache, k_scales, v_scales):
+    """Check the caches of a call over 8-bit rows; their shape."""
+    _cuda(k_cache, "k_cache", torch.float8_e4m3fn, 4)
+    _cuda(v_cache, "v_cache", torch.float8_e4m3fn, 4)
+    _cuda(k_scales, "k_scales", torch.bfloat16, 4)
+    _cuda(v_scales, "v_scales", torch.bfloat16, 4)
+    shape = k_cache.shape
+    rows = (*shape[:3], 1)
+    if v_cache.shape != shape or k_scales.shape != rows or v_scales.shape != rows:
+        raise ValueError("the caches must have one shape [NB, H, B, D], their scales [NB, H, B, 1]")
+    return shape
+
+
+def kv_append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping):
+    """:func:`kv_append` into a cache held in 8 bits: each head row of ``k`` and
+    ``v`` ([T, Hkv, D], or slices of wider token rows) becomes float8_e4m3fn
+    codes in ``k_cache`` / ``v_cache`` ([NB, Hkv, B, D]) and one scale in
+    ``k_scales`` / ``v_scales`` (bfloat16 [NB, Hkv, B, 1]), the smallest power
+    of two that leaves no element above 448, so that ``cache.float() *
+    scales.float()`` are the rows, each element rounded once.  A row with a NaN
+    or an infinity is NaN as a whole."""
+    if not isinstance(k, torch.Tensor) or k.dtype not in _DTYPE_CODE or k.dim() != 3:
+        raise ValueError("k must be float16 or bfloat16 with 3 dimensions")
+    dtype, shape = k.dtype, k.shape
+    NB, Hkv, B, D = _fp8_cache(k_cache, v_cache, k_scales, v_scales)
+    ks, vs = _token_rows(k, "k", dtype, shape), _token_rows(v, "v", dtype, shape)
+    _cuda(slot_mapping, "slot_mapping", torch.int64, 1)
+    T = shape[0]
+    if shape[1] != Hkv or shape[2] != D:
+        raise ValueError("shape mismatch between new tokens and the caches")
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping must have one entry per token")
+    dev = _same_device(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping)
+    _launch("pkv_kv_append_fp8", dev, k.data_ptr(), ks, v.data_ptr(), vs, k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(),
+            T, Hkv, D, B, NB, _DTYPE_CODE[dtype])
+
+
+def block_read_fp8(k_out, v_out, k_cache, v_cache, k_scales, v_scales, src_dst_pairs):
+    """Read blocks of a cache held in 8 bits back into 16 bits: block ``src`` of
+    the caches into block ``dst`` of ``k_out`` and ``v_out`` (float16 or
+    bfloat16 [blocks, Hkv, B, D]) for each pair of ``src_dst_pairs`` (int64
+    [P, 2] CUDA tensor; destinations distinct).  :func:`paged_attn_prefill`
+    attends over them through a table of the destinations."""
+    _cuda(k_out, "k_out", ndim=4)
+    dtype = k_out.dtype
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("k_out must be float16 or bfloat16")
+    _cuda(v_out, "v_out", dtype, 4)
+    NB, Hkv, B, D = _fp8_cache(k_cache, v_cache, k_scales, v_scales)
+    _cuda(src_dst_pairs, "src_dst_pairs", torch.int64, 2)
+    if v_out.shape != k_out.shape or k_out.shape[1:] != (Hkv, B, D):
+        raise ValueError("shape mismatch between the outputs and the caches")
+    if src_dst_pairs.shape[1] != 2:
+        raise ValueError("src_dst_pairs must be [P, 2]")
+    dev = _same_device(k_out, v_out, k_cache, v_cache, k_scales, v_scales, src_dst_pairs)
+    _launch("pkv_block_read_fp8", dev, k_out.data_ptr(), v_out.data_ptr(), k_out.shape[0],
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], Hkv, D, B, NB, _DTYPE_CODE[dtype])
+
+
+def qk_norm_rope(q_out, k_out, q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                 pair_axes=None, interleaved=False, attn_factor=1.0):
+    """Norms and rotary positions of the heads of ``q`` ([T, Hq, D]) and ``k``
+    ([T, Hkv, D]) into ``q_out`` and ``k_out`` (each may be its input; all may
+    be slices of wider token rows).  Where ``q_weight`` / ``k_weight`` ([D], of
+    q's type) is given, each head row is first divided by its root mean square
+    (``eps`` added to the mean of the squares) and multiplied by it.
+    ``positions``: int32 [T], or [axes, T] with ``pair_axes`` (rot_dim / 2
+    integers on the host) naming the axis whose position turns each pair, as
+    for the time, height and width of images; negative on the first axis =
+    padding, nothing is written.  ``inv_freq``, ``interleaved`` and
+    ``attn_factor`` as :func:`rope_kv_append`.  Returns ``(q_out, k_out)``."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE_CODE or q.dim() != 3:
+        raise ValueError("q must be float16 or bfloat16 with 3 dimensions")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must have 3 dimensions")
+    dtype, q_shape, k_shape = q.dtype, q.shape, k.shape
+    T, Hq, D = q_shape
+    Hkv = k_shape[1]
+    if k_shape[0] != T or k_shape[2] != D:
+        raise ValueError("shape mismatch between q and k")
+    strides = (_token_rows(q_out, "q_out", dtype, q_shape),
+               _token_rows(k_out, "k_out", dtype, k_shape),
+               _token_rows(q, "q", dtype, q_shape), _token_rows(k, "k", dtype, k_shape))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _cuda(w, name, dtype, 1)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must have one entry per dimension")
+    _cuda(positions, "positions", torch.int32)
+    _cuda(inv_freq, "inv_freq", torch.float64, 1)
+    pairs = inv_freq.shape[0]
+    if positions.dim() == 2:
+        axes = positions.shape[0]
+        if pair_axes is None:
+            raise ValueError("positions of several axes need pair_axes")
+    elif positions.dim() == 1:
+        axes = 1
+    else:
+        raise ValueError("positions must have 1 or 2 dimensions")
+    if positions.shape[-1] != T:
+        raise ValueError("positions must have one entry per token")
+    if pair_axes is not None:
+        if not isinstance(pair_axes, (bytes, list, tuple)):
+            pair_axes = [int(a) for a in pair_axes]
+        pair_axes = bytes(pair_axes)  # (ValueError below 0 and above 255)
+        if len(pair_axes) != pairs or (pairs and max(pair_axes) >= axes):
+            raise ValueError("pair_axes must name an axis of positions for each pair")
+    dev = _same_device(q, q_out, k, k_out, q_weight, k_weight, positions, inv_freq)
+    _launch("pkv_qk_norm_rope", dev, q_out.data_ptr(), strides[0], k_out.data_ptr(), strides[1],
+            q.data_ptr(), strides[2], k.data_ptr(), strides[3],
+            None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), float(eps), positions.data_ptr(),
+            T, axes, pair_axes, inv_freq.data_ptr(), 2 * pairs, 1 if interleaved else 0,
+            float(attn_factor), T, Hq, Hkv, D, _DTYPE_CODE[dtype])
+    return q_out, k_out
+
+
+def decode_fp8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                              partition_size=0):
+    """Bytes of scratch :func:`paged_attn_decode_fp8` needs (0 when it does not split)."""
+    return tree_fp8_workspace_size(num_seqs, 1, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                   max_context_len, partition_size)
+
+
+def tree_fp8_workspace_size(total_queries, max_query_len, num_seqs, num_q_heads, num_kv_heads,
+                            head_dim, max_context_len, partition_size=0):
+    """Bytes of scratch :func:`paged_attn_tree_fp8` needs (0 when it does not split)."""
+    n = _lib.load().pkv_tree_fp8_workspace_size(
+        _c_int(total_queries, "total_queries"), _c_int(max_query_len, "max_query_len"), num_seqs,
+        num_q_heads, num_kv_heads, head_dim, _c_int(max_context_len, "max_context_len"),
+        _c_int(partition_size, "partition_size"))
+    if n == _SIZE_T_MAX:
+        raise ValueError("invalid or unsupported sizes")
+    return n
+
+
+def _fp8_attn(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+              max_context_len, max_query_len, partition_size, workspace, *more):
+    """Checks and workspace that the two attention calls over an 8-bit cache
+    share: the common device, the sizes, and the workspace's address and bytes."""
+    _cuda(q, "q", ndim=3)
+    if q.dtype not in _DTYPE_CODE:
+        raise ValueError("q must be float16 or bfloat16")
+    _cuda(out, "out", q.dtype, 3)
+    NB, Hkv, B, D = _fp8_cache(k_cache, v_cache, k_scales, v_scales)
+    _cuda(block_tables, "block_tables", torch.int32, 2)
+    _cuda(context_lens, "context_lens", torch.int32, 1)
+    T, Hq, D2 = q.shape
+    S = context_lens.shape[0]
+    if D2 != D or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, out and the caches")
+    if block_tables.shape[0] != S:
+        raise ValueError("block_tables / context_lens must have one row per sequence")
+    dev = _same_device(q, out, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                       workspace, *more)
+    if workspace is None:
+        sizes = (T, max_query_len, S, Hq, Hkv, D, max_context_len, partition_size)
+        if dev == torch._C._cuda_getDevice():
+            size = tree_fp8_workspace_size(*sizes)
+        else:
+            with torch.cuda.device(dev):
+                size = tree_fp8_workspace_size(*sizes)
+        if size:
+            workspace = q.new_empty(size >> 1)
+    else:
+        _cuda(workspace, "workspace")
+    ws = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size())
+    return dev, (S, Hq, Hkv, D, B, NB), ws, workspace
+
+
+def paged_attn_decode_fp8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                          context_lens, scale, max_context_len, partition_size=0, workspace=None):
+    """:func:`paged_attn_decode` over a cache held in 8 bits
+    (:func:`kv_append_fp8`).  ``partition_size``: 0 or a multiple of 128;
+    ``workspace`` (any CUDA tensor of at least :func:`decode_fp8_workspace_size`
+    bytes) is allocated here with torch if omitted and needed.  Writes ``out``
+    ([S, Hq, D]) and returns it."""
+    dev, (S, Hq, Hkv, D, B, NB), ws, workspace = _fp8_attn(
+        out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+        max_context_len, 1, partition_size, workspace)
+    if q.shape[0] != S:
+        raise ValueError("q must have one row per sequence")
+    _launch("pkv_paged_attn_decode_fp8", dev, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(),
+            _c_int(max_context_len, "max_context_len"), S, Hq, Hkv, D, B, NB, float(scale),
+            _DTYPE_CODE[q.dtype], _c_int(partition_size, "partition_size"), *ws)
+    return out
+
+
+def paged_attn_tree_fp8(out, q, query_start, tree_masks, k_cache, v_cache, k_scales, v_scales,
+                        block_tables, context_lens, scale, max_context_len, max_query_len,
+                        partition_size=0, workspace=None):
+    """Attention of drafted tokens over a cache held in 8 bits, to check several
+    guesses of each sequence's next tokens in one pass.  Sequence s's queries
+    ``q[query_start[s]:query_start[s+1]]`` (at most 64) are the last positions
+    of its context, already appended.  Query j sees all positions before them
+    and, of the drafted ones, the i-th where bit i of its entry of
+    ``tree_masks`` (int64 [total_queries]) is set: its ancestors in the tree
+    and itself.  A query that sees nothing gets zeros.  Accepted rows that do
+    not follow one another are appended again at their places
+    (:func:`kv_append_fp8` gives the same bits there).  ``partition_size``,
+    ``workspace`` (:func:`tree_fp8_workspace_size`) as
+    :func:`paged_attn_decode_fp8`.  Writes ``out`` ([total_queries, Hq, D];
+    rows behind the last sequence stay) and returns it."""
+    _cuda(query_start, "query_start", torch.int32, 1)
+    _cuda(tree_masks, "tree_masks", torch.int64, 1)
+    dev, (S, Hq, Hkv, D, B, NB), ws, workspace = _fp8_attn(
+        out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+        max_context_len, max_query_len, partition_size, workspace, query_start, tree_masks)
+    T = q.shape[0]
+    if query_start.shape[0] != S + 1 or tree_masks.shape[0] != T:
+        raise ValueError("query_start / tree_masks must match context_lens / q")
+    _launch("pkv_paged_attn_tree_fp8", dev, out.data_ptr(), q.data_ptr(), T,
+            query_start.data_ptr(), _c_int(max_query_len, "max_query_len"), tree_masks.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+            _c_int(max_context_len, "max_context_len"), S, Hq, Hkv, D, B, NB, float(scale),
+            _DTYPE_CODE[q.dtype], _c_int(partition_size, "partition_size"), *ws)
+    return out
+
+
 def check_copy_pairs(pairs, num_blocks):
     """Raise ValueError unless ``pairs`` ([P, 2] ids, host data) is a valid
     block_copy batch: ids in [0, num_blocks), destinations distinct, and no
