@@ -1105,10 +1105,20 @@ pkv_status_t attn_fp8_impl(void* out, const void* q, int total_queries, const in
   p.block_size = block_size;
   p.num_blocks = num_blocks;
   p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax is evaluated with exp2
+  p.chunks = plan.chunks;
+  p.partition_size = plan.partition;
+  p.num_parts = (int)plan.parts;
+  if (plan.parts > 1) {
+    const size_t rows = (size_t)total_queries * num_q_heads * plan.parts;
+    p.ws_o = static_cast<float*>(workspace);
+    p.ws_m = p.ws_o + rows * head_dim;
+    p.ws_l = p.ws_m + rows;
+  }
   cudaError_t err = status_word(&p.status);
   if (err != cudaSuccess) return cuda_fail(err);
   bool unsupported = false;
-  err = pkv::launch_attn_fp8(p, head_dim, dtype, device_sms(),
+  const long long items = plan.parts * plan.chunks * num_kv_heads * num_seqs;
+  err = pkv::launch_attn_fp8(p, head_dim, dtype, tc_ctas(items),
                              reinterpret_cast<cudaStream_t>(stream), &unsupported);
   if (unsupported) return PKV_ERR_UNSUPPORTED;
   return err != cudaSuccess ? cuda_fail(err) : PKV_OK;

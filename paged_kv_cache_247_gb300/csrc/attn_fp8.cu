@@ -1,136 +1,957 @@
 // Attention over a paged cache held in 8 bits (the format: fp8.cuh): one query
 // per sequence, or the queries of a tree of drafted tokens ("Only 20.4% of your
 // KV cache held actual tokens", section "The page table, relocated into
-// attention"; "Why the KV cache is the thing that limits your batch": a decode
-// step's time is the bytes of the cache).
+// attention"; section "Why the KV cache is the thing that limits your batch": a
+// decode step's time is the bytes of the cache, here half of the 16-bit ones).
 //
-// One CTA per (query row, query head).  Each thread takes one key of a tile of
-// 128, the running maximum and sum are kept for the whole CTA, and then thread
-// d adds up dimension d of the tile's V rows.
+// The codes go from HBM through shared memory into the tensor core as they are
+// (tcgen05.mma kind::f8f6f4); nothing is widened on the way.  The operands on
+// the other side are split into e4m3 parts instead, which cost only columns of
+// an N that is far from full:
+//
+//   q row      = 2^e (c1 + c2 / 16 + c3 / 256), e4m3 parts of 4 bits each: two
+//                hold a bf16 row exactly (8 bits), three an fp16 row (11), down
+//                to 2^-18 of the row's largest element;
+//   S^T        [128 keys x parts * rows] = K codes . parts^T
+//   x          = scale log2(e) 2^e k_scale (s1 + s2 / 16 + s3 / 256)
+//   y          = x + log2 v_scale: the V row's scale is an addend of the base-2
+//                logit, and the running reference m is one of y, which is what
+//                gets rounded: p = 2^(y - m), at most 2^8, split into three
+//                parts (12 bits; what lies 2^-26 below the largest is lost)
+//   O^T        [D x parts * rows] += V codes^T . parts
+//   l          += p / v_scale
+//   out        = (o1 + o2 / 16 + o3 / 256) / l
+//
+// m moves when some y exceeds it by more than 8, to 6 below that y, so that p
+// lies high in the range of e4m3.
+//
+// Orientation, pipeline and roles follow the 16-bit decode kernel: keys are the
+// first product's M, the D dimensions the second's (D = 64: an M of 64, whose
+// row i lies in tensor-memory lane 32 (i / 16) + i % 16).  A work item is
+// (sequence, KV head, partition of the context, up to 32 rows), a row being a
+// query head of the group and one of the sequence's queries.  One persistent CTA
+// per SM walks the items; its rings, barriers and tensor memory flow from item
+// to item.  Warps:
+//
+//   key warpgroups (one; two, each with half the rows, for more than 16 rows):
+//              thread t has key t of the tile: scales, logits, weights, and at
+//              the end dimension t of the output.  Its parts of the weights are
+//              neighbouring bytes (MN-major operand, no swizzle): one 16-byte
+//              store for every 16 of them.
+//   K, V producers   one TMA copy per (block, head) run into a ring of tiles
+//   scale producer   the tile's K and V scales by asynchronous copies
+//   Q warps          rows split into their parts, one item ahead
+//   S, O issuers     four (D = 64: two, four) MMAs per tile
 
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
 #include "overlap.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kKeys = 128;
+using namespace tc;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kKeys) attn_fp8_simple_kernel(const AttnFp8Params p) {
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  __shared__ float q_row[D], weight[kKeys], red[2][4];
-  __shared__ long long v_row[kKeys];
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int row = blockIdx.x, h = blockIdx.y, kvh = h / p.group;
+constexpr int kKeys = kTileKeys;  // keys per tile
+constexpr int kParts = 3;         // e4m3 parts of a softmax weight
+constexpr int kScaleStages = 8;
+constexpr int kQWarps = 2;
+constexpr float kRaise = 6.f;     // a moved reference lies this far below the tile's maximum
+constexpr float kExceed = 8.f;    // weights reach 2^8 (e4m3 holds 448) before it moves
+constexpr int kMinVExponent = -60;  // V rows below 448 * 2^-60 count as zero
 
-  // The sequence whose queries hold this row.
-  int s = row, j = 0, count = 1;
-  if (p.query_start) {
-    s = -1;
-    for (int i = 0; i < p.num_seqs; ++i)
-      if (p.query_start[i] <= row && row < p.query_start[i + 1]) s = i;
-    if (s < 0) return;
-    j = row - p.query_start[s];
-    count = p.query_start[s + 1] - p.query_start[s];
-    if (count > p.max_query_len) {
-      if (t == 0) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
-      count = p.max_query_len;
-      if (j >= count) return;
-    }
-  }
-  const long long cap =
-      min((long long)p.max_context_len, (long long)p.max_blocks_per_seq * p.block_size);
-  int ctx = p.context_lens[s];
-  if (ctx < 0 || ctx > cap || (p.query_start && count > ctx)) {
-    if (t == 0) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
-    ctx = ctx < 0 ? 0 : (ctx > cap ? (int)cap : ctx);
-  }
-  const int base = p.query_start ? max(ctx - count, 0) : ctx;
-  const unsigned long long mask = p.query_start ? (unsigned long long)p.tree_masks[row] : 0;
+constexpr int up16(int x) { return (x + 15) / 16 * 16; }
+constexpr int pow2_at_least(int x, int p = 32) { return p >= x ? p : pow2_at_least(x, 2 * p); }
 
-  const T* q = static_cast<const T*>(p.q) + ((long long)row * p.num_q_heads + h) * D;
-  if (t < D) q_row[t] = static_cast<float>(q[t]) * p.qscale;
-  __syncthreads();
-  float m = -CUDART_INF_F, l = 0.f, o = 0.f;
-  for (int k0 = 0; k0 < ctx; k0 += kKeys) {
-    const int pos = k0 + t;
-    const bool seen = pos < ctx && (pos < base || (mask >> (pos - base)) & 1);
-    float x = -CUDART_INF_F, vs = 0.f;
-    v_row[t] = -1;
-    if (seen) {
-      int blk = p.block_tables[(long long)s * p.max_blocks_per_seq + pos / p.block_size];
-      if ((unsigned)blk >= (unsigned)p.num_blocks) {
-        atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
-        blk = 0;
-      }
-      const long long r =
-          ((long long)blk * p.num_kv_heads + kvh) * p.block_size + pos % p.block_size;
-      const uint4* codes = reinterpret_cast<const uint4*>(p.k_cache) + r * (D / 16);
-      float dot = 0.f;
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 w = codes[c];
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 v = decode2(u[i / 2] >> (16 * (i % 2)));
-          dot += v.x * q_row[16 * c + 2 * i] + v.y * q_row[16 * c + 2 * i + 1];
-        }
-      }
-      x = dot * scale_value(p.k_scales[r]);
-      vs = scale_value(p.v_scales[r]);
-      v_row[t] = r;
-    }
-    float mx = x;
-#pragma unroll
-    for (int mk = 16; mk >= 1; mk >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, mk));
-    if (lane == 0) red[0][warp] = mx;
-    __syncthreads();
-    const float mn =
-        fmaxf(m, fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3])));
-    const float alpha = m == mn ? 1.f : exp2f(m - mn);
-    const float e = seen ? exp2f(x - mn) : 0.f;
-    weight[t] = e * vs;
-    float sum = e;
-#pragma unroll
-    for (int mk = 16; mk >= 1; mk >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mk);
-    if (lane == 0) red[1][warp] = sum;
-    __syncthreads();
-    l = l * alpha + (red[1][0] + red[1][1] + red[1][2] + red[1][3]);
-    o *= alpha;
-    m = mn;
-    if (t < D)
-      for (int i = 0; i < kKeys; ++i)
-        if (v_row[i] >= 0)
-          o += weight[i] *
-               decode2(reinterpret_cast<const uint8_t*>(p.v_cache)[v_row[i] * D + t]).x;
-    __syncthreads();
-  }
-  if (t < D)
-    static_cast<T*>(p.out)[((long long)row * p.num_q_heads + h) * D + t] =
-        static_cast<T>(l == 0.f ? 0.f : o / l);
+template <typename T, int NH, int D>
+struct Shape {
+  static constexpr int kQParts = std::is_same<T, __half>::value ? 3 : 2;
+  static constexpr int NS = up16(kQParts * NH);  // columns of S^T
+  static constexpr int NO = up16(kParts * NH);   // columns of O^T
+  static constexpr int KG = NH > 16 ? 2 : 1;     // key warpgroups
+  static constexpr int NHW = NH / KG;            // rows per key warpgroup
+  static constexpr int kKeyThreads = 128 * KG;
+  static constexpr int kKWarp = 4 * KG;
+  static constexpr int kVWarp = kKWarp + 1;
+  static constexpr int kSWarp = kKWarp + 2;  // owns tensor memory
+  static constexpr int kOWarp = kKWarp + 3;
+  static constexpr int kScaleWarp = kKWarp + 4;
+  static constexpr int kQWarp = kKWarp + 5;
+  static constexpr int kThreads = kKeyThreads + (5 + kQWarps) * 32;
+  static constexpr int kTile = kKeys * D;     // bytes of a K or V tile
+  static constexpr int kQBytes = NS * D;
+  static constexpr int kPBuf = kKeys * NO;
+  static constexpr int SB = 3;                // S^T and P buffers
+  // scales, factors, masks, rows, reductions, barriers; alignment
+  static constexpr int kSmall = kScaleStages * kKeys * 4 + 2 * NH * 16 + KG * 4 * NHW * 4 + 1024;
+  static constexpr int kFixed = 2 * kQBytes + SB * kPBuf + kSmall + 1024;
+  static constexpr int kFit = (227 * 1024 - kFixed) / (2 * kTile);
+  static constexpr int kStages = kFit < 12 ? kFit : 12;
+  static constexpr int kQ = 2 * kStages * kTile;  // after the K and V rings
+  static constexpr int kP = kQ + 2 * kQBytes;
+  static constexpr int kScales = kP + SB * kPBuf;               // [stages][K, V][128] bfloat16
+  static constexpr int kMasks = kScales + kScaleStages * kKeys * 4;  // [2][NH] 64-bit
+  static constexpr int kFactors = kMasks + 2 * NH * 8;          // [2][NH] floats
+  static constexpr int kRows = kFactors + 2 * NH * 4;           // [2][NH] output rows
+  static constexpr int kRed = kRows + 2 * NH * 4;               // [KG][4 warps][NHW] floats
+  static constexpr int kBar = kRed + KG * 4 * NHW * 4;
+  static constexpr int kBars = 4 * kStages + 4 * SB + 2 * kScaleStages + 8;
+  static constexpr int kTmemSlot = kBar + kBars * 8;
+  static constexpr int kBytes = kTmemSlot + 16 + 1024;
+  static_assert(kBars * 8 + 16 <= 1024 && kBytes <= 227 * 1024, "shared memory overflow");
+  static constexpr int kColO = SB * NS;
+  static constexpr int kTmemCols = pow2_at_least(SB * NS + 2 * NO);
+  static_assert(kTmemCols <= 512, "tensor memory overflow");
+  static constexpr int kSwizzle = D == 128 ? 2 : 4;  // descriptor code of the D-byte swizzle
+};
+
+// Shared-memory matrix descriptor (version 1) with the given swizzle code.
+__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo, uint32_t sbo, int swizzle) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)swizzle << 61);
 }
 
-template <typename T>
-cudaError_t launch_typed(const AttnFp8Params& p, int head_dim, cudaStream_t stream) {
-  const dim3 grid(p.total_queries, p.num_q_heads);
-  return head_dim == 64
-             ? launch_overlapped(attn_fp8_simple_kernel<T, 64>, grid, dim3(kKeys), 0, stream, p)
-             : launch_overlapped(attn_fp8_simple_kernel<T, 128>, grid, dim3(kKeys), 0, stream, p);
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, both operands e4m3.
+__device__ __forceinline__ uint32_t instr(bool mn_major, int n, int m) {
+  return (1u << 4) | (mn_major ? 3u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
+
+// Warp-collective, as the helpers of tcgen05.cuh.
+__device__ __forceinline__ void mma_f8_warp(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// Offset of byte x of row r in rows of D bytes with the D-byte swizzle.
+template <int D>
+__device__ __forceinline__ int swizzled(int r, int x) {
+  const int off = r * D + x;
+  return off ^ (((off >> 7) & (D / 16 - 1)) << 4);
+}
+
+// C consecutive columns of this thread's lane, not waited for.
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+  static_assert(C == 4 || C == 8 || C == 16, "4, 8 or 16 columns");
+  if constexpr (C == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(taddr));
+  } else if constexpr (C == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr));
+  } else {
+    tmem_ld16f(taddr, v);
+  }
+}
+
+// Wait for the loads above; no use of the values is scheduled before it.
+template <int N>
+__device__ __forceinline__ void tmem_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// v[g] = the sum over PARTS parts, part c in columns c * NH ..., weighted 16^-c.
+template <int PARTS, int NH, int NHW>
+__device__ __forceinline__ void load_parts(uint32_t taddr, float* v) {
+  float part[PARTS * NHW];
+#pragma unroll
+  for (int c = 0; c < PARTS; ++c) tmem_ld<NHW>(taddr + c * NH, part + c * NHW);
+  tmem_wait<PARTS * NHW>(part);
+#pragma unroll
+  for (int g = 0; g < NHW; ++g) {
+    v[g] = part[(PARTS - 1) * NHW + g];
+#pragma unroll
+    for (int c = PARTS - 2; c >= 0; --c) v[g] = fmaf(v[g], 0.0625f, part[c * NHW + g]);
+  }
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+  return r;
+}
+
+// 16 (h - code): what the next part holds.
+__device__ __forceinline__ uint32_t remainder16(uint32_t h2, uint32_t codes) {
+  const uint32_t back = half2_of(codes);
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h2),
+                            *reinterpret_cast<const __half2*>(&back));
+  const __half2 r = __hmul2(d, __float2half2_rn(16.f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// One work item: up to NH rows of sequence s and one KV head over the partition
+// [t_begin, t_end) of the context (no tiles: nothing to do).
+struct Item {
+  int s, kvh, part, row_first, rows;  // rows [row_first, + rows) of the sequence's
+  int query0, queries;                // its first row of q, and how many
+  int ctx, base, t_begin, t_end, n_tiles, nparts_seq;
+};
+
+// Sequence s's queries (first row, count); counts that do not fit are cut.
+__device__ __forceinline__ void item_queries(const AttnFp8Params& p, int s, int ctx, Item* it,
+                                             bool* bad) {
+  if (p.query_start == nullptr) {
+    it->query0 = s;
+    it->queries = 1;
+    it->base = ctx;
+    return;
+  }
+  const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
+  const bool there = q0 >= 0 && q1 >= q0 && q1 <= p.total_queries;
+  const int n = there ? min(q1 - q0, p.max_query_len) : 0;
+  *bad = !there || n < q1 - q0 || n > ctx;
+  it->query0 = there ? q0 : 0;
+  it->queries = n;
+  it->base = max(ctx - n, 0);
+}
+
+template <int NH>
+__device__ __forceinline__ Item item_at(const AttnFp8Params& p, int j, bool report = false) {
+  Item it;
+  const int chunk = j % p.chunks;
+  int r = j / p.chunks;
+  it.part = r % p.num_parts;
+  r /= p.num_parts;
+  it.kvh = r % p.num_kv_heads;
+  it.s = r / p.num_kv_heads;
+  const int raw = __ldg(p.context_lens + it.s);
+  const long long cap = min((long long)p.max_context_len,
+                            (long long)p.max_blocks_per_seq * p.block_size);
+  it.ctx = raw < 0 ? 0 : (raw > cap ? (int)cap : raw);
+  bool bad = false;
+  item_queries(p, it.s, it.ctx, &it, &bad);
+  if (report && (bad || raw != it.ctx) && it.part == 0 && chunk == 0)
+    atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+  it.row_first = chunk * NH;
+  it.rows = min(NH, it.queries * p.group - it.row_first);
+  it.t_begin = it.part * p.partition_size;
+  it.t_end = partition_end(it.ctx, it.t_begin, p.partition_size);
+  it.n_tiles = it.rows > 0 && it.t_begin < it.t_end ? (it.t_end - it.t_begin + kKeys - 1) / kKeys
+                                                    : 0;
+  it.nparts_seq = context_partitions(it.ctx, p.partition_size);
+  return it;
+}
+
+// Output row (query row * Hq + head) of the item's row r.
+__device__ __forceinline__ int output_row(const AttnFp8Params& p, const Item& it, int r) {
+  const int row = it.row_first + r, j = row / p.group;
+  return (it.query0 + j) * p.num_q_heads + it.kvh * p.group + (row - j * p.group);
+}
+
+// True if any of the 128 threads of key warpgroup kg passes true.
+__device__ __forceinline__ bool group_any(int kg, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %2, 0;\n\t"
+      "bar.red.or.pred po, %1, 128, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"(1 + kg), "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void tma_load_run(void* dst, const CUtensorMap* map, int row,
+                                             uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Eight bytes, or zeros where `bytes` is 0.
+__device__ __forceinline__ void copy8_async(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+
+template <typename T, int NH, int D>
+__global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
+    attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap, int num_items) {
+  using L = Shape<T, NH, D>;
+  constexpr int S = L::kStages, SB = L::SB, SC = kScaleStages, NHW = L::NHW;
+  grid_dep_wait();
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* sK = smem;
+  unsigned char* sV = smem + S * L::kTile;
+  unsigned char* sQ = smem + L::kQ;
+  unsigned char* sP = smem + L::kP;
+  uint16_t* sScales = reinterpret_cast<uint16_t*>(smem + L::kScales);
+  unsigned long long* sMasks = reinterpret_cast<unsigned long long*>(smem + L::kMasks);
+  float* sFactors = reinterpret_cast<float*>(smem + L::kFactors);
+  int* sRows = reinterpret_cast<int*>(smem + L::kRows);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kBar);  // [S] tile landed
+  uint64_t* k_empty = k_full + S;   // [S] its MMAs are done (commit)
+  uint64_t* v_full = k_empty + S;   // [S]
+  uint64_t* v_empty = v_full + S;   // [S]
+  uint64_t* s_full = v_empty + S;   // [SB] S^T computed (commit)
+  uint64_t* s_free = s_full + SB;   // [SB] read by the key warpgroups
+  uint64_t* p_full = s_free + SB;   // [SB] weights written
+  uint64_t* p_free = p_full + SB;   // [SB] their MMAs are done (commit)
+  uint64_t* c_full = p_free + SB;   // [SC] the tile's scales landed
+  uint64_t* c_free = c_full + SC;   // [SC] read by the key warpgroups
+  uint64_t* q_full = c_free + SC;   // [2] an item's rows, factors and masks written
+  uint64_t* q_free = q_full + 2;    // [2] the item done
+  uint64_t* o_free = q_free + 2;    // [2] O^T buffer read
+  uint64_t* drain = o_free + 2;     // [2] each issuer's last MMAs finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int b = 0; b < SB; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], L::kKeyThreads);
+      mbar_init(&p_full[b], L::kKeyThreads);
+      mbar_init(&p_free[b], 1);
+    }
+    for (int b = 0; b < SC; ++b) {
+      mbar_init(&c_full[b], 32);
+      mbar_init(&c_free[b], L::kKeyThreads);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&q_full[b], 32 * kQWarps);
+      mbar_init(&q_free[b], L::kKeyThreads);
+      mbar_init(&o_free[b], L::kKeyThreads);
+      mbar_init(&drain[b], 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == L::kSWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(L::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == L::kKWarp || warp == L::kVWarp) {
+    // ----------------------------------------------------------- producers
+    // Tile i covers keys [t_begin + 128 i, + 128): runs of B rows, one block
+    // each, lane l copies run l.  Block ids are read a tile ahead.
+    const bool is_k = warp == L::kKWarp;
+    const CUtensorMap* map = is_k ? &kmap : &vmap;
+    unsigned char* ring = is_k ? sK : sV;
+    uint64_t* full = is_k ? k_full : v_full;
+    uint64_t* empty = is_k ? k_empty : v_empty;
+    const int B = p.block_size;
+    prefetch_tensormap(map);
+    int kt = 0;
+    bool ok = true;
+    for (int j = blockIdx.x; ok && j < num_items; j += gridDim.x) {
+      const Item it = item_at<NH>(p, j);
+      if (it.n_tiles == 0) continue;
+      const int32_t* trow = p.block_tables + (size_t)it.s * p.max_blocks_per_seq;
+      auto table_entry = [&](int i) -> int {
+        const int key = it.t_begin + i * kKeys + lane * B;
+        return (lane * B < kKeys && i < it.n_tiles && key < it.t_end) ? __ldg(trow + key / B) : 0;
+      };
+      int next = table_entry(0);
+      for (int i = 0; i < it.n_tiles; ++i, ++kt) {
+        const int st = kt % S;
+        const int nvalid = min(kKeys, it.t_end - (it.t_begin + i * kKeys));
+        const int nseg = (nvalid + B - 1) / B;
+        int phys = next;
+        next = table_entry(i + 1);
+        if ((unsigned)phys >= (unsigned)p.num_blocks) {
+          if (lane < nseg) atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
+          phys = 0;
+        }
+        if (kt >= S && !mbar_wait_warp(&empty[st], ((kt / S) - 1) & 1, p.status)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)nseg * B * D);
+        __syncwarp();
+        if (lane < nseg)
+          tma_load_run(ring + st * L::kTile + lane * B * D, map,
+                       (phys * p.num_kv_heads + it.kvh) * B, &full[st]);
+      }
+    }
+    // After a timeout, copies still in flight land before the CTA leaves.
+    if (timed_out(p.status))
+      for (int i = kt > S ? kt - S : 0; i < kt; ++i) mbar_drain(&full[i % S], (i / S) & 1);
+    __syncwarp();
+  } else if (warp == L::kScaleWarp) {
+    // ------------------------------------------------------ scale producer
+    // Lane l copies the scales of keys 4 l .. 4 l + 3 (one block: B >= 8).
+    const int B = p.block_size;
+    int kt = 0;
+    bool ok = true;
+    for (int j = blockIdx.x; ok && j < num_items; j += gridDim.x) {
+      const Item it = item_at<NH>(p, j);
+      if (it.n_tiles == 0) continue;
+      const int32_t* trow = p.block_tables + (size_t)it.s * p.max_blocks_per_seq;
+      auto table_entry = [&](int i) -> int {
+        const int key = it.t_begin + i * kKeys + lane * 4;
+        return i < it.n_tiles && key < it.t_end ? __ldg(trow + key / B) : 0;
+      };
+      int next = table_entry(0);
+      for (int i = 0; i < it.n_tiles; ++i, ++kt) {
+        const int key = it.t_begin + i * kKeys + lane * 4;
+        int phys = next;
+        next = table_entry(i + 1);
+        if ((unsigned)phys >= (unsigned)p.num_blocks) phys = 0;  // (flagged by the others)
+        const int st = kt % SC;
+        if (kt >= SC && !mbar_wait_warp(&c_free[st], ((kt / SC) - 1) & 1, p.status)) {
+          ok = false;
+          break;
+        }
+        const size_t row = ((size_t)phys * p.num_kv_heads + it.kvh) * B + key % B;
+        const int bytes = key < it.t_end ? 8 : 0;
+        copy8_async(sScales + (2 * st) * kKeys + lane * 4, p.k_scales + (bytes ? row : 0), bytes);
+        copy8_async(sScales + (2 * st + 1) * kKeys + lane * 4, p.v_scales + (bytes ? row : 0),
+                    bytes);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_addr(&c_full[st]))
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  } else if (warp >= L::kQWarp) {
+    // -------------------------------------------------------------- Q warps
+    // Warp w of kQWarps splits rows w, w + kQWarps, ...: lane l holds elements
+    // D / 32 * l ...  Rows past the item's are zeros.
+    constexpr int E = D / 32;
+    const int w = warp - L::kQWarp;
+    int k_item = 0;
+    for (int j = blockIdx.x; j < num_items; j += gridDim.x) {
+      const Item it = item_at<NH>(p, j);
+      if (it.n_tiles == 0) continue;
+      const int b = k_item & 1;
+      if (k_item >= 2 && !mbar_wait_warp(&q_free[b], ((k_item - 2) >> 1) & 1, p.status)) break;
+      unsigned char* dst = sQ + b * L::kQBytes;
+#pragma unroll 4
+      for (int r = w; r < NH; r += kQWarps) {
+        const bool there = r < it.rows;
+        const int out_row = there ? output_row(p, it, r) : 0;
+        uint32_t raw[E / 2] = {};
+        if (there) {
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(
+              static_cast<const T*>(p.q) + (size_t)out_row * D + lane * E);
+          if constexpr (E == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+            raw[0] = v.x;
+            raw[1] = v.y;
+          } else {
+            raw[0] = __ldg(src);
+          }
+        }
+        uint32_t top = raw[0] & 0x7fff7fffu;
+        if constexpr (E == 4) top = __vmaxu2(top, raw[1] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool finite = top < Magnitude<T>::kInf;
+        const int e = row_exponent(finite ? Magnitude<T>::value(top) : 0.f);
+        const float inv = finite ? pow2(-e) : 0.f;
+        float y[E];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          const float2 f = Cvt<T>::to_float2(raw[i]);
+          y[2 * i] = finite ? f.x * inv : 0.f;
+          y[2 * i + 1] = finite ? f.y * inv : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < L::kQParts; ++c) {
+          uint32_t codes = 0;
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]),
+                                                          __NV_SATFINITE, __NV_E4M3);
+            codes |= two << (16 * i);
+            const float2 back = decode2(two);
+            y[2 * i] = (y[2 * i] - back.x) * 16.f;
+            y[2 * i + 1] = (y[2 * i + 1] - back.y) * 16.f;
+          }
+          unsigned char* to = dst + swizzled<D>(c * NH + r, lane * E);
+          if constexpr (E == 4)
+            *reinterpret_cast<uint32_t*>(to) = codes;
+          else
+            *reinterpret_cast<uint16_t*>(to) = (uint16_t)codes;
+        }
+        if (lane == 0) {
+          sFactors[b * NH + r] = finite ? p.qscale * pow2(e) : CUDART_NAN_F;
+          sRows[b * NH + r] = out_row;
+          if (p.tree_masks)
+            sMasks[b * NH + r] =
+                there ? (unsigned long long)__ldg(
+                            reinterpret_cast<const long long*>(p.tree_masks) +
+                            out_row / p.num_q_heads)
+                      : 0;
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&q_full[b]);
+      ++k_item;
+    }
+    __syncwarp();
+  } else if (warp == L::kSWarp || warp == L::kOWarp) {
+    // ------------------------------------------------------------ issuers
+    const bool is_s = warp == L::kSWarp;
+    const uint32_t idesc = is_s ? instr(false, L::NS, kKeys) : instr(true, L::NO, D);
+    const uint32_t aK = smem_addr(sK), aV = smem_addr(sV), aQ = smem_addr(sQ),
+                   aP = smem_addr(sP);
+    int kt = 0, k_item = 0;
+    bool ok = true;
+    for (int j = blockIdx.x; ok && j < num_items; j += gridDim.x) {
+      const Item it = item_at<NH>(p, j);
+      if (it.n_tiles == 0) continue;
+      const int b = k_item & 1;
+      if (is_s) {
+        if (!mbar_wait_warp(&q_full[b], (k_item >> 1) & 1, p.status)) break;
+        for (int i = 0; i < it.n_tiles; ++i, ++kt) {
+          const int st = kt % S;
+          if (!mbar_wait_warp(&k_full[st], (kt / S) & 1, p.status) ||
+              (kt >= SB && !mbar_wait_warp(&s_free[kt % SB], ((kt / SB) - 1) & 1, p.status))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // 32 dimensions per MMA: a 32-byte step inside the swizzled rows.
+#pragma unroll
+          for (int ks = 0; ks < D / 32; ++ks)
+            mma_f8_warp(tmem + (kt % SB) * L::NS,
+                        desc(aK + st * L::kTile + ks * 32, 16, 8 * D, L::kSwizzle),
+                        desc(aQ + b * L::kQBytes + ks * 32, 16, 8 * D, L::kSwizzle), idesc,
+                        ks > 0 ? 1u : 0u);
+          mma_commit_warp(&s_full[kt % SB]);
+          mma_commit_warp(&k_empty[st]);
+        }
+      } else {
+        if (k_item >= 2 && !mbar_wait_warp(&o_free[b], ((k_item - 2) >> 1) & 1, p.status)) break;
+        for (int i = 0; i < it.n_tiles; ++i, ++kt) {
+          const int st = kt % S;
+          if (!mbar_wait_warp(&v_full[st], (kt / S) & 1, p.status) ||
+              !mbar_wait_warp(&p_full[kt % SB], (kt / SB) & 1, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // 32 keys per MMA, four groups of 8.  V: the D columns are one
+          // swizzled atom, groups 8 D bytes apart.  P: 16-byte columns 128
+          // bytes apart, groups 8 NO bytes apart.
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 32; ++ks)
+            mma_f8_warp(tmem + L::kColO + b * L::NO,
+                        desc(aV + st * L::kTile + ks * 32 * D, 16, 8 * D, L::kSwizzle),
+                        desc(aP + (kt % SB) * L::kPBuf + ks * 32 * L::NO, 8 * L::NO, 128, 0),
+                        idesc, (i > 0 || ks > 0) ? 1u : 0u);
+          mma_commit_warp(&p_free[kt % SB]);
+          mma_commit_warp(&v_empty[st]);
+        }
+      }
+      ++k_item;
+    }
+    uint64_t* d = &drain[is_s ? 0 : 1];
+    mma_commit_warp(d);
+    mbar_drain(d, 0);
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------- key warpgroups
+    const int kg = warp >> 2;
+    const int t = threadIdx.x & 127;  // key of the tile == tensor-memory lane
+    const int hb = kg * NHW;          // first row of this warpgroup
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    // the dimension whose outputs this lane holds (D = 64: half of the lanes)
+    const int d = D == 128 ? t : (warp & 3) * 16 + lane;
+    const bool has_d = D == 128 || lane < 16;
+    float* red = reinterpret_cast<float*>(smem + L::kRed) + kg * 4 * NHW;
+    int kt = 0, k_item = 0;
+    bool ok = true;
+    for (int j = blockIdx.x; j < num_items; j += gridDim.x) {
+      const Item it = item_at<NH>(p, j, kg == 0 && t == 0);
+      if (it.n_tiles == 0) {
+        if (it.ctx == 0 && it.part == 0 && has_d)  // nothing to see: zeros
+          for (int g = hb; g < min(hb + NHW, it.rows); ++g)
+            static_cast<T*>(p.out)[(size_t)output_row(p, it, g) * D + d] = static_cast<T>(0.f);
+        continue;
+      }
+      const int ob = k_item & 1;
+      if (ok && !mbar_wait_warp(&q_full[ob], (k_item >> 1) & 1, p.status)) ok = false;
+      const float* factors = sFactors + ob * NH + hb;
+      const uint32_t my_rows =
+          it.rows >= hb + NHW ? (1u << NHW) - 1u : (1u << max(it.rows - hb, 0)) - 1u;
+      // The references are the same in every thread of the warpgroup.
+      float mref[NHW], l_part[NHW];
+#pragma unroll
+      for (int g = 0; g < NHW; ++g) {
+        mref[g] = -CUDART_INF_F;
+        l_part[g] = 0.f;
+      }
+      for (int i = 0; i < it.n_tiles; ++i, ++kt) {
+        const int key0 = it.t_begin + i * kKeys;
+        const int nvalid = min(kKeys, it.t_end - key0);
+        const bool valid = t < nvalid;
+        // A wait that gives up (never expected) leaves ok false; the loop runs
+        // on without waiting, so that every named barrier stays matched, and
+        // nothing it computes is stored.
+        if (ok && !mbar_wait_warp(&c_full[kt % SC], (kt / SC) & 1, p.status)) ok = false;
+        const float ks = scale_value(sScales[2 * (kt % SC) * kKeys + t]);
+        const uint32_t vbits = sScales[(2 * (kt % SC) + 1) * kKeys + t];
+        mbar_arrive(&c_free[kt % SC]);
+        if (ok && !mbar_wait_warp(&s_full[kt % SB], (kt / SB) & 1, p.status)) ok = false;
+        tc_fence_after();
+        float y[NHW];
+        load_parts<L::kQParts, NH, NHW>(tmem + (kt % SB) * L::NS + hb + lane_base, y);
+        tc_fence_before();
+        mbar_arrive(&s_free[kt % SB]);
+
+        // What this key's V scale does: y = x + lv, l gets p * 2^-lv.
+        const int ev = (int)(vbits >> 7) - 127;
+        const bool tiny = ev < kMinVExponent;
+        int lv = max(ev, kMinVExponent);
+        float lvf = vbits > 0x7f80u ? CUDART_NAN_F : (float)lv;
+        const float inv_v = pow2(-min(lv, 126));
+        uint32_t seen = valid ? my_rows : 0u;
+        const bool tail = p.tree_masks != nullptr && key0 + nvalid > it.base;
+        const int st = kt % S;
+        if (tail) {
+          // Drafted positions: a row sees those of its mask.  What is masked
+          // must not reach the second product, whose zero weights do not hide
+          // a NaN code: such a row of V counts as NaN by its scale, and its
+          // codes are cleared below.
+          const int rel = key0 + t - it.base;
+          if (valid && rel >= 0) {
+            const unsigned long long* masks = sMasks + ob * NH + hb;
+            uint32_t bits = 0;
+#pragma unroll
+            for (int g = 0; g < NHW; ++g) bits |= (uint32_t)((masks[g] >> rel) & 1) << g;
+            seen &= bits;
+          }
+          if (ok && !mbar_wait_warp(&v_full[st], (kt / S) & 1, p.status)) ok = false;
+          bool nan = false;
+          const uint4* row = reinterpret_cast<const uint4*>(sV + st * L::kTile + t * D);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 w = row[c];
+            nan |= (__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                    __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                    __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                    __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0;
+          }
+          if constexpr (L::KG > 1) named_barrier_sync(1 + L::KG, L::kKeyThreads);  // both have read
+          if (nan && valid) {
+            lvf = CUDART_NAN_F;
+            if (kg == 0)
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c)
+                reinterpret_cast<uint4*>(sV + st * L::kTile + t * D)[c] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        bool exceed = false;
+#pragma unroll
+        for (int g = 0; g < NHW; ++g) {
+          y[g] = fmaf(y[g], factors[g] * ks, lvf);
+          exceed |= (seen >> g & 1) && y[g] > mref[g] + kExceed;
+        }
+        if (group_any(kg, exceed)) {
+          // The tile's maxima per row, then the rows whose reference moves.
+#pragma unroll
+          for (int g = 0; g < NHW; ++g) {
+            float v = (seen >> g & 1) ? y[g] : -CUDART_INF_F;
+#pragma unroll
+            for (int mk = 16; mk >= 1; mk >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, mk));
+            if (lane == 0) red[(warp & 3) * NHW + g] = v;
+          }
+          named_barrier_sync(1 + kg, 128);
+          float alpha[NHW];
+          bool moved = false;
+#pragma unroll
+          for (int g = 0; g < NHW; ++g) {
+            const float mt =
+                fmaxf(fmaxf(red[g], red[NHW + g]), fmaxf(red[2 * NHW + g], red[3 * NHW + g]));
+            const float mn = mt > mref[g] + kExceed ? mt - kRaise : mref[g];
+            alpha[g] = mn == mref[g] ? 1.f : ex2(mref[g] - mn);
+            moved |= mn != mref[g];
+            mref[g] = mn;
+            l_part[g] *= alpha[g];
+          }
+          named_barrier_sync(1 + kg, 128);  // every thread has read red[]
+          if (i > 0 && moved) {
+            // O^T holds this item's tiles so far: rescaled once their MMAs are
+            // done (P buffer of the previous tile released).
+            if (ok && !mbar_wait_warp(&p_free[(kt - 1) % SB], ((kt - 1) / SB) & 1, p.status))
+              ok = false;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kParts; ++c) {
+              const uint32_t addr = tmem + L::kColO + ob * L::NO + c * NH + hb + lane_base;
+              float o[NHW];
+              tmem_load_small<NHW>(addr, o);
+#pragma unroll
+              for (int g = 0; g < NHW; ++g) o[g] *= alpha[g];
+              tmem_store_small<NHW>(addr, o);
+            }
+            tc_fence_before();
+          }
+        }
+        // The weights of this key: rounded to fp16, then split in three.
+        uint32_t part[kParts][NHW / 4];
+#pragma unroll
+        for (int g = 0; g < NHW; g += 4) {
+          uint32_t h[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float e0 = (seen >> (g + 2 * u) & 1) ? ex2(y[g + 2 * u] - mref[g + 2 * u]) : 0.f;
+            const float e1 =
+                (seen >> (g + 2 * u + 1) & 1) ? ex2(y[g + 2 * u + 1] - mref[g + 2 * u + 1]) : 0.f;
+            l_part[g + 2 * u] = fmaf(e0, inv_v, l_part[g + 2 * u]);
+            l_part[g + 2 * u + 1] = fmaf(e1, inv_v, l_part[g + 2 * u + 1]);
+            h[u] = tiny ? 0u : Cvt<__half>::from_float2(e0, e1);
+          }
+#pragma unroll
+          for (int c = 0; c < kParts; ++c) {
+            const uint32_t lo = e4m3x2(h[0]), hi = e4m3x2(h[1]);
+            part[c][g / 4] = lo | hi << 16;
+            if (c + 1 < kParts) {
+              h[0] = remainder16(h[0], lo);
+              h[1] = remainder16(h[1], hi);
+            }
+          }
+        }
+        // The buffer was last read by the MMAs of tile kt - SB.
+        if (kt >= SB && ok && !mbar_wait_warp(&p_free[kt % SB], ((kt / SB) - 1) & 1, p.status))
+          ok = false;
+        uint4* pb = reinterpret_cast<uint4*>(sP + (kt % SB) * L::kPBuf + (t >> 3) * 8 * L::NO +
+                                             (t & 7) * 16);
+        if constexpr (NH == 4) {
+          pb[0] = make_uint4(part[0][0], part[1][0], part[2][0], 0u);
+        } else if constexpr (NH == 8) {
+          pb[0] = make_uint4(part[0][0], part[0][1], part[1][0], part[1][1]);
+          pb[8] = make_uint4(part[2][0], part[2][1], 0u, 0u);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kParts; ++c)
+            pb[8 * ((c * NH + hb) / 16)] =
+                make_uint4(part[c][0], part[c][1], part[c][2], part[c][3]);
+        }
+        if (nvalid < kKeys && kg == 0) {
+          // The item's last tile: V rows past the context must not feed stale
+          // or NaN values into O^T (their weights are 0, but 0 * NaN is NaN).
+          if (ok && !mbar_wait_warp(&v_full[st], (kt / S) & 1, p.status)) ok = false;
+          if (!valid) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+              reinterpret_cast<uint4*>(sV + st * L::kTile + t * D)[c] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&p_full[kt % SB]);
+      }
+
+      // Row sums over the 128 keys.
+#pragma unroll
+      for (int g = 0; g < NHW; ++g) {
+        float v = l_part[g];
+#pragma unroll
+        for (int mk = 16; mk >= 1; mk >>= 1) v += __shfl_xor_sync(0xffffffffu, v, mk);
+        if (lane == 0) red[(warp & 3) * NHW + g] = v;
+      }
+      named_barrier_sync(1 + kg, 128);
+      const int last = kt - 1;
+      if (ok && !mbar_wait_warp(&p_free[last % SB], (last / SB) & 1, p.status)) ok = false;
+      tc_fence_after();
+      float o[NHW];
+      load_parts<kParts, NH, NHW>(tmem + L::kColO + ob * L::NO + hb + lane_base, o);
+      tc_fence_before();
+      mbar_arrive(&o_free[ob]);
+      float l[NHW];
+#pragma unroll
+      for (int g = 0; g < NHW; ++g)
+        l[g] = (red[g] + red[NHW + g]) + (red[2 * NHW + g] + red[3 * NHW + g]);
+      if (ok) {
+        const int* rows = sRows + ob * NH + hb;
+#pragma unroll
+        for (int g = 0; g < NHW; ++g) {
+          if (!(my_rows >> g & 1)) continue;
+          const float v = l[g] == 0.f ? 0.f : __fdividef(o[g], l[g]);
+          const size_t row = rows[g];
+          if (it.nparts_seq == 1) {
+            if (has_d) static_cast<T*>(p.out)[row * D + d] = static_cast<T>(v);
+          } else {
+            const size_t r = row * p.num_parts + it.part;
+            if (has_d) p.ws_o[r * D + d] = v;
+            if (t == g) {
+              p.ws_m[r] = mref[g];
+              p.ws_l[r] = l[g];
+            }
+          }
+        }
+      }
+      named_barrier_sync(1 + kg, 128);  // red[] and the item's rows are read
+      mbar_arrive(&q_free[ob]);
+      ++k_item;
+    }
+    grid_dep_launch_dependents();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::kSWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(L::kTmemCols));
+  }
+}
+
+// Merge the partitions of sequences whose context spans more than one:
+// out = sum_i w_i o_i / sum_i w_i with w_i = l_i 2^(m_i - max m).  A warp per
+// output row.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) attn_fp8_reduce_kernel(const AttnFp8Params p) {
+  constexpr int E = D / 32;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= (long long)p.total_queries * p.num_q_heads) return;
+  const int query = (int)(row / p.num_q_heads);
+  int s = query;
+  if (p.query_start) {  // the last sequence that starts at or before the query
+    int lo = 0, hi = p.num_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (__ldg(p.query_start + mid) <= query) lo = mid; else hi = mid;
+    }
+    s = lo;
+  }
+  const int raw = __ldg(p.context_lens + s);
+  const long long cap = min((long long)p.max_context_len,
+                            (long long)p.max_blocks_per_seq * p.block_size);
+  const int ctx = raw < 0 ? 0 : (raw > cap ? (int)cap : raw);
+  Item it;
+  bool bad;
+  item_queries(p, s, ctx, &it, &bad);
+  if (query < it.query0 || query >= it.query0 + it.queries) return;
+  const int np = context_partitions(ctx, p.partition_size);
+  if (np <= 1) return;  // written by the attention kernel
+  const float* mrow = p.ws_m + row * p.num_parts;
+  const float* lrow = p.ws_l + row * p.num_parts;
+  const float* orow = p.ws_o + row * p.num_parts * D + lane * E;
+  float M = -CUDART_INF_F;
+  for (int i = lane; i < np; i += 32) M = fmaxf(M, mrow[i]);
+#pragma unroll
+  for (int mk = 16; mk >= 1; mk >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, mk));
+  float sum = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < np; ++i) {
+    const float l = lrow[i];
+    const float w = l == 0.f ? 0.f : l * exp2f(mrow[i] - M);
+    sum += w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, orow[(size_t)i * D + e], acc[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e)
+    out[e] = Cvt<T>::from_float2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+}
+
+// The cache's rows of D codes: boxes of a block's rows of one head, D-byte
+// swizzle.
+bool make_codes_map(CUtensorMap* map, const void* base, long long rows, int head_dim,
+                    int block_size) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)head_dim};
+  const cuuint32_t box[2] = {(cuuint32_t)head_dim, (cuuint32_t)block_size};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int NH, int D>
+cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CUtensorMap& vm,
+                         int ctas, cudaStream_t stream) {
+  using L = Shape<T, NH, D>;
+  static unsigned long long configured = 0;  // bit per device ordinal (< 64)
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    err = cudaFuncSetAttribute(attn_fp8_kernel<T, NH, D>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  const int items = p.num_seqs * p.num_kv_heads * p.num_parts * p.chunks;
+  err = launch_overlapped(attn_fp8_kernel<T, NH, D>, dim3(ctas), dim3(L::kThreads), L::kBytes,
+                          stream, p, km, vm, items);
+  if (err != cudaSuccess || p.num_parts <= 1) return err;
+  const long long rows = (long long)p.total_queries * p.num_q_heads;
+  return launch_overlapped(attn_fp8_reduce_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)),
+                           dim3(128), 0, stream, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const AttnFp8Params& p, const CUtensorMap& km, const CUtensorMap& vm,
+                        int ctas, cudaStream_t stream) {
+  static_assert(kFp8Rows == 32, "the instantiations cover items of up to 32 rows");
+  const int rows = p.max_query_len * p.group;
+  if (rows <= 4) return launch_shape<T, 4, D>(p, km, vm, ctas, stream);
+  if (rows <= 8) return launch_shape<T, 8, D>(p, km, vm, ctas, stream);
+  if (rows <= 16) return launch_shape<T, 16, D>(p, km, vm, ctas, stream);
+  return launch_shape<T, 32, D>(p, km, vm, ctas, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, int sms,
+cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, int ctas,
                             cudaStream_t stream, bool* unsupported) {
-  *unsupported = false;
-  return dtype == PKV_F16 ? launch_typed<__half>(p, head_dim, stream)
-                          : launch_typed<__nv_bfloat16>(p, head_dim, stream);
+  CUtensorMap km, vm;
+  const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
+  *unsupported = !make_codes_map(&km, p.k_cache, rows, head_dim, p.block_size) ||
+                 !make_codes_map(&vm, p.v_cache, rows, head_dim, p.block_size);
+  if (*unsupported) return cudaErrorInvalidValue;
+  if (dtype == PKV_F16)
+    return head_dim == 64 ? launch_rows<__half, 64>(p, km, vm, ctas, stream)
+                          : launch_rows<__half, 128>(p, km, vm, ctas, stream);
+  return head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(p, km, vm, ctas, stream)
+                        : launch_rows<__nv_bfloat16, 128>(p, km, vm, ctas, stream);
 }
 
 }  // namespace pkv

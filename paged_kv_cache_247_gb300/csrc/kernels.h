@@ -340,9 +340,17 @@ struct AttnFp8Params {
   int block_size;
   int num_blocks;
   float qscale;  // scale * log2(e)
+  int chunks;          // work items of up to kFp8Rows rows per (sequence, KV head, partition)
+  int partition_size;  // multiple of 128
+  int num_parts;       // ceil(max_context_len / partition_size), >= 1
+  float* ws_o;         // split only: [total_queries, Hq, num_parts, D]
+  float* ws_m;         // split only: [total_queries, Hq, num_parts] (log2 domain)
+  float* ws_l;
 };
 
-cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, int sms,
+// Persistent: `ctas` CTAs walk the work items.  unsupported is set when the
+// tensor maps of the caches cannot be encoded.
+cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, int ctas,
                             cudaStream_t stream, bool* unsupported);
 
 // Diagnostic: one bounded wait on an mbarrier that nothing completes; it
