@@ -16,14 +16,15 @@
 //   x          = scale log2(e) 2^e k_scale (s1 + s2 / 16 + s3 / 256)
 //   y          = x + log2 v_scale: the V row's scale is an addend of the base-2
 //                logit, and the running reference m is one of y, which is what
-//                gets rounded: p = 2^(y - m), at most 2^8, split into three
-//                parts (12 bits; what lies 2^-26 below the largest is lost)
+//                gets rounded: p = 2^(y - m), at most 2^8, = c1 + c2 / 32 +
+//                c3 / 1024 (12 bits, in steps of 2^-19 or finer)
 //   O^T        [D x parts * rows] += V codes^T . parts
 //   l          += p / v_scale
-//   out        = (o1 + o2 / 16 + o3 / 256) / l
+//   out        = (o1 + o2 / 32 + o3 / 1024) / l
 //
-// m moves when some y exceeds it by more than 8, to 6 below that y, so that p
-// lies high in the range of e4m3.
+// m moves when some y exceeds it by more than 8, to 4 below that y: high in the
+// range of e4m3 (what a part leaves of a p of at most 2^8 is at most 2^3, 2^8
+// times 32), and with room for a larger y before it has to move again.
 //
 // Orientation, pipeline and roles follow the 16-bit decode kernel: keys are the
 // first product's M, the D dimensions the second's (D = 64: an M of 64, whose
@@ -62,8 +63,10 @@ constexpr int kKeys = kTileKeys;  // keys per tile
 constexpr int kParts = 3;         // e4m3 parts of a softmax weight
 constexpr int kScaleStages = 8;
 constexpr int kQWarps = 2;
-constexpr float kRaise = 6.f;     // a moved reference lies this far below the tile's maximum
-constexpr float kExceed = 8.f;    // weights reach 2^8 (e4m3 holds 448) before it moves
+constexpr int kPStep = 32;        // each part of a weight holds 32 times what the last one left
+constexpr float kRaise = 4.f;     // a moved reference lies this far below the tile's maximum
+constexpr float kExceed = 8.f;    // weights reach 2^8 before it moves
+constexpr float kNoRef = -3e38f;  // the reference before any
 constexpr int kMinVExponent = -60;  // V rows below 448 * 2^-60 count as zero
 
 constexpr int up16(int x) { return (x + 15) / 16 * 16; }
@@ -166,19 +169,60 @@ __device__ __forceinline__ void tmem_wait(float* v) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-// v[g] = the sum over PARTS parts, part c in columns c * NH ..., weighted 16^-c.
+// Two floats that one instruction works on.
+struct Pair {
+  unsigned long long v;
+};
+
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 both(Pair a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// v = the sum over PARTS parts, part c in columns c * NH ..., weighted step^c.
 template <int PARTS, int NH, int NHW>
-__device__ __forceinline__ void load_parts(uint32_t taddr, float* v) {
+__device__ __forceinline__ void load_parts(uint32_t taddr, float step, Pair* v) {
   float part[PARTS * NHW];
 #pragma unroll
   for (int c = 0; c < PARTS; ++c) tmem_ld<NHW>(taddr + c * NH, part + c * NHW);
   tmem_wait<PARTS * NHW>(part);
+  const Pair step2 = pair(step, step);
 #pragma unroll
-  for (int g = 0; g < NHW; ++g) {
-    v[g] = part[(PARTS - 1) * NHW + g];
+  for (int g = 0; g < NHW / 2; ++g) {
+    const float* last = part + (PARTS - 1) * NHW + 2 * g;
+    v[g] = pair(last[0], last[1]);
 #pragma unroll
-    for (int c = PARTS - 2; c >= 0; --c) v[g] = fmaf(v[g], 0.0625f, part[c * NHW + g]);
+    for (int c = PARTS - 2; c >= 0; --c)
+      v[g] = fma2(v[g], step2, pair(part[c * NHW + 2 * g], part[c * NHW + 2 * g + 1]));
   }
+}
+
+// The maximum over a warp's lanes.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(uint32_t h2) {
@@ -193,12 +237,12 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
   return r;
 }
 
-// 16 (h - code): what the next part holds.
-__device__ __forceinline__ uint32_t remainder16(uint32_t h2, uint32_t codes) {
+// kPStep (h - code): what the next part holds.
+__device__ __forceinline__ uint32_t remainder_of(uint32_t h2, uint32_t codes) {
   const uint32_t back = half2_of(codes);
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h2),
                             *reinterpret_cast<const __half2*>(&back));
-  const __half2 r = __hmul2(d, __float2half2_rn(16.f));
+  const __half2 r = __hmul2(d, __float2half2_rn((float)kPStep));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -609,12 +653,14 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
       const float* factors = sFactors + ob * NH + hb;
       const uint32_t my_rows =
           it.rows >= hb + NHW ? (1u << NHW) - 1u : (1u << max(it.rows - hb, 0)) - 1u;
-      // The references are the same in every thread of the warpgroup.
-      float mref[NHW], l_part[NHW];
+      // Minus the references, the same in every thread of the warpgroup; rows
+      // past the item's get weights of zero by theirs.
+      Pair nm[NHW / 2], l_part[NHW / 2];
 #pragma unroll
-      for (int g = 0; g < NHW; ++g) {
-        mref[g] = -CUDART_INF_F;
-        l_part[g] = 0.f;
+      for (int g = 0; g < NHW / 2; ++g) {
+        nm[g] = pair(my_rows >> (2 * g) & 1 ? -kNoRef : -CUDART_INF_F,
+                     my_rows >> (2 * g + 1) & 1 ? -kNoRef : -CUDART_INF_F);
+        l_part[g] = pair(0.f, 0.f);
       }
       for (int i = 0; i < it.n_tiles; ++i, ++kt) {
         const int key0 = it.t_begin + i * kKeys;
@@ -629,8 +675,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
         mbar_arrive(&c_free[kt % SC]);
         if (ok && !mbar_wait_warp(&s_full[kt % SB], (kt / SB) & 1, p.status)) ok = false;
         tc_fence_after();
-        float y[NHW];
-        load_parts<L::kQParts, NH, NHW>(tmem + (kt % SB) * L::NS + hb + lane_base, y);
+        Pair y[NHW / 2];
+        load_parts<L::kQParts, NH, NHW>(tmem + (kt % SB) * L::NS + hb + lane_base, 0.0625f, y);
         tc_fence_before();
         mbar_arrive(&s_free[kt % SB]);
 
@@ -640,7 +686,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
         int lv = max(ev, kMinVExponent);
         float lvf = vbits > 0x7f80u ? CUDART_NAN_F : (float)lv;
         const float inv_v = pow2(-min(lv, 126));
-        uint32_t seen = valid ? my_rows : 0u;
+        uint32_t seen = valid ? 0xffffffffu : 0u;
         const bool tail = p.tree_masks != nullptr && key0 + nvalid > it.base;
         const int st = kt % S;
         if (tail) {
@@ -676,33 +722,53 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
                 reinterpret_cast<uint4*>(sV + st * L::kTile + t * D)[c] = make_uint4(0, 0, 0, 0);
           }
         }
-        bool exceed = false;
+        const Pair ks2 = pair(ks, ks), lv2 = pair(lvf, lvf);
 #pragma unroll
-        for (int g = 0; g < NHW; ++g) {
-          y[g] = fmaf(y[g], factors[g] * ks, lvf);
-          exceed |= (seen >> g & 1) && y[g] > mref[g] + kExceed;
+        for (int g = 0; g < NHW / 2; ++g)
+          y[g] = fma2(y[g], mul2(*reinterpret_cast<const Pair*>(factors + 2 * g), ks2), lv2);
+        if (tail || nvalid < kKeys) {
+#pragma unroll
+          for (int g = 0; g < NHW / 2; ++g) {
+            const float2 v = both(y[g]);
+            y[g] = pair(seen >> (2 * g) & 1 ? v.x : -CUDART_INF_F,
+                        seen >> (2 * g + 1) & 1 ? v.y : -CUDART_INF_F);
+          }
         }
-        if (group_any(kg, exceed)) {
+        float2 e[NHW / 2];  // y - m, then the weights
+        float top = -CUDART_INF_F;
+#pragma unroll
+        for (int g = 0; g < NHW / 2; ++g) {
+          e[g] = both(add2(y[g], nm[g]));
+          top = fmax3(top, e[g].x, e[g].y);
+        }
+        if (group_any(kg, top > kExceed)) {
           // The tile's maxima per row, then the rows whose reference moves.
 #pragma unroll
-          for (int g = 0; g < NHW; ++g) {
-            float v = (seen >> g & 1) ? y[g] : -CUDART_INF_F;
-#pragma unroll
-            for (int mk = 16; mk >= 1; mk >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, mk));
-            if (lane == 0) red[(warp & 3) * NHW + g] = v;
+          for (int g = 0; g < NHW / 2; ++g) {
+            const float2 v = both(y[g]);
+            const float a = warp_max(v.x), b = warp_max(v.y);
+            if (lane == 0)
+              *reinterpret_cast<float2*>(red + (warp & 3) * NHW + 2 * g) = make_float2(a, b);
           }
           named_barrier_sync(1 + kg, 128);
           float alpha[NHW];
           bool moved = false;
 #pragma unroll
           for (int g = 0; g < NHW; ++g) {
-            const float mt =
-                fmaxf(fmaxf(red[g], red[NHW + g]), fmaxf(red[2 * NHW + g], red[3 * NHW + g]));
-            const float mn = mt > mref[g] + kExceed ? mt - kRaise : mref[g];
-            alpha[g] = mn == mref[g] ? 1.f : ex2(mref[g] - mn);
-            moved |= mn != mref[g];
-            mref[g] = mn;
-            l_part[g] *= alpha[g];
+            const float2 n2 = both(nm[g / 2]);
+            const float n = g & 1 ? n2.y : n2.x;
+            const float mt = fmax3(fmaxf(red[g], red[NHW + g]), red[2 * NHW + g],
+                                   red[3 * NHW + g]);
+            const bool moves = mt + n > kExceed;
+            alpha[g] = moves ? ex2(kRaise - mt - n) : 1.f;
+            moved |= moves;
+            nm[g / 2] = g & 1 ? pair(n2.x, moves ? kRaise - mt : n)
+                              : pair(moves ? kRaise - mt : n, n2.y);
+          }
+#pragma unroll
+          for (int g = 0; g < NHW / 2; ++g) {
+            l_part[g] = mul2(l_part[g], pair(alpha[2 * g], alpha[2 * g + 1]));
+            e[g] = both(add2(y[g], nm[g]));
           }
           named_barrier_sync(1 + kg, 128);  // every thread has read red[]
           if (i > 0 && moved) {
@@ -724,26 +790,28 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
           }
         }
         // The weights of this key: rounded to fp16, then split in three.
+        const Pair inv2 = pair(inv_v, inv_v);
+        uint32_t h[NHW / 2];
+#pragma unroll
+        for (int g = 0; g < NHW / 2; ++g) {
+          e[g] = make_float2(ex2(e[g].x), ex2(e[g].y));
+          l_part[g] = fma2(pair(e[g].x, e[g].y), inv2, l_part[g]);
+          h[g] = Cvt<__half>::from_float2(e[g].x, e[g].y);
+        }
+        if (tiny) {
+#pragma unroll
+          for (int g = 0; g < NHW / 2; ++g) h[g] = 0u;
+        }
         uint32_t part[kParts][NHW / 4];
 #pragma unroll
-        for (int g = 0; g < NHW; g += 4) {
-          uint32_t h[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float e0 = (seen >> (g + 2 * u) & 1) ? ex2(y[g + 2 * u] - mref[g + 2 * u]) : 0.f;
-            const float e1 =
-                (seen >> (g + 2 * u + 1) & 1) ? ex2(y[g + 2 * u + 1] - mref[g + 2 * u + 1]) : 0.f;
-            l_part[g + 2 * u] = fmaf(e0, inv_v, l_part[g + 2 * u]);
-            l_part[g + 2 * u + 1] = fmaf(e1, inv_v, l_part[g + 2 * u + 1]);
-            h[u] = tiny ? 0u : Cvt<__half>::from_float2(e0, e1);
-          }
+        for (int g = 0; g < NHW / 4; ++g) {
 #pragma unroll
           for (int c = 0; c < kParts; ++c) {
-            const uint32_t lo = e4m3x2(h[0]), hi = e4m3x2(h[1]);
-            part[c][g / 4] = lo | hi << 16;
+            const uint32_t lo = e4m3x2(h[2 * g]), hi = e4m3x2(h[2 * g + 1]);
+            part[c][g] = lo | hi << 16;
             if (c + 1 < kParts) {
-              h[0] = remainder16(h[0], lo);
-              h[1] = remainder16(h[1], hi);
+              h[2 * g] = remainder_of(h[2 * g], lo);
+              h[2 * g + 1] = remainder_of(h[2 * g + 1], hi);
             }
           }
         }
@@ -780,7 +848,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
       // Row sums over the 128 keys.
 #pragma unroll
       for (int g = 0; g < NHW; ++g) {
-        float v = l_part[g];
+        const float2 v2 = both(l_part[g / 2]);
+        float v = g & 1 ? v2.y : v2.x;
 #pragma unroll
         for (int mk = 16; mk >= 1; mk >>= 1) v += __shfl_xor_sync(0xffffffffu, v, mk);
         if (lane == 0) red[(warp & 3) * NHW + g] = v;
@@ -789,8 +858,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
       const int last = kt - 1;
       if (ok && !mbar_wait_warp(&p_free[last % SB], (last / SB) & 1, p.status)) ok = false;
       tc_fence_after();
-      float o[NHW];
-      load_parts<kParts, NH, NHW>(tmem + L::kColO + ob * L::NO + hb + lane_base, o);
+      Pair o[NHW / 2];
+      load_parts<kParts, NH, NHW>(tmem + L::kColO + ob * L::NO + hb + lane_base, 1.f / kPStep, o);
       tc_fence_before();
       mbar_arrive(&o_free[ob]);
       float l[NHW];
@@ -802,7 +871,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
 #pragma unroll
         for (int g = 0; g < NHW; ++g) {
           if (!(my_rows >> g & 1)) continue;
-          const float v = l[g] == 0.f ? 0.f : __fdividef(o[g], l[g]);
+          const float2 o2 = both(o[g / 2]), n2 = both(nm[g / 2]);
+          const float v = l[g] == 0.f ? 0.f : __fdividef(g & 1 ? o2.y : o2.x, l[g]);
           const size_t row = rows[g];
           if (it.nparts_seq == 1) {
             if (has_d) static_cast<T*>(p.out)[row * D + d] = static_cast<T>(v);
@@ -810,7 +880,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
             const size_t r = row * p.num_parts + it.part;
             if (has_d) p.ws_o[r * D + d] = v;
             if (t == g) {
-              p.ws_m[r] = mref[g];
+              p.ws_m[r] = g & 1 ? -n2.y : -n2.x;
               p.ws_l[r] = l[g];
             }
           }
