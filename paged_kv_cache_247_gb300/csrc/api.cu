@@ -1117,9 +1117,8 @@ pkv_status_t attn_fp8_impl(void* out, const void* q, int total_queries, const in
   cudaError_t err = status_word(&p.status);
   if (err != cudaSuccess) return cuda_fail(err);
   bool unsupported = false;
-  const long long items = plan.parts * plan.chunks * num_kv_heads * num_seqs;
-  err = pkv::launch_attn_fp8(p, head_dim, dtype, tc_ctas(items),
-                             reinterpret_cast<cudaStream_t>(stream), &unsupported);
+  err = pkv::launch_attn_fp8(p, head_dim, dtype, reinterpret_cast<cudaStream_t>(stream),
+                             &unsupported);
   if (unsupported) return PKV_ERR_UNSUPPORTED;
   return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
 }

@@ -62,7 +62,8 @@ using namespace tc;
 constexpr int kKeys = kTileKeys;  // keys per tile
 constexpr int kParts = 3;         // e4m3 parts of a softmax weight
 constexpr int kScaleStages = 8;
-constexpr int kQWarps = 2;
+constexpr int kBufs = 2;          // buffers of S^T and of the weights
+constexpr int kItemBufs = 2;      // items handed out ahead
 constexpr int kPStep = 32;        // each part of a weight holds 32 times what the last one left
 constexpr float kRaise = 4.f;     // a moved reference lies this far below the tile's maximum
 constexpr float kExceed = 8.f;    // weights reach 2^8 before it moves
@@ -79,38 +80,51 @@ struct Shape {
   static constexpr int NO = up16(kParts * NH);   // columns of O^T
   static constexpr int KG = NH > 16 ? 2 : 1;     // key warpgroups
   static constexpr int NHW = NH / KG;            // rows per key warpgroup
+  static constexpr int kPerSm = KG == 1 ? 2 : 1; // CTAs per SM
+  static constexpr int kQWarps = KG;
   static constexpr int kKeyThreads = 128 * KG;
   static constexpr int kKWarp = 4 * KG;
   static constexpr int kVWarp = kKWarp + 1;
   static constexpr int kSWarp = kKWarp + 2;  // owns tensor memory
   static constexpr int kOWarp = kKWarp + 3;
   static constexpr int kScaleWarp = kKWarp + 4;
-  static constexpr int kQWarp = kKWarp + 5;
-  static constexpr int kThreads = kKeyThreads + (5 + kQWarps) * 32;
+  static constexpr int kItemWarp = kKWarp + 5;
+  static constexpr int kQWarp = kKWarp + 6;
+  static constexpr int kWarps = kQWarp + kQWarps;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kTile = kKeys * D;     // bytes of a K or V tile
   static constexpr int kQBytes = NS * D;
+  static constexpr int kRaw = NH * D * 2;     // q rows as they are
   static constexpr int kPBuf = kKeys * NO;
-  static constexpr int SB = 3;                // S^T and P buffers
-  // scales, factors, masks, rows, reductions, barriers; alignment
-  static constexpr int kSmall = kScaleStages * kKeys * 4 + 2 * NH * 16 + KG * 4 * NHW * 4 + 1024;
-  static constexpr int kFixed = 2 * kQBytes + SB * kPBuf + kSmall + 1024;
-  static constexpr int kFit = (227 * 1024 - kFixed) / (2 * kTile);
-  static constexpr int kStages = kFit < 12 ? kFit : 12;
+  // scales, an item's rows, reductions, items, barriers; alignment
+  static constexpr int kSmall = kScaleStages * kKeys * 4 + 2 * NH * 16 + 4 * 4 * NH * 4 + 1024;
+  static constexpr int kFixed = 2 * kQBytes + kRaw + kBufs * kPBuf + kSmall + 1024;
+  static constexpr int kRoom = kPerSm == 2 ? 113 * 1024 : 227 * 1024;
+  static constexpr int kFit = (kRoom - kFixed) / (2 * kTile);
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kQ = 2 * kStages * kTile;  // after the K and V rings
-  static constexpr int kP = kQ + 2 * kQBytes;
-  static constexpr int kScales = kP + SB * kPBuf;               // [stages][K, V][128] bfloat16
+  static constexpr int kQRaw = kQ + 2 * kQBytes;
+  static constexpr int kP = kQRaw + kRaw;
+  static constexpr int kScales = kP + kBufs * kPBuf;            // [stages][K, V][128] bfloat16
   static constexpr int kMasks = kScales + kScaleStages * kKeys * 4;  // [2][NH] 64-bit
   static constexpr int kFactors = kMasks + 2 * NH * 8;          // [2][NH] floats
   static constexpr int kRows = kFactors + 2 * NH * 4;           // [2][NH] output rows
-  static constexpr int kRed = kRows + 2 * NH * 4;               // [KG][4 warps][NHW] floats
-  static constexpr int kBar = kRed + KG * 4 * NHW * 4;
-  static constexpr int kBars = 4 * kStages + 4 * SB + 2 * kScaleStages + 8;
+  static constexpr int kTop = kRows + 2 * NH * 4;               // [KG][4 warps][NHW] floats
+  static constexpr int kSum = kTop + 4 * NH * 4;                // [KG][4 warps][NHW]
+  static constexpr int kRef = kSum + 4 * NH * 4;                // [KG][4 warps][NHW]
+  static constexpr int kAlpha = kRef + 4 * NH * 4;              // [KG][4 warps][NHW]
+  static constexpr int kItems = kAlpha + 4 * NH * 4;            // [kItemBufs] Item
+  static constexpr int kTicket = kItems + kItemBufs * 64;
+  static constexpr int kBar = kTicket + 16;
+  static constexpr int kBars =
+      4 * kStages + 4 * kBufs + 2 * kScaleStages + 8 + 2 * kItemBufs + 1;
   static constexpr int kTmemSlot = kBar + kBars * 8;
   static constexpr int kBytes = kTmemSlot + 16 + 1024;
-  static_assert(kBars * 8 + 16 <= 1024 && kBytes <= 227 * 1024, "shared memory overflow");
-  static constexpr int kColO = SB * NS;
-  static constexpr int kTmemCols = pow2_at_least(SB * NS + 2 * NO);
-  static_assert(kTmemCols <= 512, "tensor memory overflow");
+  static_assert(kItemBufs * 64 + kBars * 8 + 32 <= 1024 && kBytes <= kRoom && kStages >= 2,
+                "shared memory overflow");
+  static constexpr int kColO = kBufs * NS;
+  static constexpr int kTmemCols = pow2_at_least(kBufs * NS + 2 * NO);
+  static_assert(kTmemCols <= 512 / kPerSm, "tensor memory overflow");
   static constexpr int kSwizzle = D == 128 ? 2 : 4;  // descriptor code of the D-byte swizzle
 };
 
@@ -248,11 +262,12 @@ __device__ __forceinline__ uint32_t remainder_of(uint32_t h2, uint32_t codes) {
 
 // One work item: up to NH rows of sequence s and one KV head over the partition
 // [t_begin, t_end) of the context (no tiles: nothing to do).
-struct Item {
+struct alignas(16) Item {
   int s, kvh, part, row_first, rows;  // rows [row_first, + rows) of the sequence's
   int query0, queries;                // its first row of q, and how many
-  int ctx, base, t_begin, t_end, n_tiles, nparts_seq;
+  int ctx, base, t_begin, t_end, n_tiles, nparts_seq, unused[3];
 };
+static_assert(sizeof(Item) == 64, "four 16-byte words");
 
 // Sequence s's queries (first row, count); counts that do not fit are cut.
 __device__ __forceinline__ void item_queries(const AttnFp8Params& p, int s, int ctx, Item* it,
@@ -273,8 +288,8 @@ __device__ __forceinline__ void item_queries(const AttnFp8Params& p, int s, int 
 }
 
 template <int NH>
-__device__ __forceinline__ Item item_at(const AttnFp8Params& p, int j, bool report = false) {
-  Item it;
+__device__ __forceinline__ Item item_at(const AttnFp8Params& p, int j, bool report) {
+  Item it{};
   const int chunk = j % p.chunks;
   int r = j / p.chunks;
   it.part = r % p.num_parts;
@@ -305,6 +320,94 @@ __device__ __forceinline__ int output_row(const AttnFp8Params& p, const Item& it
   return (it.query0 + j) * p.num_q_heads + it.kvh * p.group + (row - j * p.group);
 }
 
+// The items a warp goes through, in the order the item warp hands them out.
+struct ItemWalk {
+  const Item* items;
+  uint64_t* full;
+  uint64_t* empty;
+  unsigned int* status;
+  int n = 0;
+
+  // False after the last one, or when the wait gave up (the whole warp agrees).
+  __device__ __forceinline__ bool next(Item* it) {
+    const int b = n % kItemBufs;
+    if (!mbar_wait_warp(&full[b], (n / kItemBufs) & 1, status)) return false;
+    *it = items[b];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[b]);
+    ++n;
+    return it->n_tiles > 0;
+  }
+};
+
+// Ask for the index of a CTA of this grid that has not started, which then
+// never does: this CTA works in its place.  The answer comes as 16 bytes.
+__device__ __forceinline__ void take_cta(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(smem_addr(answer)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+// The index, or -1 where none was left.
+__device__ __forceinline__ int taken_cta(const void* answer) {
+  const volatile unsigned long long* a = static_cast<const volatile unsigned long long*>(answer);
+  uint32_t ok, x = 0;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\tmov.b128 a, {%2, %3};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(ok), "+r"(x)
+      : "l"(a[0]), "l"(a[1]));
+  return ok ? (int)x : -1;
+}
+
+// The sums over a warp's lanes of N values: lane l returns that of value
+// l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float* v) {
+  const int lane = threadIdx.x & 31;
+  int mask = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, mask /= 2) {
+    const bool upper = lane & mask;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = upper ? v[n + i] : v[i], send = upper ? v[i] : v[n + i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
+    }
+  }
+  float r = v[0];
+  for (; mask >= 1; mask /= 2) r += __shfl_xor_sync(0xffffffffu, r, mask);
+  return r;
+}
+
+// Entries [0, n) of a row of the block table, a warp's 32 at a time, the next
+// 32 on their way.
+struct TableWindow {
+  const int32_t* row;
+  int n, first = 0, now, ahead;
+
+  __device__ __forceinline__ TableWindow(const int32_t* r, int entries) : row(r), n(entries) {
+    now = load(0);
+    ahead = load(32);
+  }
+  __device__ __forceinline__ int load(int at) const {
+    const int i = at + (threadIdx.x & 31);
+    return i < n ? __ldg(row + i) : 0;
+  }
+  // Lane l's entry i + at(l); i + at(l) never goes back by more than the window.
+  __device__ __forceinline__ int entry(int i, int at) {
+    if (i >= first + 32) {
+      first += 32;
+      now = ahead;
+      ahead = load(first + 32);
+    }
+    return __shfl_sync(0xffffffffu, now, (i - first + at) & 31);
+  }
+};
+
 // True if any of the 128 threads of key warpgroup kg passes true.
 __device__ __forceinline__ bool group_any(int kg, bool v) {
   uint32_t r;
@@ -313,6 +416,19 @@ __device__ __forceinline__ bool group_any(int kg, bool v) {
       "bar.red.or.pred po, %1, 128, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
       : "=r"(r)
       : "r"(1 + kg), "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// True if any of the threads of the KG key warpgroups passes true.
+template <int KG>
+__device__ __forceinline__ bool keys_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %3, 0;\n\t"
+      "bar.red.or.pred po, %1, %2, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "n"(1 + KG), "n"(128 * KG), "r"(v ? 1u : 0u)
       : "memory");
   return r != 0;
 }
@@ -333,12 +449,18 @@ __device__ __forceinline__ void copy8_async(void* dst, const void* src, int byte
                : "memory");
 }
 
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+
 template <typename T, int NH, int D>
-__global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kPerSm)
     attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap vmap, int num_items) {
+                    const __grid_constant__ CUtensorMap vmap) {
   using L = Shape<T, NH, D>;
-  constexpr int S = L::kStages, SB = L::SB, SC = kScaleStages, NHW = L::NHW;
+  constexpr int S = L::kStages, SB = kBufs, SC = kScaleStages, NHW = L::NHW;
   grid_dep_wait();
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -351,6 +473,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
   unsigned long long* sMasks = reinterpret_cast<unsigned long long*>(smem + L::kMasks);
   float* sFactors = reinterpret_cast<float*>(smem + L::kFactors);
   int* sRows = reinterpret_cast<int*>(smem + L::kRows);
+  Item* sItems = reinterpret_cast<Item*>(smem + L::kItems);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kBar);  // [S] tile landed
   uint64_t* k_empty = k_full + S;   // [S] its MMAs are done (commit)
   uint64_t* v_full = k_empty + S;   // [S]
@@ -365,6 +488,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
   uint64_t* q_free = q_full + 2;    // [2] the item done
   uint64_t* o_free = q_free + 2;    // [2] O^T buffer read
   uint64_t* drain = o_free + 2;     // [2] each issuer's last MMAs finished
+  uint64_t* i_full = drain + 2;     // [kItemBufs] item written
+  uint64_t* i_free = i_full + kItemBufs;  // [kItemBufs] read by every warp
+  uint64_t* ticket = i_free + kItemBufs;  // the answer landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
 
   const int warp = threadIdx.x >> 5;
@@ -388,11 +514,16 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
       mbar_init(&c_free[b], L::kKeyThreads);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&q_full[b], 32 * kQWarps);
+      mbar_init(&q_full[b], 32 * L::kQWarps);
       mbar_init(&q_free[b], L::kKeyThreads);
       mbar_init(&o_free[b], L::kKeyThreads);
       mbar_init(&drain[b], 1);
     }
+    for (int b = 0; b < kItemBufs; ++b) {
+      mbar_init(&i_full[b], 1);
+      mbar_init(&i_free[b], L::kWarps - 1);
+    }
+    mbar_init(ticket, 1);
     fence_barrier_init();
   }
   if (warp == L::kSWarp) {
@@ -405,37 +536,76 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  ItemWalk walk{sItems, i_full, i_free, p.status};
+  Item it;
 
-  if (warp == L::kKWarp || warp == L::kVWarp) {
+  if (warp == L::kItemWarp) {
+    // ------------------------------------------------------------ item warp
+    // Starts with the CTA's own index and goes on with those of CTAs that have
+    // not started, so that an SM whose items are short takes more of them.
+    void* answer = smem + L::kTicket;
+    int j = blockIdx.x, n = 0, asked = 0;
+    bool ok = true;
+    while (ok && j >= 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(ticket, 16);
+        take_cta(answer, ticket);
+      }
+      it = item_at<NH>(p, j, lane == 0);
+      if (it.n_tiles > 0) {
+        const int b = n % kItemBufs;
+        ok = n < kItemBufs || mbar_wait_warp(&i_free[b], (n / kItemBufs - 1) & 1, p.status);
+        if (ok && lane == 0) {
+          sItems[b] = it;
+          mbar_arrive(&i_full[b]);
+        }
+        ++n;
+      } else if (it.ctx == 0 && it.part == 0) {  // nothing to see: zeros
+        constexpr int kWords = D / 8;
+        for (int i = lane; i < it.rows * kWords; i += 32)
+          reinterpret_cast<uint4*>(p.out)[(size_t)output_row(p, it, i / kWords) * kWords +
+                                          i % kWords] = make_uint4(0, 0, 0, 0);
+      }
+      if (!mbar_wait_warp(ticket, asked & 1, p.status)) {
+        mbar_drain(ticket, asked & 1);
+        ok = false;
+        break;
+      }
+      ++asked;
+      j = taken_cta(answer);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    }
+    const int b = n % kItemBufs;
+    if (ok && (n < kItemBufs || mbar_wait_warp(&i_free[b], (n / kItemBufs - 1) & 1, p.status)) &&
+        lane == 0) {
+      sItems[b].n_tiles = 0;  // the end
+      mbar_arrive(&i_full[b]);
+    }
+    __syncwarp();
+  } else if (warp == L::kKWarp || warp == L::kVWarp) {
     // ----------------------------------------------------------- producers
     // Tile i covers keys [t_begin + 128 i, + 128): runs of B rows, one block
-    // each, lane l copies run l.  Block ids are read a tile ahead.
+    // each, lane l copies run l.
     const bool is_k = warp == L::kKWarp;
     const CUtensorMap* map = is_k ? &kmap : &vmap;
     unsigned char* ring = is_k ? sK : sV;
     uint64_t* full = is_k ? k_full : v_full;
     uint64_t* empty = is_k ? k_empty : v_empty;
-    const int B = p.block_size;
+    const int B = p.block_size, shift = 31 - __clz(B), runs = kKeys >> shift;
     prefetch_tensormap(map);
     int kt = 0;
     bool ok = true;
-    for (int j = blockIdx.x; ok && j < num_items; j += gridDim.x) {
-      const Item it = item_at<NH>(p, j);
-      if (it.n_tiles == 0) continue;
-      const int32_t* trow = p.block_tables + (size_t)it.s * p.max_blocks_per_seq;
-      auto table_entry = [&](int i) -> int {
-        const int key = it.t_begin + i * kKeys + lane * B;
-        return (lane * B < kKeys && i < it.n_tiles && key < it.t_end) ? __ldg(trow + key / B) : 0;
-      };
-      int next = table_entry(0);
+    while (ok && walk.next(&it)) {
+      const int blocks = (it.t_end - it.t_begin + B - 1) >> shift;
+      TableWindow table(p.block_tables + (size_t)it.s * p.max_blocks_per_seq +
+                            (it.t_begin >> shift), blocks);
       for (int i = 0; i < it.n_tiles; ++i, ++kt) {
         const int st = kt % S;
-        const int nvalid = min(kKeys, it.t_end - (it.t_begin + i * kKeys));
-        const int nseg = (nvalid + B - 1) / B;
-        int phys = next;
-        next = table_entry(i + 1);
-        if ((unsigned)phys >= (unsigned)p.num_blocks) {
-          if (lane < nseg) atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
+        const int nseg = min(runs, blocks - i * runs);
+        int phys = table.entry(i * runs, lane);
+        if (lane < nseg && (unsigned)phys >= (unsigned)p.num_blocks) {
+          atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
           phys = 0;
         }
         if (kt >= S && !mbar_wait_warp(&empty[st], ((kt / S) - 1) & 1, p.status)) {
@@ -456,29 +626,23 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
   } else if (warp == L::kScaleWarp) {
     // ------------------------------------------------------ scale producer
     // Lane l copies the scales of keys 4 l .. 4 l + 3 (one block: B >= 8).
-    const int B = p.block_size;
+    const int B = p.block_size, shift = 31 - __clz(B), runs = kKeys >> shift;
     int kt = 0;
     bool ok = true;
-    for (int j = blockIdx.x; ok && j < num_items; j += gridDim.x) {
-      const Item it = item_at<NH>(p, j);
-      if (it.n_tiles == 0) continue;
-      const int32_t* trow = p.block_tables + (size_t)it.s * p.max_blocks_per_seq;
-      auto table_entry = [&](int i) -> int {
-        const int key = it.t_begin + i * kKeys + lane * 4;
-        return i < it.n_tiles && key < it.t_end ? __ldg(trow + key / B) : 0;
-      };
-      int next = table_entry(0);
+    while (ok && walk.next(&it)) {
+      TableWindow table(p.block_tables + (size_t)it.s * p.max_blocks_per_seq +
+                            (it.t_begin >> shift),
+                        (it.t_end - it.t_begin + B - 1) >> shift);
       for (int i = 0; i < it.n_tiles; ++i, ++kt) {
         const int key = it.t_begin + i * kKeys + lane * 4;
-        int phys = next;
-        next = table_entry(i + 1);
+        int phys = table.entry(i * runs, (lane * 4) >> shift);
         if ((unsigned)phys >= (unsigned)p.num_blocks) phys = 0;  // (flagged by the others)
         const int st = kt % SC;
         if (kt >= SC && !mbar_wait_warp(&c_free[st], ((kt / SC) - 1) & 1, p.status)) {
           ok = false;
           break;
         }
-        const size_t row = ((size_t)phys * p.num_kv_heads + it.kvh) * B + key % B;
+        const size_t row = (((size_t)phys * p.num_kv_heads + it.kvh) << shift) + (key & (B - 1));
         const int bytes = key < it.t_end ? 8 : 0;
         copy8_async(sScales + (2 * st) * kKeys + lane * 4, p.k_scales + (bytes ? row : 0), bytes);
         copy8_async(sScales + (2 * st + 1) * kKeys + lane * 4, p.v_scales + (bytes ? row : 0),
@@ -492,79 +656,72 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
     __syncwarp();
   } else if (warp >= L::kQWarp) {
     // -------------------------------------------------------------- Q warps
-    // Warp w of kQWarps splits rows w, w + kQWarps, ...: lane l holds elements
-    // D / 32 * l ...  Rows past the item's are zeros.
-    constexpr int E = D / 32;
-    const int w = warp - L::kQWarp;
-    int k_item = 0;
-    for (int j = blockIdx.x; j < num_items; j += gridDim.x) {
-      const Item it = item_at<NH>(p, j);
-      if (it.n_tiles == 0) continue;
-      const int b = k_item & 1;
+    // Warp w brings its rows into shared memory as they are, then splits them:
+    // a row lies in D / 8 lanes.  Rows past the item's are zeros.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = NH / L::kQWarps;
+    const int w = warp - L::kQWarp, c = lane % kLanes;
+    unsigned char* raw = smem + L::kQRaw + w * kMine * D * 2;
+    while (walk.next(&it)) {
+      const int k_item = walk.n - 1, b = k_item & 1;
+      const int my_row = min(lane, it.rows - 1);  // lane l knows row l
+      const int my_out = output_row(p, it, my_row);
+      for (int r = lane / kLanes; r < kMine; r += kAtOnce) {
+        const int row = w * kMine + r;
+        const int from = __shfl_sync(0xffffffffu, my_out, row);
+        copy16_async(raw + (r * kLanes + c) * 16,
+                     static_cast<const T*>(p.q) + (size_t)from * D + c * 8,
+                     row < it.rows ? 16 : 0);
+      }
+      unsigned long long mask = 0;
+      if (p.tree_masks && w == 0)
+        mask = (unsigned long long)__ldg(reinterpret_cast<const long long*>(p.tree_masks) +
+                                         my_out / p.num_q_heads);
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (k_item >= 2 && !mbar_wait_warp(&q_free[b], ((k_item - 2) >> 1) & 1, p.status)) break;
+      if (w == 0 && lane < NH) {
+        sRows[b * NH + lane] = my_out;
+        sMasks[b * NH + lane] = mask;
+      }
       unsigned char* dst = sQ + b * L::kQBytes;
-#pragma unroll 4
-      for (int r = w; r < NH; r += kQWarps) {
-        const bool there = r < it.rows;
-        const int out_row = there ? output_row(p, it, r) : 0;
-        uint32_t raw[E / 2] = {};
-        if (there) {
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(
-              static_cast<const T*>(p.q) + (size_t)out_row * D + lane * E);
-          if constexpr (E == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-            raw[0] = v.x;
-            raw[1] = v.y;
-          } else {
-            raw[0] = __ldg(src);
-          }
-        }
-        uint32_t top = raw[0] & 0x7fff7fffu;
-        if constexpr (E == 4) top = __vmaxu2(top, raw[1] & 0x7fff7fffu);
+#pragma unroll 1
+      for (int r = lane / kLanes; r < kMine; r += kAtOnce) {
+        const uint4 x = *reinterpret_cast<const uint4*>(raw + (r * kLanes + c) * 16);
+        uint32_t top = max_magnitude(x);
+#pragma unroll
+        for (int mk = kLanes / 2; mk >= 1; mk >>= 1)
+          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, mk));
         top = max(top & 0xffffu, top >> 16);
-        top = __reduce_max_sync(0xffffffffu, top);
         const bool finite = top < Magnitude<T>::kInf;
         const int e = row_exponent(finite ? Magnitude<T>::value(top) : 0.f);
         const float inv = finite ? pow2(-e) : 0.f;
-        float y[E];
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+        float y[8];
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          const float2 f = Cvt<T>::to_float2(raw[i]);
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = Cvt<T>::to_float2(words[i]);
           y[2 * i] = finite ? f.x * inv : 0.f;
           y[2 * i + 1] = finite ? f.y * inv : 0.f;
         }
 #pragma unroll
-        for (int c = 0; c < L::kQParts; ++c) {
-          uint32_t codes = 0;
+        for (int part = 0; part < L::kQParts; ++part) {
+          uint32_t codes[4];
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i) {
-            const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]),
-                                                          __NV_SATFINITE, __NV_E4M3);
-            codes |= two << (16 * i);
-            const float2 back = decode2(two);
+          for (int i = 0; i < 4; ++i) {
+            codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]),
+                                                __NV_SATFINITE, __NV_E4M3);
+            const float2 back = decode2(codes[i]);
             y[2 * i] = (y[2 * i] - back.x) * 16.f;
             y[2 * i + 1] = (y[2 * i + 1] - back.y) * 16.f;
           }
-          unsigned char* to = dst + swizzled<D>(c * NH + r, lane * E);
-          if constexpr (E == 4)
-            *reinterpret_cast<uint32_t*>(to) = codes;
-          else
-            *reinterpret_cast<uint16_t*>(to) = (uint16_t)codes;
+          *reinterpret_cast<uint2*>(dst + swizzled<D>(part * NH + w * kMine + r, c * 8)) =
+              make_uint2(codes[0] | codes[1] << 16, codes[2] | codes[3] << 16);
         }
-        if (lane == 0) {
-          sFactors[b * NH + r] = finite ? p.qscale * pow2(e) : CUDART_NAN_F;
-          sRows[b * NH + r] = out_row;
-          if (p.tree_masks)
-            sMasks[b * NH + r] =
-                there ? (unsigned long long)__ldg(
-                            reinterpret_cast<const long long*>(p.tree_masks) +
-                            out_row / p.num_q_heads)
-                      : 0;
-        }
+        if (c == 0)
+          sFactors[b * NH + w * kMine + r] = finite ? p.qscale * pow2(e) : CUDART_NAN_F;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&q_full[b]);
-      ++k_item;
+      __syncwarp();  // the rows are read before the next item's land
     }
     __syncwarp();
   } else if (warp == L::kSWarp || warp == L::kOWarp) {
@@ -573,12 +730,10 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
     const uint32_t idesc = is_s ? instr(false, L::NS, kKeys) : instr(true, L::NO, D);
     const uint32_t aK = smem_addr(sK), aV = smem_addr(sV), aQ = smem_addr(sQ),
                    aP = smem_addr(sP);
-    int kt = 0, k_item = 0;
+    int kt = 0;
     bool ok = true;
-    for (int j = blockIdx.x; ok && j < num_items; j += gridDim.x) {
-      const Item it = item_at<NH>(p, j);
-      if (it.n_tiles == 0) continue;
-      const int b = k_item & 1;
+    while (ok && walk.next(&it)) {
+      const int k_item = walk.n - 1, b = k_item & 1;
       if (is_s) {
         if (!mbar_wait_warp(&q_full[b], (k_item >> 1) & 1, p.status)) break;
         for (int i = 0; i < it.n_tiles; ++i, ++kt) {
@@ -622,7 +777,6 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
           mma_commit_warp(&v_empty[st]);
         }
       }
-      ++k_item;
     }
     uint64_t* d = &drain[is_s ? 0 : 1];
     mma_commit_warp(d);
@@ -630,60 +784,62 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
     __syncwarp();
   } else {
     // ----------------------------------------------------- key warpgroups
+    // Code that runs once per item or seldom is kept short (loops that stay
+    // loops): straight-line code met for the first time runs at the latency of
+    // its fetch.
     const int kg = warp >> 2;
     const int t = threadIdx.x & 127;  // key of the tile == tensor-memory lane
     const int hb = kg * NHW;          // first row of this warpgroup
+    const int row = lane & (NHW - 1); // the row whose reference this lane keeps
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     // the dimension whose outputs this lane holds (D = 64: half of the lanes)
     const int d = D == 128 ? t : (warp & 3) * 16 + lane;
     const bool has_d = D == 128 || lane < 16;
-    float* red = reinterpret_cast<float*>(smem + L::kRed) + kg * 4 * NHW;
-    int kt = 0, k_item = 0;
+    const int at = (kg * 4 + (warp & 3)) * NHW;
+    float* tops = reinterpret_cast<float*>(smem + L::kTop) + kg * 4 * NHW;
+    float* sums = reinterpret_cast<float*>(smem + L::kSum) + kg * 4 * NHW;
+    float* refs = reinterpret_cast<float*>(smem + L::kRef) + at;      // minus the references
+    float* alphas = reinterpret_cast<float*>(smem + L::kAlpha) + at;  // this warp's copies
+    int kt = 0;
     bool ok = true;
-    for (int j = blockIdx.x; j < num_items; j += gridDim.x) {
-      const Item it = item_at<NH>(p, j, kg == 0 && t == 0);
-      if (it.n_tiles == 0) {
-        if (it.ctx == 0 && it.part == 0 && has_d)  // nothing to see: zeros
-          for (int g = hb; g < min(hb + NHW, it.rows); ++g)
-            static_cast<T*>(p.out)[(size_t)output_row(p, it, g) * D + d] = static_cast<T>(0.f);
-        continue;
-      }
-      const int ob = k_item & 1;
-      if (ok && !mbar_wait_warp(&q_full[ob], (k_item >> 1) & 1, p.status)) ok = false;
+    for (;;) {
+      const bool more = walk.next(&it);
+      if (keys_any<L::KG>(!more)) break;  // the key warps leave together
+      const int k_item = walk.n - 1, ob = k_item & 1;
+      ok = ok && mbar_wait(&q_full[ob], (k_item >> 1) & 1, p.status);
       const float* factors = sFactors + ob * NH + hb;
-      const uint32_t my_rows =
-          it.rows >= hb + NHW ? (1u << NHW) - 1u : (1u << max(it.rows - hb, 0)) - 1u;
-      // Minus the references, the same in every thread of the warpgroup; rows
-      // past the item's get weights of zero by theirs.
-      Pair nm[NHW / 2], l_part[NHW / 2];
+      // Rows past the item's get weights of zero by their reference.
+      float nm = hb + row < it.rows ? -kNoRef : -CUDART_INF_F;
+      if (lane < NHW) refs[row] = nm;
+      __syncwarp();
+      Pair l_part[NHW / 2];
 #pragma unroll
-      for (int g = 0; g < NHW / 2; ++g) {
-        nm[g] = pair(my_rows >> (2 * g) & 1 ? -kNoRef : -CUDART_INF_F,
-                     my_rows >> (2 * g + 1) & 1 ? -kNoRef : -CUDART_INF_F);
-        l_part[g] = pair(0.f, 0.f);
-      }
+      for (int g = 0; g < NHW / 2; ++g) l_part[g] = pair(0.f, 0.f);
       for (int i = 0; i < it.n_tiles; ++i, ++kt) {
         const int key0 = it.t_begin + i * kKeys;
         const int nvalid = min(kKeys, it.t_end - key0);
         const bool valid = t < nvalid;
+        const int sb = kt % SB, sc = kt % SC;
+        const uint32_t s_phase = (kt / SB) & 1;
         // A wait that gives up (never expected) leaves ok false; the loop runs
         // on without waiting, so that every named barrier stays matched, and
         // nothing it computes is stored.
-        if (ok && !mbar_wait_warp(&c_full[kt % SC], (kt / SC) & 1, p.status)) ok = false;
-        const float ks = scale_value(sScales[2 * (kt % SC) * kKeys + t]);
-        const uint32_t vbits = sScales[(2 * (kt % SC) + 1) * kKeys + t];
-        mbar_arrive(&c_free[kt % SC]);
-        if (ok && !mbar_wait_warp(&s_full[kt % SB], (kt / SB) & 1, p.status)) ok = false;
+        ok = ok && mbar_wait(&c_full[sc], (kt / SC) & 1, p.status);
+        const float ks = scale_value(sScales[2 * sc * kKeys + t]);
+        const uint32_t vbits = sScales[(2 * sc + 1) * kKeys + t];
+        mbar_arrive(&c_free[sc]);
+        ok = ok && mbar_wait(&s_full[sb], s_phase, p.status);
+        __syncwarp();
         tc_fence_after();
         Pair y[NHW / 2];
-        load_parts<L::kQParts, NH, NHW>(tmem + (kt % SB) * L::NS + hb + lane_base, 0.0625f, y);
+        load_parts<L::kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, 0.0625f, y);
         tc_fence_before();
-        mbar_arrive(&s_free[kt % SB]);
+        mbar_arrive(&s_free[sb]);
 
         // What this key's V scale does: y = x + lv, l gets p * 2^-lv.
         const int ev = (int)(vbits >> 7) - 127;
         const bool tiny = ev < kMinVExponent;
-        int lv = max(ev, kMinVExponent);
+        const int lv = max(ev, kMinVExponent);
         float lvf = vbits > 0x7f80u ? CUDART_NAN_F : (float)lv;
         const float inv_v = pow2(-min(lv, 126));
         uint32_t seen = valid ? 0xffffffffu : 0u;
@@ -698,16 +854,16 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
           if (valid && rel >= 0) {
             const unsigned long long* masks = sMasks + ob * NH + hb;
             uint32_t bits = 0;
-#pragma unroll
+#pragma unroll 4
             for (int g = 0; g < NHW; ++g) bits |= (uint32_t)((masks[g] >> rel) & 1) << g;
-            seen &= bits;
+            seen = bits;
           }
-          if (ok && !mbar_wait_warp(&v_full[st], (kt / S) & 1, p.status)) ok = false;
+          ok = ok && mbar_wait(&v_full[st], (kt / S) & 1, p.status);
           bool nan = false;
-          const uint4* row = reinterpret_cast<const uint4*>(sV + st * L::kTile + t * D);
-#pragma unroll
+          uint4* v_row = reinterpret_cast<uint4*>(sV + st * L::kTile + t * D);
+#pragma unroll 2
           for (int c = 0; c < D / 16; ++c) {
-            const uint4 w = row[c];
+            const uint4 w = v_row[c];
             nan |= (__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
                     __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
                     __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu) |
@@ -717,9 +873,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
           if (nan && valid) {
             lvf = CUDART_NAN_F;
             if (kg == 0)
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c)
-                reinterpret_cast<uint4*>(sV + st * L::kTile + t * D)[c] = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+              for (int c = 0; c < D / 16; ++c) v_row[c] = make_uint4(0, 0, 0, 0);
           }
         }
         const Pair ks2 = pair(ks, ks), lv2 = pair(lvf, lvf);
@@ -738,52 +893,50 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
         float top = -CUDART_INF_F;
 #pragma unroll
         for (int g = 0; g < NHW / 2; ++g) {
-          e[g] = both(add2(y[g], nm[g]));
+          e[g] = both(add2(y[g], *reinterpret_cast<const Pair*>(refs + 2 * g)));
           top = fmax3(top, e[g].x, e[g].y);
         }
         if (group_any(kg, top > kExceed)) {
-          // The tile's maxima per row, then the rows whose reference moves.
+          // The tile's maxima per row, then the rows whose reference moves:
+          // lane r of each warp settles row r.
+          float mine = 0.f;
 #pragma unroll
           for (int g = 0; g < NHW / 2; ++g) {
             const float2 v = both(y[g]);
             const float a = warp_max(v.x), b = warp_max(v.y);
-            if (lane == 0)
-              *reinterpret_cast<float2*>(red + (warp & 3) * NHW + 2 * g) = make_float2(a, b);
+            if (row / 2 == g) mine = row & 1 ? b : a;
           }
+          if (lane < NHW) tops[(warp & 3) * NHW + row] = mine;
           named_barrier_sync(1 + kg, 128);
-          float alpha[NHW];
-          bool moved = false;
-#pragma unroll
-          for (int g = 0; g < NHW; ++g) {
-            const float2 n2 = both(nm[g / 2]);
-            const float n = g & 1 ? n2.y : n2.x;
-            const float mt = fmax3(fmaxf(red[g], red[NHW + g]), red[2 * NHW + g],
-                                   red[3 * NHW + g]);
-            const bool moves = mt + n > kExceed;
-            alpha[g] = moves ? ex2(kRaise - mt - n) : 1.f;
-            moved |= moves;
-            nm[g / 2] = g & 1 ? pair(n2.x, moves ? kRaise - mt : n)
-                              : pair(moves ? kRaise - mt : n, n2.y);
+          const float mt = fmax3(fmaxf(tops[row], tops[NHW + row]), tops[2 * NHW + row],
+                                 tops[3 * NHW + row]);
+          const bool moves = mt + nm > kExceed;
+          const float alpha = moves ? ex2(kRaise - mt - nm) : 1.f;
+          if (moves) nm = kRaise - mt;
+          if (lane < NHW) {
+            refs[row] = nm;
+            alphas[row] = alpha;
           }
+          const bool moved = __any_sync(0xffffffffu, moves);  // (orders the stores, too)
+          __syncwarp();
 #pragma unroll
           for (int g = 0; g < NHW / 2; ++g) {
-            l_part[g] = mul2(l_part[g], pair(alpha[2 * g], alpha[2 * g + 1]));
-            e[g] = both(add2(y[g], nm[g]));
+            l_part[g] = mul2(l_part[g], *reinterpret_cast<const Pair*>(alphas + 2 * g));
+            e[g] = both(add2(y[g], *reinterpret_cast<const Pair*>(refs + 2 * g)));
           }
-          named_barrier_sync(1 + kg, 128);  // every thread has read red[]
           if (i > 0 && moved) {
             // O^T holds this item's tiles so far: rescaled once their MMAs are
             // done (P buffer of the previous tile released).
-            if (ok && !mbar_wait_warp(&p_free[(kt - 1) % SB], ((kt - 1) / SB) & 1, p.status))
-              ok = false;
+            ok = ok && mbar_wait(&p_free[(kt - 1) % SB], ((kt - 1) / SB) & 1, p.status);
+            __syncwarp();
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kParts; ++c) {
               const uint32_t addr = tmem + L::kColO + ob * L::NO + c * NH + hb + lane_base;
               float o[NHW];
               tmem_load_small<NHW>(addr, o);
 #pragma unroll
-              for (int g = 0; g < NHW; ++g) o[g] *= alpha[g];
+              for (int g = 0; g < NHW; ++g) o[g] *= alphas[g];
               tmem_store_small<NHW>(addr, o);
             }
             tc_fence_before();
@@ -816,9 +969,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
           }
         }
         // The buffer was last read by the MMAs of tile kt - SB.
-        if (kt >= SB && ok && !mbar_wait_warp(&p_free[kt % SB], ((kt / SB) - 1) & 1, p.status))
-          ok = false;
-        uint4* pb = reinterpret_cast<uint4*>(sP + (kt % SB) * L::kPBuf + (t >> 3) * 8 * L::NO +
+        if (kt >= SB) ok = ok && mbar_wait(&p_free[sb], s_phase ^ 1, p.status);
+        uint4* pb = reinterpret_cast<uint4*>(sP + sb * L::kPBuf + (t >> 3) * 8 * L::NO +
                                              (t & 7) * 16);
         if constexpr (NH == 4) {
           pb[0] = make_uint4(part[0][0], part[1][0], part[2][0], 0u);
@@ -834,61 +986,62 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 1)
         if (nvalid < kKeys && kg == 0) {
           // The item's last tile: V rows past the context must not feed stale
           // or NaN values into O^T (their weights are 0, but 0 * NaN is NaN).
-          if (ok && !mbar_wait_warp(&v_full[st], (kt / S) & 1, p.status)) ok = false;
+          ok = ok && mbar_wait(&v_full[st], (kt / S) & 1, p.status);
           if (!valid) {
-#pragma unroll
+#pragma unroll 2
             for (int c = 0; c < D / 16; ++c)
               reinterpret_cast<uint4*>(sV + st * L::kTile + t * D)[c] = make_uint4(0, 0, 0, 0);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(&p_full[kt % SB]);
+        mbar_arrive(&p_full[sb]);
       }
 
       // Row sums over the 128 keys.
+      float l_mine[NHW];
 #pragma unroll
-      for (int g = 0; g < NHW; ++g) {
-        const float2 v2 = both(l_part[g / 2]);
-        float v = g & 1 ? v2.y : v2.x;
-#pragma unroll
-        for (int mk = 16; mk >= 1; mk >>= 1) v += __shfl_xor_sync(0xffffffffu, v, mk);
-        if (lane == 0) red[(warp & 3) * NHW + g] = v;
+      for (int g = 0; g < NHW / 2; ++g) {
+        const float2 v = both(l_part[g]);
+        l_mine[2 * g] = v.x;
+        l_mine[2 * g + 1] = v.y;
       }
+      __syncwarp();
+      const float sum = warp_sums<NHW>(l_mine);
+      if (lane % (32 / NHW) == 0) sums[(warp & 3) * NHW + lane / (32 / NHW)] = sum;
       named_barrier_sync(1 + kg, 128);
       const int last = kt - 1;
-      if (ok && !mbar_wait_warp(&p_free[last % SB], (last / SB) & 1, p.status)) ok = false;
+      ok = ok && mbar_wait(&p_free[last % SB], (last / SB) & 1, p.status);
+      __syncwarp();
       tc_fence_after();
-      Pair o[NHW / 2];
-      load_parts<kParts, NH, NHW>(tmem + L::kColO + ob * L::NO + hb + lane_base, 1.f / kPStep, o);
-      tc_fence_before();
-      mbar_arrive(&o_free[ob]);
-      float l[NHW];
+      const int* rows = sRows + ob * NH + hb;
+      const int there = it.rows - hb;  // of this warpgroup's rows
+#pragma unroll 1
+      for (int g = 0; g < NHW && g < there; g += 4) {
+        Pair o[2];
+        load_parts<kParts, NH, 4>(tmem + L::kColO + ob * L::NO + hb + g + lane_base,
+                                  1.f / kPStep, o);
+        const float2 lo = both(o[0]), hi = both(o[1]);
+        const float v[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-      for (int g = 0; g < NHW; ++g)
-        l[g] = (red[g] + red[NHW + g]) + (red[2 * NHW + g] + red[3 * NHW + g]);
-      if (ok) {
-        const int* rows = sRows + ob * NH + hb;
-#pragma unroll
-        for (int g = 0; g < NHW; ++g) {
-          if (!(my_rows >> g & 1)) continue;
-          const float2 o2 = both(o[g / 2]), n2 = both(nm[g / 2]);
-          const float v = l[g] == 0.f ? 0.f : __fdividef(g & 1 ? o2.y : o2.x, l[g]);
-          const size_t row = rows[g];
-          if (it.nparts_seq == 1) {
-            if (has_d) static_cast<T*>(p.out)[row * D + d] = static_cast<T>(v);
-          } else {
-            const size_t r = row * p.num_parts + it.part;
-            if (has_d) p.ws_o[r * D + d] = v;
-            if (t == g) {
-              p.ws_m[r] = g & 1 ? -n2.y : -n2.x;
-              p.ws_l[r] = l[g];
-            }
-          }
+        for (int u = 0; u < 4; ++u) {
+          const float l = (sums[g + u] + sums[NHW + g + u]) +
+                          (sums[2 * NHW + g + u] + sums[3 * NHW + g + u]);
+          const float x = l == 0.f ? 0.f : __fdividef(v[u], l);
+          if (!ok || !has_d || g + u >= there) continue;
+          if (it.nparts_seq == 1)
+            static_cast<T*>(p.out)[(size_t)rows[g + u] * D + d] = static_cast<T>(x);
+          else
+            p.ws_o[((size_t)rows[g + u] * p.num_parts + it.part) * D + d] = x;
         }
       }
-      named_barrier_sync(1 + kg, 128);  // red[] and the item's rows are read
-      mbar_arrive(&q_free[ob]);
-      ++k_item;
+      tc_fence_before();
+      mbar_arrive(&o_free[ob]);
+      if (ok && it.nparts_seq > 1 && t < NHW && t < there) {
+        const size_t r = (size_t)rows[t] * p.num_parts + it.part;
+        p.ws_m[r] = -nm;
+        p.ws_l[r] = (sums[t] + sums[NHW + t]) + (sums[2 * NHW + t] + sums[3 * NHW + t]);
+      }
+      mbar_arrive(&q_free[ob]);  // the item's rows are read
     }
     grid_dep_launch_dependents();
   }
@@ -976,7 +1129,7 @@ bool make_codes_map(CUtensorMap* map, const void* base, long long rows, int head
 
 template <typename T, int NH, int D>
 cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CUtensorMap& vm,
-                         int ctas, cudaStream_t stream) {
+                         cudaStream_t stream) {
   using L = Shape<T, NH, D>;
   static unsigned long long configured = 0;  // bit per device ordinal (< 64)
   int dev = 0;
@@ -989,8 +1142,8 @@ cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CU
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
   const int items = p.num_seqs * p.num_kv_heads * p.num_parts * p.chunks;
-  err = launch_overlapped(attn_fp8_kernel<T, NH, D>, dim3(ctas), dim3(L::kThreads), L::kBytes,
-                          stream, p, km, vm, items);
+  err = launch_overlapped(attn_fp8_kernel<T, NH, D>, dim3(items), dim3(L::kThreads), L::kBytes,
+                          stream, p, km, vm);
   if (err != cudaSuccess || p.num_parts <= 1) return err;
   const long long rows = (long long)p.total_queries * p.num_q_heads;
   return launch_overlapped(attn_fp8_reduce_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)),
@@ -999,29 +1152,29 @@ cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CU
 
 template <typename T, int D>
 cudaError_t launch_rows(const AttnFp8Params& p, const CUtensorMap& km, const CUtensorMap& vm,
-                        int ctas, cudaStream_t stream) {
+                        cudaStream_t stream) {
   static_assert(kFp8Rows == 32, "the instantiations cover items of up to 32 rows");
   const int rows = p.max_query_len * p.group;
-  if (rows <= 4) return launch_shape<T, 4, D>(p, km, vm, ctas, stream);
-  if (rows <= 8) return launch_shape<T, 8, D>(p, km, vm, ctas, stream);
-  if (rows <= 16) return launch_shape<T, 16, D>(p, km, vm, ctas, stream);
-  return launch_shape<T, 32, D>(p, km, vm, ctas, stream);
+  if (rows <= 4) return launch_shape<T, 4, D>(p, km, vm, stream);
+  if (rows <= 8) return launch_shape<T, 8, D>(p, km, vm, stream);
+  if (rows <= 16) return launch_shape<T, 16, D>(p, km, vm, stream);
+  return launch_shape<T, 32, D>(p, km, vm, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, int ctas,
-                            cudaStream_t stream, bool* unsupported) {
+cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, cudaStream_t stream,
+                            bool* unsupported) {
   CUtensorMap km, vm;
   const long long rows = (long long)p.num_blocks * p.num_kv_heads * p.block_size;
   *unsupported = !make_codes_map(&km, p.k_cache, rows, head_dim, p.block_size) ||
                  !make_codes_map(&vm, p.v_cache, rows, head_dim, p.block_size);
   if (*unsupported) return cudaErrorInvalidValue;
   if (dtype == PKV_F16)
-    return head_dim == 64 ? launch_rows<__half, 64>(p, km, vm, ctas, stream)
-                          : launch_rows<__half, 128>(p, km, vm, ctas, stream);
-  return head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(p, km, vm, ctas, stream)
-                        : launch_rows<__nv_bfloat16, 128>(p, km, vm, ctas, stream);
+    return head_dim == 64 ? launch_rows<__half, 64>(p, km, vm, stream)
+                          : launch_rows<__half, 128>(p, km, vm, stream);
+  return head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(p, km, vm, stream)
+                        : launch_rows<__nv_bfloat16, 128>(p, km, vm, stream);
 }
 
 }  // namespace pkv

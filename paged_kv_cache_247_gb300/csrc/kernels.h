@@ -348,10 +348,9 @@ struct AttnFp8Params {
   float* ws_l;
 };
 
-// Persistent: `ctas` CTAs walk the work items.  unsupported is set when the
-// tensor maps of the caches cannot be encoded.
-cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, int ctas,
-                            cudaStream_t stream, bool* unsupported);
+// unsupported is set when the tensor maps of the caches cannot be encoded.
+cudaError_t launch_attn_fp8(const AttnFp8Params& p, int head_dim, int dtype, cudaStream_t stream,
+                            bool* unsupported);
 
 // Diagnostic: one bounded wait on an mbarrier that nothing completes; it
 // gives up after the wait limit and raises PKV_DEV_WAIT_TIMEOUT.
