@@ -16,15 +16,16 @@
 //   x          = scale log2(e) 2^e k_scale (s1 + s2 / 16 + s3 / 256)
 //   y          = x + log2 v_scale: the V row's scale is an addend of the base-2
 //                logit, and the running reference m is one of y, which is what
-//                gets rounded: p = 2^(y - m), at most 2^8, = c1 + c2 / 32 +
-//                c3 / 1024 (12 bits, in steps of 2^-19 or finer)
+//                gets rounded: p = 2^(y - m) < 2^15, to fp16, which is c1 + c2 +
+//                c3 in e5m2: what each part leaves of 11 bits fits the next
+//                (3 bits and twice 3 and the sign), down to steps of 2^-16
 //   O^T        [D x parts * rows] += V codes^T . parts
 //   l          += p / v_scale
-//   out        = (o1 + o2 / 32 + o3 / 1024) / l
+//   out        = (o1 + o2 + o3) / l
 //
-// m moves when some y exceeds it by more than 8, to 4 below that y: high in the
-// range of e4m3 (what a part leaves of a p of at most 2^8 is at most 2^3, 2^8
-// times 32), and with room for a larger y before it has to move again.
+// m moves when some y is 15 above it, to 8 below that y: what is lost of a
+// weight is at most 2^-25 of the largest, and the largest has room to grow by
+// 2^7 before m moves again, which costs about as much as a tile.
 //
 // Orientation, pipeline and roles follow the 16-bit decode kernel: keys are the
 // first product's M, the D dimensions the second's (D = 64: an M of 64, whose
@@ -39,9 +40,10 @@
 //              the end dimension t of the output.  Its parts of the weights are
 //              neighbouring bytes (MN-major operand, no swizzle): one 16-byte
 //              store for every 16 of them.
-//   K, V producers   one TMA copy per (block, head) run into a ring of tiles
-//   scale producer   the tile's K and V scales by asynchronous copies
+//   K, V producers   one TMA copy per (block, head) run into a ring of tiles, the
+//              K warp also the scales of both
 //   Q warps          rows split into their parts, one item ahead
+//   item warp        the next items, from the CTAs that have not started
 //   S, O issuers     four (D = 64: two, four) MMAs per tile
 
 #include <math_constants.h>
@@ -60,13 +62,11 @@ namespace {
 using namespace tc;
 
 constexpr int kKeys = kTileKeys;  // keys per tile
-constexpr int kParts = 3;         // e4m3 parts of a softmax weight
-constexpr int kScaleStages = 8;
+constexpr int kParts = 3;         // e5m2 parts of a softmax weight
 constexpr int kBufs = 2;          // buffers of S^T and of the weights
 constexpr int kItemBufs = 2;      // items handed out ahead
-constexpr int kPStep = 32;        // each part of a weight holds 32 times what the last one left
-constexpr float kRaise = 4.f;     // a moved reference lies this far below the tile's maximum
-constexpr float kExceed = 8.f;    // weights reach 2^8 before it moves
+constexpr float kRaise = 8.f;     // a moved reference lies this far below the tile's maximum
+constexpr float kExceed = 15.f;   // weights reach 2^15 (e5m2 and fp16 hold them) before it moves
 constexpr float kNoRef = -3e38f;  // the reference before any
 constexpr int kMinVExponent = -60;  // V rows below 448 * 2^-60 count as zero
 
@@ -82,14 +82,12 @@ struct Shape {
   static constexpr int NHW = NH / KG;            // rows per key warpgroup
   static constexpr int kPerSm = KG == 1 ? 2 : 1; // CTAs per SM
   static constexpr int kQWarps = KG;
-  static constexpr int kKeyThreads = 128 * KG;
   static constexpr int kKWarp = 4 * KG;
   static constexpr int kVWarp = kKWarp + 1;
   static constexpr int kSWarp = kKWarp + 2;  // owns tensor memory
   static constexpr int kOWarp = kKWarp + 3;
-  static constexpr int kScaleWarp = kKWarp + 4;
-  static constexpr int kItemWarp = kKWarp + 5;
-  static constexpr int kQWarp = kKWarp + 6;
+  static constexpr int kItemWarp = kKWarp + 4;
+  static constexpr int kQWarp = kKWarp + 5;
   static constexpr int kWarps = kQWarp + kQWarps;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTile = kKeys * D;     // bytes of a K or V tile
@@ -97,14 +95,19 @@ struct Shape {
   static constexpr int kRaw = NH * D * 2;     // q rows as they are
   static constexpr int kPBuf = kKeys * NO;
   // scales, an item's rows, reductions, items, barriers; alignment
-  static constexpr int kSmall = kScaleStages * kKeys * 4 + 2 * NH * 16 + 4 * 4 * NH * 4 + 1024;
+  static constexpr int kMaxStages = 8;
+  static constexpr int kSmall = (kMaxStages + kBufs) * kKeys * 4 + 2 * NH * 16 + 4 * 4 * NH * 4 + 1024;
   static constexpr int kFixed = 2 * kQBytes + kRaw + kBufs * kPBuf + kSmall + 1024;
   static constexpr int kRoom = kPerSm == 2 ? 113 * 1024 : 227 * 1024;
   static constexpr int kFit = (kRoom - kFixed) / (2 * kTile);
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kQ = 2 * kStages * kTile;  // after the K and V rings
   static constexpr int kQRaw = kQ + 2 * kQBytes;
   static constexpr int kP = kQRaw + kRaw;
+  // A tile's scales come with its K rows.  Nothing says when they have been
+  // read: they are before the tile's S^T is given back, without which the tile
+  // kBufs later is not multiplied, without which its K stage does not get free.
+  static constexpr int kScaleStages = kStages + kBufs;
   static constexpr int kScales = kP + kBufs * kPBuf;            // [stages][K, V][128] bfloat16
   static constexpr int kMasks = kScales + kScaleStages * kKeys * 4;  // [2][NH] 64-bit
   static constexpr int kFactors = kMasks + 2 * NH * 8;          // [2][NH] floats
@@ -117,7 +120,7 @@ struct Shape {
   static constexpr int kTicket = kItems + kItemBufs * 64;
   static constexpr int kBar = kTicket + 16;
   static constexpr int kBars =
-      4 * kStages + 4 * kBufs + 2 * kScaleStages + 8 + 2 * kItemBufs + 1;
+      4 * kStages + 4 * kBufs + kScaleStages + 8 + 2 * kItemBufs + 1;
   static constexpr int kTmemSlot = kBar + kBars * 8;
   static constexpr int kBytes = kTmemSlot + 16 + 1024;
   static_assert(kItemBufs * 64 + kBars * 8 + 32 <= 1024 && kBytes <= kRoom && kStages >= 2,
@@ -135,9 +138,11 @@ __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo, uint32_t s
          ((uint64_t)swizzle << 61);
 }
 
-// Instruction descriptor of kind::f8f6f4: fp32 accumulator, both operands e4m3.
-__device__ __forceinline__ uint32_t instr(bool mn_major, int n, int m) {
-  return (1u << 4) | (mn_major ? 3u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) |
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator (bit 4), e4m3 codes
+// of the cache times e4m3 parts of queries, both K-major, or e5m2 parts of
+// weights (bits 10-12), both MN-major (bits 15, 16).
+__device__ __forceinline__ uint32_t instr(bool weights, int n, int m) {
+  return (1u << 4) | (weights ? 1u << 10 | 3u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
 
@@ -214,21 +219,30 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
   return r;
 }
 
-// v = the sum over PARTS parts, part c in columns c * NH ..., weighted step^c.
-template <int PARTS, int NH, int NHW>
-__device__ __forceinline__ void load_parts(uint32_t taddr, float step, Pair* v) {
+// Values 2 g and 2 g + 1 of an array at a 16-byte boundary, read four at a time.
+__device__ __forceinline__ Pair pair_at(const float* x, int g) {
+  const float4 v = *reinterpret_cast<const float4*>(x + (g & ~1) * 2);
+  return g & 1 ? pair(v.z, v.w) : pair(v.x, v.y);
+}
+
+// v = the sum over PARTS parts, part c in columns c * NH ..., weighted 16^-c
+// where they are scaled.
+template <int PARTS, int NH, int NHW, bool SCALED>
+__device__ __forceinline__ void load_parts(uint32_t taddr, Pair* v) {
   float part[PARTS * NHW];
 #pragma unroll
   for (int c = 0; c < PARTS; ++c) tmem_ld<NHW>(taddr + c * NH, part + c * NHW);
   tmem_wait<PARTS * NHW>(part);
-  const Pair step2 = pair(step, step);
+  const Pair step = pair(0.0625f, 0.0625f);
 #pragma unroll
   for (int g = 0; g < NHW / 2; ++g) {
     const float* last = part + (PARTS - 1) * NHW + 2 * g;
     v[g] = pair(last[0], last[1]);
 #pragma unroll
-    for (int c = PARTS - 2; c >= 0; --c)
-      v[g] = fma2(v[g], step2, pair(part[c * NHW + 2 * g], part[c * NHW + 2 * g + 1]));
+    for (int c = PARTS - 2; c >= 0; --c) {
+      const Pair next = pair(part[c * NHW + 2 * g], part[c * NHW + 2 * g + 1]);
+      v[g] = SCALED ? fma2(v[g], step, next) : add2(v[g], next);
+    }
   }
 }
 
@@ -239,25 +253,18 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t h2) {
+__device__ __forceinline__ uint32_t e5m2x2(uint32_t h2) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
   return r;
 }
 
-__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
-  return r;
-}
-
-// kPStep (h - code): what the next part holds.
+// h - codes (an e5m2 code is the upper byte of its fp16 value): exact.
 __device__ __forceinline__ uint32_t remainder_of(uint32_t h2, uint32_t codes) {
-  const uint32_t back = half2_of(codes);
+  const uint32_t back = __byte_perm(codes, 0u, 0x1404);
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h2),
                             *reinterpret_cast<const __half2*>(&back));
-  const __half2 r = __hmul2(d, __float2half2_rn((float)kPStep));
-  return *reinterpret_cast<const uint32_t*>(&r);
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 // One work item: up to NH rows of sequence s and one KV head over the partition
@@ -449,6 +456,13 @@ __device__ __forceinline__ void copy8_async(void* dst, const void* src, int byte
                : "memory");
 }
 
+// One arrival for what every lane of the warp has done.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Sixteen bytes, or zeros where `bytes` is 0.
 __device__ __forceinline__ void copy16_async(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
                "r"(bytes)
@@ -460,7 +474,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap) {
   using L = Shape<T, NH, D>;
-  constexpr int S = L::kStages, SB = kBufs, SC = kScaleStages, NHW = L::NHW;
+  constexpr int S = L::kStages, SB = kBufs, SC = L::kScaleStages, NHW = L::NHW;
   grid_dep_wait();
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -483,8 +497,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
   uint64_t* p_full = s_free + SB;   // [SB] weights written
   uint64_t* p_free = p_full + SB;   // [SB] their MMAs are done (commit)
   uint64_t* c_full = p_free + SB;   // [SC] the tile's scales landed
-  uint64_t* c_free = c_full + SC;   // [SC] read by the key warpgroups
-  uint64_t* q_full = c_free + SC;   // [2] an item's rows, factors and masks written
+  uint64_t* q_full = c_full + SC;   // [2] an item's rows, factors and masks written
   uint64_t* q_free = q_full + 2;    // [2] the item done
   uint64_t* o_free = q_free + 2;    // [2] O^T buffer read
   uint64_t* drain = o_free + 2;     // [2] each issuer's last MMAs finished
@@ -505,18 +518,15 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     }
     for (int b = 0; b < SB; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_free[b], L::kKeyThreads);
-      mbar_init(&p_full[b], L::kKeyThreads);
+      mbar_init(&s_free[b], 4 * L::KG);  // a lane of each key warp arrives
+      mbar_init(&p_full[b], 4 * L::KG);
       mbar_init(&p_free[b], 1);
     }
-    for (int b = 0; b < SC; ++b) {
-      mbar_init(&c_full[b], 32);
-      mbar_init(&c_free[b], L::kKeyThreads);
-    }
+    for (int b = 0; b < SC; ++b) mbar_init(&c_full[b], 32);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&q_full[b], 32 * L::kQWarps);
-      mbar_init(&q_free[b], L::kKeyThreads);
-      mbar_init(&o_free[b], L::kKeyThreads);
+      mbar_init(&q_full[b], L::kQWarps);
+      mbar_init(&q_free[b], 4 * L::KG);
+      mbar_init(&o_free[b], 4 * L::KG);
       mbar_init(&drain[b], 1);
     }
     for (int b = 0; b < kItemBufs; ++b) {
@@ -586,7 +596,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
   } else if (warp == L::kKWarp || warp == L::kVWarp) {
     // ----------------------------------------------------------- producers
     // Tile i covers keys [t_begin + 128 i, + 128): runs of B rows, one block
-    // each, lane l copies run l.
+    // each, lane l copies run l.  The K warp brings the scales as well: lane l
+    // those of keys 4 l .. 4 l + 3 (one block: B >= 8).
     const bool is_k = warp == L::kKWarp;
     const CUtensorMap* map = is_k ? &kmap : &vmap;
     unsigned char* ring = is_k ? sK : sV;
@@ -603,56 +614,39 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       for (int i = 0; i < it.n_tiles; ++i, ++kt) {
         const int st = kt % S;
         const int nseg = min(runs, blocks - i * runs);
-        int phys = table.entry(i * runs, lane);
-        if (lane < nseg && (unsigned)phys >= (unsigned)p.num_blocks) {
-          atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
+        int phys = table.entry(i * runs, lane & 15);
+        int phys4 = is_k ? table.entry(i * runs, (lane * 4) >> shift) : 0;
+        if ((unsigned)phys >= (unsigned)p.num_blocks) {
+          if (lane < nseg) atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
           phys = 0;
         }
+        if ((unsigned)phys4 >= (unsigned)p.num_blocks) phys4 = 0;
         if (kt >= S && !mbar_wait_warp(&empty[st], ((kt / S) - 1) & 1, p.status)) {
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)nseg * B * D);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nseg * D) << shift);
         __syncwarp();
         if (lane < nseg)
-          tma_load_run(ring + st * L::kTile + lane * B * D, map,
-                       (phys * p.num_kv_heads + it.kvh) * B, &full[st]);
-      }
-    }
-    // After a timeout, copies still in flight land before the CTA leaves.
-    if (timed_out(p.status))
-      for (int i = kt > S ? kt - S : 0; i < kt; ++i) mbar_drain(&full[i % S], (i / S) & 1);
-    __syncwarp();
-  } else if (warp == L::kScaleWarp) {
-    // ------------------------------------------------------ scale producer
-    // Lane l copies the scales of keys 4 l .. 4 l + 3 (one block: B >= 8).
-    const int B = p.block_size, shift = 31 - __clz(B), runs = kKeys >> shift;
-    int kt = 0;
-    bool ok = true;
-    while (ok && walk.next(&it)) {
-      TableWindow table(p.block_tables + (size_t)it.s * p.max_blocks_per_seq +
-                            (it.t_begin >> shift),
-                        (it.t_end - it.t_begin + B - 1) >> shift);
-      for (int i = 0; i < it.n_tiles; ++i, ++kt) {
-        const int key = it.t_begin + i * kKeys + lane * 4;
-        int phys = table.entry(i * runs, (lane * 4) >> shift);
-        if ((unsigned)phys >= (unsigned)p.num_blocks) phys = 0;  // (flagged by the others)
-        const int st = kt % SC;
-        if (kt >= SC && !mbar_wait_warp(&c_free[st], ((kt / SC) - 1) & 1, p.status)) {
-          ok = false;
-          break;
+          tma_load_run(ring + st * L::kTile + ((lane * D) << shift), map,
+                       (phys * p.num_kv_heads + it.kvh) << shift, &full[st]);
+        if (is_k) {
+          const int key = it.t_begin + i * kKeys + lane * 4;
+          const size_t row = (((size_t)phys4 * p.num_kv_heads + it.kvh) << shift) + (key & (B - 1));
+          const int bytes = key < it.t_end ? 8 : 0;
+          uint16_t* to = sScales + 2 * (kt % SC) * kKeys + lane * 4;
+          copy8_async(to, p.k_scales + (bytes ? row : 0), bytes);
+          copy8_async(to + kKeys, p.v_scales + (bytes ? row : 0), bytes);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                           smem_addr(&c_full[kt % SC]))
+                       : "memory");
         }
-        const size_t row = (((size_t)phys * p.num_kv_heads + it.kvh) << shift) + (key & (B - 1));
-        const int bytes = key < it.t_end ? 8 : 0;
-        copy8_async(sScales + (2 * st) * kKeys + lane * 4, p.k_scales + (bytes ? row : 0), bytes);
-        copy8_async(sScales + (2 * st + 1) * kKeys + lane * 4, p.v_scales + (bytes ? row : 0),
-                    bytes);
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_addr(&c_full[st]))
-                     : "memory");
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    // After a timeout, copies still in flight land before the CTA leaves.
+    if (timed_out(p.status))
+      for (int i = kt > S ? kt - S : 0; i < kt; ++i) mbar_drain(&full[i % S], (i / S) & 1);
     __syncwarp();
   } else if (warp >= L::kQWarp) {
     // -------------------------------------------------------------- Q warps
@@ -720,8 +714,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           sFactors[b * NH + w * kMine + r] = finite ? p.qscale * pow2(e) : CUDART_NAN_F;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&q_full[b]);
-      __syncwarp();  // the rows are read before the next item's land
+      arrive_warp(&q_full[b]);
     }
     __syncwarp();
   } else if (warp == L::kSWarp || warp == L::kOWarp) {
@@ -800,7 +793,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     float* sums = reinterpret_cast<float*>(smem + L::kSum) + kg * 4 * NHW;
     float* refs = reinterpret_cast<float*>(smem + L::kRef) + at;      // minus the references
     float* alphas = reinterpret_cast<float*>(smem + L::kAlpha) + at;  // this warp's copies
-    int kt = 0;
+    int kt = 0, sc = 0;
+    uint32_t sc_phase = 0;
     bool ok = true;
     for (;;) {
       const bool more = walk.next(&it);
@@ -819,22 +813,30 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         const int key0 = it.t_begin + i * kKeys;
         const int nvalid = min(kKeys, it.t_end - key0);
         const bool valid = t < nvalid;
-        const int sb = kt % SB, sc = kt % SC;
+        const int sb = kt % SB;
         const uint32_t s_phase = (kt / SB) & 1;
         // A wait that gives up (never expected) leaves ok false; the loop runs
         // on without waiting, so that every named barrier stays matched, and
         // nothing it computes is stored.
-        ok = ok && mbar_wait(&c_full[sc], (kt / SC) & 1, p.status);
-        const float ks = scale_value(sScales[2 * sc * kKeys + t]);
-        const uint32_t vbits = sScales[(2 * sc + 1) * kKeys + t];
-        mbar_arrive(&c_free[sc]);
-        ok = ok && mbar_wait(&s_full[sb], s_phase, p.status);
+        // (Both are asked before either answer is looked at.)
+        const bool c_here = mbar_try_wait(&c_full[sc], sc_phase);
+        const bool s_here = mbar_try_wait(&s_full[sb], s_phase);
+        if (!(c_here && s_here))
+          ok = ok && mbar_wait(&c_full[sc], sc_phase, p.status) &&
+               mbar_wait(&s_full[sb], s_phase, p.status);
         __syncwarp();
         tc_fence_after();
+        const uint16_t* scales = sScales + 2 * sc * kKeys + t;
+        if (++sc == SC) {
+          sc = 0;
+          sc_phase ^= 1;
+        }
+        const float ks = scale_value(scales[0]);
+        const uint32_t vbits = scales[kKeys];
         Pair y[NHW / 2];
-        load_parts<L::kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, 0.0625f, y);
+        load_parts<L::kQParts, NH, NHW, true>(tmem + sb * L::NS + hb + lane_base, y);
         tc_fence_before();
-        mbar_arrive(&s_free[sb]);
+        arrive_warp(&s_free[sb]);
 
         // What this key's V scale does: y = x + lv, l gets p * 2^-lv.
         const int ev = (int)(vbits >> 7) - 127;
@@ -869,7 +871,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
                     __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu) |
                     __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0;
           }
-          if constexpr (L::KG > 1) named_barrier_sync(1 + L::KG, L::kKeyThreads);  // both have read
+          if constexpr (L::KG > 1) named_barrier_sync(1 + L::KG, 128 * L::KG);  // both have read
           if (nan && valid) {
             lvf = CUDART_NAN_F;
             if (kg == 0)
@@ -879,8 +881,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         }
         const Pair ks2 = pair(ks, ks), lv2 = pair(lvf, lvf);
 #pragma unroll
-        for (int g = 0; g < NHW / 2; ++g)
-          y[g] = fma2(y[g], mul2(*reinterpret_cast<const Pair*>(factors + 2 * g), ks2), lv2);
+        for (int g = 0; g < NHW / 2; ++g) y[g] = fma2(y[g], mul2(pair_at(factors, g), ks2), lv2);
         if (tail || nvalid < kKeys) {
 #pragma unroll
           for (int g = 0; g < NHW / 2; ++g) {
@@ -893,7 +894,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         float top = -CUDART_INF_F;
 #pragma unroll
         for (int g = 0; g < NHW / 2; ++g) {
-          e[g] = both(add2(y[g], *reinterpret_cast<const Pair*>(refs + 2 * g)));
+          e[g] = both(add2(y[g], pair_at(refs, g)));
           top = fmax3(top, e[g].x, e[g].y);
         }
         if (group_any(kg, top > kExceed)) {
@@ -921,8 +922,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           __syncwarp();
 #pragma unroll
           for (int g = 0; g < NHW / 2; ++g) {
-            l_part[g] = mul2(l_part[g], *reinterpret_cast<const Pair*>(alphas + 2 * g));
-            e[g] = both(add2(y[g], *reinterpret_cast<const Pair*>(refs + 2 * g)));
+            l_part[g] = mul2(l_part[g], pair_at(alphas, g));
+            e[g] = both(add2(y[g], pair_at(refs, g)));
           }
           if (i > 0 && moved) {
             // O^T holds this item's tiles so far: rescaled once their MMAs are
@@ -942,7 +943,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
             tc_fence_before();
           }
         }
-        // The weights of this key: rounded to fp16, then split in three.
+        // The weights of this key: rounded to fp16, then split in three.  The
+        // buffer was last read by the MMAs of tile kt - SB.
+        const bool p_here = kt < SB || mbar_test_wait(&p_free[sb], s_phase ^ 1);
         const Pair inv2 = pair(inv_v, inv_v);
         uint32_t h[NHW / 2];
 #pragma unroll
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         for (int g = 0; g < NHW / 4; ++g) {
 #pragma unroll
           for (int c = 0; c < kParts; ++c) {
-            const uint32_t lo = e4m3x2(h[2 * g]), hi = e4m3x2(h[2 * g + 1]);
+            const uint32_t lo = e5m2x2(h[2 * g]), hi = e5m2x2(h[2 * g + 1]);
             part[c][g] = lo | hi << 16;
             if (c + 1 < kParts) {
               h[2 * g] = remainder_of(h[2 * g], lo);
@@ -968,8 +971,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
             }
           }
         }
-        // The buffer was last read by the MMAs of tile kt - SB.
-        if (kt >= SB) ok = ok && mbar_wait(&p_free[sb], s_phase ^ 1, p.status);
+        if (!p_here) ok = ok && mbar_wait(&p_free[sb], s_phase ^ 1, p.status);
         uint4* pb = reinterpret_cast<uint4*>(sP + sb * L::kPBuf + (t >> 3) * 8 * L::NO +
                                              (t & 7) * 16);
         if constexpr (NH == 4) {
@@ -994,7 +996,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(&p_full[sb]);
+        arrive_warp(&p_full[sb]);
       }
 
       // Row sums over the 128 keys.
@@ -1018,8 +1020,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
 #pragma unroll 1
       for (int g = 0; g < NHW && g < there; g += 4) {
         Pair o[2];
-        load_parts<kParts, NH, 4>(tmem + L::kColO + ob * L::NO + hb + g + lane_base,
-                                  1.f / kPStep, o);
+        load_parts<kParts, NH, 4, false>(tmem + L::kColO + ob * L::NO + hb + g + lane_base, o);
         const float2 lo = both(o[0]), hi = both(o[1]);
         const float v[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
@@ -1035,13 +1036,13 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         }
       }
       tc_fence_before();
-      mbar_arrive(&o_free[ob]);
+      arrive_warp(&o_free[ob]);
       if (ok && it.nparts_seq > 1 && t < NHW && t < there) {
         const size_t r = (size_t)rows[t] * p.num_parts + it.part;
         p.ws_m[r] = -nm;
         p.ws_l[r] = (sums[t] + sums[NHW + t]) + (sums[2 * NHW + t] + sums[3 * NHW + t]);
       }
-      mbar_arrive(&q_free[ob]);  // the item's rows are read
+      arrive_warp(&q_free[ob]);  // the item's rows are read
     }
     grid_dep_launch_dependents();
   }
