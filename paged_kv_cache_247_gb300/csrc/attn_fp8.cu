@@ -42,7 +42,7 @@
 //              store for every 16 of them.
 //   K, V producers   one TMA copy per (block, head) run into a ring of tiles, the
 //              K warp also the scales of both
-//   Q warps          rows split into their parts, one item ahead
+//   Q warps          rows split into their parts, an item ahead
 //   item warp        the next items, from the CTAs that have not started
 //   S, O issuers     four (D = 64: two, four) MMAs per tile
 
@@ -63,7 +63,7 @@ using namespace tc;
 
 constexpr int kKeys = kTileKeys;  // keys per tile
 constexpr int kParts = 3;         // e5m2 parts of a softmax weight
-constexpr int kBufs = 2;          // buffers of S^T and of the weights
+constexpr int kBufs = 2;          // buffers of the weights
 constexpr int kItemBufs = 2;      // items handed out ahead
 constexpr float kRaise = 8.f;     // a moved reference lies this far below the tile's maximum
 constexpr float kExceed = 15.f;   // weights reach 2^15 (e5m2 and fp16 hold them) before it moves
@@ -80,34 +80,39 @@ struct Shape {
   static constexpr int NO = up16(kParts * NH);   // columns of O^T
   static constexpr int KG = NH > 16 ? 2 : 1;     // key warpgroups
   static constexpr int NHW = NH / KG;            // rows per key warpgroup
-  static constexpr int kPerSm = KG == 1 ? 2 : 1; // CTAs per SM
   static constexpr int kQWarps = KG;
+  static constexpr int kQBufs = KG == 1 ? 2 : 1;                // items' parts of q held
+  static constexpr int SB = KG == 2 && kQParts == 3 ? 1 : 2;    // S^T buffers
   static constexpr int kKWarp = 4 * KG;
   static constexpr int kVWarp = kKWarp + 1;
   static constexpr int kSWarp = kKWarp + 2;  // owns tensor memory
   static constexpr int kOWarp = kKWarp + 3;
   static constexpr int kItemWarp = kKWarp + 4;
   static constexpr int kQWarp = kKWarp + 5;
-  static constexpr int kWarps = kQWarp + kQWarps;
+  static constexpr int kReaders = kQWarp + kQWarps - 1;  // warps that read the items
+  // Two key warpgroups take most of the registers, which warpgroups give and
+  // take as a whole: one warp more, idle, fills the last.
+  static constexpr int kWarps = KG == 1 ? kQWarp + kQWarps : 16;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTile = kKeys * D;     // bytes of a K or V tile
   static constexpr int kQBytes = NS * D;
-  static constexpr int kRaw = NH * D * 2;     // q rows as they are
+  static constexpr int kRawRows = NH < 16 ? NH : 16;
+  static constexpr int kRaw = kRawRows * D * 2;  // q rows as they are, some at a time
   static constexpr int kPBuf = kKeys * NO;
   // scales, an item's rows, reductions, items, barriers; alignment
-  static constexpr int kMaxStages = 8;
-  static constexpr int kSmall = (kMaxStages + kBufs) * kKeys * 4 + 2 * NH * 16 + 4 * 4 * NH * 4 + 1024;
-  static constexpr int kFixed = 2 * kQBytes + kRaw + kBufs * kPBuf + kSmall + 1024;
-  static constexpr int kRoom = kPerSm == 2 ? 113 * 1024 : 227 * 1024;
+  static constexpr int kMaxStages = 384 / D;  // (no more fit beside two CTAs' other needs)
+  static constexpr int kSmall = (kMaxStages + SB) * kKeys * 4 + 2 * NH * 16 + 4 * 4 * NH * 4 + 1024;
+  static constexpr int kFixed = kQBufs * kQBytes + kRaw + kBufs * kPBuf + kSmall + 1024;
+  static constexpr int kRoom = 113 * 1024;  // two CTAs per SM
   static constexpr int kFit = (kRoom - kFixed) / (2 * kTile);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kQ = 2 * kStages * kTile;  // after the K and V rings
-  static constexpr int kQRaw = kQ + 2 * kQBytes;
+  static constexpr int kQRaw = kQ + kQBufs * kQBytes;
   static constexpr int kP = kQRaw + kRaw;
   // A tile's scales come with its K rows.  Nothing says when they have been
   // read: they are before the tile's S^T is given back, without which the tile
-  // kBufs later is not multiplied, without which its K stage does not get free.
-  static constexpr int kScaleStages = kStages + kBufs;
+  // SB later is not multiplied, without which its K stage does not get free.
+  static constexpr int kScaleStages = kStages + SB;
   static constexpr int kScales = kP + kBufs * kPBuf;            // [stages][K, V][128] bfloat16
   static constexpr int kMasks = kScales + kScaleStages * kKeys * 4;  // [2][NH] 64-bit
   static constexpr int kFactors = kMasks + 2 * NH * 8;          // [2][NH] floats
@@ -120,14 +125,14 @@ struct Shape {
   static constexpr int kTicket = kItems + kItemBufs * 64;
   static constexpr int kBar = kTicket + 16;
   static constexpr int kBars =
-      4 * kStages + 4 * kBufs + kScaleStages + 8 + 2 * kItemBufs + 1;
+      4 * kStages + 2 * SB + 2 * kBufs + kScaleStages + 2 * kQBufs + 4 + 2 * kItemBufs + 1;
   static constexpr int kTmemSlot = kBar + kBars * 8;
   static constexpr int kBytes = kTmemSlot + 16 + 1024;
   static_assert(kItemBufs * 64 + kBars * 8 + 32 <= 1024 && kBytes <= kRoom && kStages >= 2,
                 "shared memory overflow");
-  static constexpr int kColO = kBufs * NS;
-  static constexpr int kTmemCols = pow2_at_least(kBufs * NS + 2 * NO);
-  static_assert(kTmemCols <= 512 / kPerSm, "tensor memory overflow");
+  static constexpr int kColO = SB * NS;
+  static constexpr int kTmemCols = pow2_at_least(SB * NS + NO);
+  static_assert(kTmemCols <= 256, "tensor memory overflow");
   static constexpr int kSwizzle = D == 128 ? 2 : 4;  // descriptor code of the D-byte swizzle
 };
 
@@ -229,19 +234,23 @@ __device__ __forceinline__ Pair pair_at(const float* x, int g) {
 // where they are scaled.
 template <int PARTS, int NH, int NHW, bool SCALED>
 __device__ __forceinline__ void load_parts(uint32_t taddr, Pair* v) {
-  float part[PARTS * NHW];
-#pragma unroll
-  for (int c = 0; c < PARTS; ++c) tmem_ld<NHW>(taddr + c * NH, part + c * NHW);
-  tmem_wait<PARTS * NHW>(part);
+  constexpr int kOnce = NHW < 8 ? NHW : 8;  // more would not fit the registers
   const Pair step = pair(0.0625f, 0.0625f);
 #pragma unroll
-  for (int g = 0; g < NHW / 2; ++g) {
-    const float* last = part + (PARTS - 1) * NHW + 2 * g;
-    v[g] = pair(last[0], last[1]);
+  for (int first = 0; first < NHW; first += kOnce) {
+    float part[PARTS * kOnce];
 #pragma unroll
-    for (int c = PARTS - 2; c >= 0; --c) {
-      const Pair next = pair(part[c * NHW + 2 * g], part[c * NHW + 2 * g + 1]);
-      v[g] = SCALED ? fma2(v[g], step, next) : add2(v[g], next);
+    for (int c = 0; c < PARTS; ++c) tmem_ld<kOnce>(taddr + c * NH + first, part + c * kOnce);
+    tmem_wait<PARTS * kOnce>(part);
+#pragma unroll
+    for (int g = 0; g < kOnce / 2; ++g) {
+      Pair x = pair(part[(PARTS - 1) * kOnce + 2 * g], part[(PARTS - 1) * kOnce + 2 * g + 1]);
+#pragma unroll
+      for (int c = PARTS - 2; c >= 0; --c) {
+        const Pair next = pair(part[c * kOnce + 2 * g], part[c * kOnce + 2 * g + 1]);
+        x = SCALED ? fma2(x, step, next) : add2(x, next);
+      }
+      v[first / 2 + g] = x;
     }
   }
 }
@@ -470,11 +479,12 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src, int byt
 }
 
 template <typename T, int NH, int D>
-__global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kPerSm)
+__global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
     attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap) {
   using L = Shape<T, NH, D>;
-  constexpr int S = L::kStages, SB = kBufs, SC = L::kScaleStages, NHW = L::NHW;
+  constexpr int S = L::kStages, SB = L::SB, PB = kBufs, SC = L::kScaleStages, NHW = L::NHW,
+                QB = L::kQBufs;
   grid_dep_wait();
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -494,13 +504,13 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
   uint64_t* v_empty = v_full + S;   // [S]
   uint64_t* s_full = v_empty + S;   // [SB] S^T computed (commit)
   uint64_t* s_free = s_full + SB;   // [SB] read by the key warpgroups
-  uint64_t* p_full = s_free + SB;   // [SB] weights written
-  uint64_t* p_free = p_full + SB;   // [SB] their MMAs are done (commit)
-  uint64_t* c_full = p_free + SB;   // [SC] the tile's scales landed
-  uint64_t* q_full = c_full + SC;   // [2] an item's rows, factors and masks written
-  uint64_t* q_free = q_full + 2;    // [2] the item done
-  uint64_t* o_free = q_free + 2;    // [2] O^T buffer read
-  uint64_t* drain = o_free + 2;     // [2] each issuer's last MMAs finished
+  uint64_t* p_full = s_free + SB;   // [PB] weights written (and O^T of the item before read)
+  uint64_t* p_free = p_full + PB;   // [PB] their MMAs are done (commit)
+  uint64_t* c_full = p_free + PB;   // [SC] the tile's scales landed
+  uint64_t* q_full = c_full + SC;   // [QB] an item's rows, factors and masks written
+  uint64_t* q_free = q_full + QB;   // [QB] its S^T computed (commit)
+  uint64_t* m_free = q_free + QB;   // [2] its rows, factors and masks read
+  uint64_t* drain = m_free + 2;     // [2] each issuer's last MMAs finished
   uint64_t* i_full = drain + 2;     // [kItemBufs] item written
   uint64_t* i_free = i_full + kItemBufs;  // [kItemBufs] read by every warp
   uint64_t* ticket = i_free + kItemBufs;  // the answer landed
@@ -519,19 +529,23 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     for (int b = 0; b < SB; ++b) {
       mbar_init(&s_full[b], 1);
       mbar_init(&s_free[b], 4 * L::KG);  // a lane of each key warp arrives
+    }
+    for (int b = 0; b < PB; ++b) {
       mbar_init(&p_full[b], 4 * L::KG);
       mbar_init(&p_free[b], 1);
     }
     for (int b = 0; b < SC; ++b) mbar_init(&c_full[b], 32);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < QB; ++b) {
       mbar_init(&q_full[b], L::kQWarps);
-      mbar_init(&q_free[b], 4 * L::KG);
-      mbar_init(&o_free[b], 4 * L::KG);
+      mbar_init(&q_free[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&m_free[b], 4 * L::KG);
       mbar_init(&drain[b], 1);
     }
     for (int b = 0; b < kItemBufs; ++b) {
       mbar_init(&i_full[b], 1);
-      mbar_init(&i_free[b], L::kWarps - 1);
+      mbar_init(&i_free[b], L::kReaders);
     }
     mbar_init(ticket, 1);
     fence_barrier_init();
@@ -548,8 +562,16 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
   const uint32_t tmem = *tmem_slot;
   ItemWalk walk{sItems, i_full, i_free, p.status};
   Item it;
+  // Two key warpgroups: 256 threads of 88 registers and 256 of 40, out of 512 of
+  // 64.  (Said in each branch: where they meet, the compiler counts on the least.)
+  auto few_registers = [] {
+    if constexpr (L::KG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+  };
 
-  if (warp == L::kItemWarp) {
+  if (warp > L::kReaders) {
+    few_registers();  // the idle warp
+  } else if (warp == L::kItemWarp) {
+    few_registers();
     // ------------------------------------------------------------ item warp
     // Starts with the CTA's own index and goes on with those of CTAs that have
     // not started, so that an SM whose items are short takes more of them.
@@ -594,6 +616,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     }
     __syncwarp();
   } else if (warp == L::kKWarp || warp == L::kVWarp) {
+    few_registers();
     // ----------------------------------------------------------- producers
     // Tile i covers keys [t_begin + 128 i, + 128): runs of B rows, one block
     // each, lane l copies run l.  The K warp brings the scales as well: lane l
@@ -649,75 +672,88 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       for (int i = kt > S ? kt - S : 0; i < kt; ++i) mbar_drain(&full[i % S], (i / S) & 1);
     __syncwarp();
   } else if (warp >= L::kQWarp) {
+    few_registers();
     // -------------------------------------------------------------- Q warps
     // Warp w brings its rows into shared memory as they are, then splits them:
     // a row lies in D / 8 lanes.  Rows past the item's are zeros.
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = NH / L::kQWarps;
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = NH / L::kQWarps,
+                  kRound = L::kRawRows / L::kQWarps;
     const int w = warp - L::kQWarp, c = lane % kLanes;
-    unsigned char* raw = smem + L::kQRaw + w * kMine * D * 2;
+    unsigned char* raw = smem + L::kQRaw + w * kRound * D * 2;
     while (walk.next(&it)) {
-      const int k_item = walk.n - 1, b = k_item & 1;
+      const int k_item = walk.n - 1, b = k_item % QB, mb = k_item & 1;
       const int my_row = min(lane, it.rows - 1);  // lane l knows row l
       const int my_out = output_row(p, it, my_row);
-      for (int r = lane / kLanes; r < kMine; r += kAtOnce) {
-        const int row = w * kMine + r;
-        const int from = __shfl_sync(0xffffffffu, my_out, row);
-        copy16_async(raw + (r * kLanes + c) * 16,
-                     static_cast<const T*>(p.q) + (size_t)from * D + c * 8,
-                     row < it.rows ? 16 : 0);
-      }
       unsigned long long mask = 0;
       if (p.tree_masks && w == 0)
         mask = (unsigned long long)__ldg(reinterpret_cast<const long long*>(p.tree_masks) +
                                          my_out / p.num_q_heads);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (k_item >= 2 && !mbar_wait_warp(&q_free[b], ((k_item - 2) >> 1) & 1, p.status)) break;
-      if (w == 0 && lane < NH) {
-        sRows[b * NH + lane] = my_out;
-        sMasks[b * NH + lane] = mask;
-      }
+      bool ok = true;
       unsigned char* dst = sQ + b * L::kQBytes;
 #pragma unroll 1
-      for (int r = lane / kLanes; r < kMine; r += kAtOnce) {
-        const uint4 x = *reinterpret_cast<const uint4*>(raw + (r * kLanes + c) * 16);
-        uint32_t top = max_magnitude(x);
-#pragma unroll
-        for (int mk = kLanes / 2; mk >= 1; mk >>= 1)
-          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, mk));
-        top = max(top & 0xffffu, top >> 16);
-        const bool finite = top < Magnitude<T>::kInf;
-        const int e = row_exponent(finite ? Magnitude<T>::value(top) : 0.f);
-        const float inv = finite ? pow2(-e) : 0.f;
-        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = Cvt<T>::to_float2(words[i]);
-          y[2 * i] = finite ? f.x * inv : 0.f;
-          y[2 * i + 1] = finite ? f.y * inv : 0.f;
+      for (int first = 0; first < kMine; first += kRound) {
+#pragma unroll 1
+        for (int r = lane / kLanes; r < kRound; r += kAtOnce) {
+          const int row = w * kMine + first + r;
+          const int from = __shfl_sync(0xffffffffu, my_out, row);
+          copy16_async(raw + (r * kLanes + c) * 16,
+                       static_cast<const T*>(p.q) + (size_t)from * D + c * 8,
+                       row < it.rows ? 16 : 0);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (first == 0) {
+          ok = (k_item < QB || mbar_wait_warp(&q_free[b], (k_item / QB - 1) & 1, p.status)) &&
+               (k_item < 2 || mbar_wait_warp(&m_free[mb], (k_item / 2 - 1) & 1, p.status));
+          if (!ok) break;
+        }
+#pragma unroll 1
+        for (int r = lane / kLanes; r < kRound; r += kAtOnce) {
+          const uint4 x = *reinterpret_cast<const uint4*>(raw + (r * kLanes + c) * 16);
+          uint32_t top = max_magnitude(x);
 #pragma unroll
-        for (int part = 0; part < L::kQParts; ++part) {
-          uint32_t codes[4];
+          for (int mk = kLanes / 2; mk >= 1; mk >>= 1)
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, mk));
+          top = max(top & 0xffffu, top >> 16);
+          const bool finite = top < Magnitude<T>::kInf;
+          const int e = row_exponent(finite ? Magnitude<T>::value(top) : 0.f);
+          const float inv = finite ? pow2(-e) : 0.f;
+          const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+          float y[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]),
-                                                __NV_SATFINITE, __NV_E4M3);
-            const float2 back = decode2(codes[i]);
-            y[2 * i] = (y[2 * i] - back.x) * 16.f;
-            y[2 * i + 1] = (y[2 * i + 1] - back.y) * 16.f;
+            const float2 f = Cvt<T>::to_float2(words[i]);
+            y[2 * i] = finite ? f.x * inv : 0.f;
+            y[2 * i + 1] = finite ? f.y * inv : 0.f;
           }
-          *reinterpret_cast<uint2*>(dst + swizzled<D>(part * NH + w * kMine + r, c * 8)) =
-              make_uint2(codes[0] | codes[1] << 16, codes[2] | codes[3] << 16);
+#pragma unroll
+          for (int part = 0; part < L::kQParts; ++part) {
+            uint32_t codes[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]),
+                                                  __NV_SATFINITE, __NV_E4M3);
+              const float2 back = decode2(codes[i]);
+              y[2 * i] = (y[2 * i] - back.x) * 16.f;
+              y[2 * i + 1] = (y[2 * i + 1] - back.y) * 16.f;
+            }
+            *reinterpret_cast<uint2*>(dst + swizzled<D>(part * NH + w * kMine + first + r, c * 8)) =
+                make_uint2(codes[0] | codes[1] << 16, codes[2] | codes[3] << 16);
+          }
+          if (c == 0)
+            sFactors[mb * NH + w * kMine + first + r] = finite ? p.qscale * pow2(e) : CUDART_NAN_F;
         }
-        if (c == 0)
-          sFactors[b * NH + w * kMine + r] = finite ? p.qscale * pow2(e) : CUDART_NAN_F;
+      }
+      if (!ok) break;
+      if (w == 0 && lane < NH) {
+        sRows[mb * NH + lane] = my_out;
+        sMasks[mb * NH + lane] = mask;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       arrive_warp(&q_full[b]);
     }
     __syncwarp();
   } else if (warp == L::kSWarp || warp == L::kOWarp) {
+    few_registers();
     // ------------------------------------------------------------ issuers
     const bool is_s = warp == L::kSWarp;
     const uint32_t idesc = is_s ? instr(false, L::NS, kKeys) : instr(true, L::NO, D);
@@ -726,9 +762,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     int kt = 0;
     bool ok = true;
     while (ok && walk.next(&it)) {
-      const int k_item = walk.n - 1, b = k_item & 1;
       if (is_s) {
-        if (!mbar_wait_warp(&q_full[b], (k_item >> 1) & 1, p.status)) break;
+        const int k_item = walk.n - 1, b = k_item % QB;
+        if (!mbar_wait_warp(&q_full[b], (k_item / QB) & 1, p.status)) break;
         for (int i = 0; i < it.n_tiles; ++i, ++kt) {
           const int st = kt % S;
           if (!mbar_wait_warp(&k_full[st], (kt / S) & 1, p.status) ||
@@ -747,12 +783,12 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           mma_commit_warp(&s_full[kt % SB]);
           mma_commit_warp(&k_empty[st]);
         }
+        if (ok) mma_commit_warp(&q_free[b]);
       } else {
-        if (k_item >= 2 && !mbar_wait_warp(&o_free[b], ((k_item - 2) >> 1) & 1, p.status)) break;
         for (int i = 0; i < it.n_tiles; ++i, ++kt) {
           const int st = kt % S;
           if (!mbar_wait_warp(&v_full[st], (kt / S) & 1, p.status) ||
-              !mbar_wait_warp(&p_full[kt % SB], (kt / SB) & 1, p.status)) {
+              !mbar_wait_warp(&p_full[kt % PB], (kt / PB) & 1, p.status)) {
             ok = false;
             break;
           }
@@ -762,11 +798,11 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           // bytes apart, groups 8 NO bytes apart.
 #pragma unroll
           for (int ks = 0; ks < kKeys / 32; ++ks)
-            mma_f8_warp(tmem + L::kColO + b * L::NO,
+            mma_f8_warp(tmem + L::kColO,
                         desc(aV + st * L::kTile + ks * 32 * D, 16, 8 * D, L::kSwizzle),
-                        desc(aP + (kt % SB) * L::kPBuf + ks * 32 * L::NO, 8 * L::NO, 128, 0),
+                        desc(aP + (kt % PB) * L::kPBuf + ks * 32 * L::NO, 8 * L::NO, 128, 0),
                         idesc, (i > 0 || ks > 0) ? 1u : 0u);
-          mma_commit_warp(&p_free[kt % SB]);
+          mma_commit_warp(&p_free[kt % PB]);
           mma_commit_warp(&v_empty[st]);
         }
       }
@@ -776,6 +812,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     mbar_drain(d, 0);
     __syncwarp();
   } else {
+    if constexpr (L::KG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // ----------------------------------------------------- key warpgroups
     // Code that runs once per item or seldom is kept short (loops that stay
     // loops): straight-line code met for the first time runs at the latency of
@@ -799,9 +836,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     for (;;) {
       const bool more = walk.next(&it);
       if (keys_any<L::KG>(!more)) break;  // the key warps leave together
-      const int k_item = walk.n - 1, ob = k_item & 1;
-      ok = ok && mbar_wait(&q_full[ob], (k_item >> 1) & 1, p.status);
-      const float* factors = sFactors + ob * NH + hb;
+      const int k_item = walk.n - 1, mb = k_item & 1;
+      ok = ok && mbar_wait(&q_full[k_item % QB], (k_item / QB) & 1, p.status);
+      const float* factors = sFactors + mb * NH + hb;
       // Rows past the item's get weights of zero by their reference.
       float nm = hb + row < it.rows ? -kNoRef : -CUDART_INF_F;
       if (lane < NHW) refs[row] = nm;
@@ -814,7 +851,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         const int nvalid = min(kKeys, it.t_end - key0);
         const bool valid = t < nvalid;
         const int sb = kt % SB;
-        const uint32_t s_phase = (kt / SB) & 1;
+        const uint32_t s_phase = (kt / SB) & 1, p_phase = (kt / PB) & 1;
+        const int pb = kt % PB;
         // A wait that gives up (never expected) leaves ok false; the loop runs
         // on without waiting, so that every named barrier stays matched, and
         // nothing it computes is stored.
@@ -854,7 +892,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           // codes are cleared below.
           const int rel = key0 + t - it.base;
           if (valid && rel >= 0) {
-            const unsigned long long* masks = sMasks + ob * NH + hb;
+            const unsigned long long* masks = sMasks + mb * NH + hb;
             uint32_t bits = 0;
 #pragma unroll 4
             for (int g = 0; g < NHW; ++g) bits |= (uint32_t)((masks[g] >> rel) & 1) << g;
@@ -863,16 +901,18 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           ok = ok && mbar_wait(&v_full[st], (kt / S) & 1, p.status);
           bool nan = false;
           uint4* v_row = reinterpret_cast<uint4*>(sV + st * L::kTile + t * D);
+          if (valid && rel >= 0) {
 #pragma unroll 2
-          for (int c = 0; c < D / 16; ++c) {
-            const uint4 w = v_row[c];
-            nan |= (__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                    __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                    __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                    __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0;
+            for (int c = 0; c < D / 16; ++c) {
+              const uint4 w = v_row[(c + t) % (D / 16)];  // (neighbours in different banks)
+              nan |= (__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                      __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                      __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                      __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0;
+            }
           }
           if constexpr (L::KG > 1) named_barrier_sync(1 + L::KG, 128 * L::KG);  // both have read
-          if (nan && valid) {
+          if (nan) {
             lvf = CUDART_NAN_F;
             if (kg == 0)
 #pragma unroll 2
@@ -911,7 +951,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           named_barrier_sync(1 + kg, 128);
           const float mt = fmax3(fmaxf(tops[row], tops[NHW + row]), tops[2 * NHW + row],
                                  tops[3 * NHW + row]);
-          const bool moves = mt + nm > kExceed;
+          const bool moves = mt + nm > kRaise;  // (all that have grown, now that some must)
           const float alpha = moves ? ex2(kRaise - mt - nm) : 1.f;
           if (moves) nm = kRaise - mt;
           if (lane < NHW) {
@@ -928,12 +968,12 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           if (i > 0 && moved) {
             // O^T holds this item's tiles so far: rescaled once their MMAs are
             // done (P buffer of the previous tile released).
-            ok = ok && mbar_wait(&p_free[(kt - 1) % SB], ((kt - 1) / SB) & 1, p.status);
+            ok = ok && mbar_wait(&p_free[(kt - 1) % PB], ((kt - 1) / PB) & 1, p.status);
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kParts; ++c) {
-              const uint32_t addr = tmem + L::kColO + ob * L::NO + c * NH + hb + lane_base;
+              const uint32_t addr = tmem + L::kColO + c * NH + hb + lane_base;
               float o[NHW];
               tmem_load_small<NHW>(addr, o);
 #pragma unroll
@@ -944,8 +984,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           }
         }
         // The weights of this key: rounded to fp16, then split in three.  The
-        // buffer was last read by the MMAs of tile kt - SB.
-        const bool p_here = kt < SB || mbar_test_wait(&p_free[sb], s_phase ^ 1);
+        // buffer was last read by the MMAs of tile kt - PB.
+        const bool p_here = kt < PB || mbar_test_wait(&p_free[pb], p_phase ^ 1);
         const Pair inv2 = pair(inv_v, inv_v);
         uint32_t h[NHW / 2];
 #pragma unroll
@@ -971,18 +1011,18 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
             }
           }
         }
-        if (!p_here) ok = ok && mbar_wait(&p_free[sb], s_phase ^ 1, p.status);
-        uint4* pb = reinterpret_cast<uint4*>(sP + sb * L::kPBuf + (t >> 3) * 8 * L::NO +
+        if (!p_here) ok = ok && mbar_wait(&p_free[pb], p_phase ^ 1, p.status);
+        uint4* to = reinterpret_cast<uint4*>(sP + pb * L::kPBuf + (t >> 3) * 8 * L::NO +
                                              (t & 7) * 16);
         if constexpr (NH == 4) {
-          pb[0] = make_uint4(part[0][0], part[1][0], part[2][0], 0u);
+          to[0] = make_uint4(part[0][0], part[1][0], part[2][0], 0u);
         } else if constexpr (NH == 8) {
-          pb[0] = make_uint4(part[0][0], part[0][1], part[1][0], part[1][1]);
-          pb[8] = make_uint4(part[2][0], part[2][1], 0u, 0u);
+          to[0] = make_uint4(part[0][0], part[0][1], part[1][0], part[1][1]);
+          to[8] = make_uint4(part[2][0], part[2][1], 0u, 0u);
         } else {
 #pragma unroll
           for (int c = 0; c < kParts; ++c)
-            pb[8 * ((c * NH + hb) / 16)] =
+            to[8 * ((c * NH + hb) / 16)] =
                 make_uint4(part[c][0], part[c][1], part[c][2], part[c][3]);
         }
         if (nvalid < kKeys && kg == 0) {
@@ -992,11 +1032,12 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           if (!valid) {
 #pragma unroll 2
             for (int c = 0; c < D / 16; ++c)
-              reinterpret_cast<uint4*>(sV + st * L::kTile + t * D)[c] = make_uint4(0, 0, 0, 0);
+              reinterpret_cast<uint4*>(sV + st * L::kTile + t * D)[(c + t) % (D / 16)] =
+                  make_uint4(0, 0, 0, 0);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        arrive_warp(&p_full[sb]);
+        arrive_warp(&p_full[pb]);
       }
 
       // Row sums over the 128 keys.
@@ -1012,22 +1053,23 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       if (lane % (32 / NHW) == 0) sums[(warp & 3) * NHW + lane / (32 / NHW)] = sum;
       named_barrier_sync(1 + kg, 128);
       const int last = kt - 1;
-      ok = ok && mbar_wait(&p_free[last % SB], (last / SB) & 1, p.status);
+      ok = ok && mbar_wait(&p_free[last % PB], (last / PB) & 1, p.status);
       __syncwarp();
       tc_fence_after();
-      const int* rows = sRows + ob * NH + hb;
+      const int* rows = sRows + mb * NH + hb;
       const int there = it.rows - hb;  // of this warpgroup's rows
+      const float l = (sums[row] + sums[NHW + row]) + (sums[2 * NHW + row] + sums[3 * NHW + row]);
+      if (lane < NHW) alphas[row] = l == 0.f ? 0.f : __fdividef(1.f, l);
+      __syncwarp();
 #pragma unroll 1
       for (int g = 0; g < NHW && g < there; g += 4) {
         Pair o[2];
-        load_parts<kParts, NH, 4, false>(tmem + L::kColO + ob * L::NO + hb + g + lane_base, o);
+        load_parts<kParts, NH, 4, false>(tmem + L::kColO + hb + g + lane_base, o);
         const float2 lo = both(o[0]), hi = both(o[1]);
         const float v[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float l = (sums[g + u] + sums[NHW + g + u]) +
-                          (sums[2 * NHW + g + u] + sums[3 * NHW + g + u]);
-          const float x = l == 0.f ? 0.f : __fdividef(v[u], l);
+          const float inv = alphas[g + u], x = inv == 0.f ? 0.f : v[u] * inv;
           if (!ok || !has_d || g + u >= there) continue;
           if (it.nparts_seq == 1)
             static_cast<T*>(p.out)[(size_t)rows[g + u] * D + d] = static_cast<T>(x);
@@ -1036,13 +1078,12 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         }
       }
       tc_fence_before();
-      arrive_warp(&o_free[ob]);
       if (ok && it.nparts_seq > 1 && t < NHW && t < there) {
         const size_t r = (size_t)rows[t] * p.num_parts + it.part;
         p.ws_m[r] = -nm;
-        p.ws_l[r] = (sums[t] + sums[NHW + t]) + (sums[2 * NHW + t] + sums[3 * NHW + t]);
+        p.ws_l[r] = l;
       }
-      arrive_warp(&q_free[ob]);  // the item's rows are read
+      arrive_warp(&m_free[mb]);  // the item's rows are read
     }
     grid_dep_launch_dependents();
   }
