@@ -262,15 +262,22 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t e5m2x2(uint32_t h2) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+// Four e5m2 codes of two packed pairs.
+__device__ __forceinline__ uint32_t e5m2x4(uint32_t lo, uint32_t hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 a, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 b, %2;\n\tmov.b32 %0, {a, b};\n\t}"
+      : "=r"(r)
+      : "r"(lo), "r"(hi));
   return r;
 }
 
-// h - codes (an e5m2 code is the upper byte of its fp16 value): exact.
+// h - the lower or upper two codes (a code is the upper byte of its fp16
+// value): exact.
+template <int UPPER>
 __device__ __forceinline__ uint32_t remainder_of(uint32_t h2, uint32_t codes) {
-  const uint32_t back = __byte_perm(codes, 0u, 0x1404);
+  const uint32_t back = __byte_perm(codes, 0u, UPPER ? 0x3424 : 0x1404);
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h2),
                             *reinterpret_cast<const __half2*>(&back));
   return *reinterpret_cast<const uint32_t*>(&d);
@@ -1003,11 +1010,10 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
         for (int g = 0; g < NHW / 4; ++g) {
 #pragma unroll
           for (int c = 0; c < kParts; ++c) {
-            const uint32_t lo = e5m2x2(h[2 * g]), hi = e5m2x2(h[2 * g + 1]);
-            part[c][g] = lo | hi << 16;
+            part[c][g] = e5m2x4(h[2 * g], h[2 * g + 1]);
             if (c + 1 < kParts) {
-              h[2 * g] = remainder_of(h[2 * g], lo);
-              h[2 * g + 1] = remainder_of(h[2 * g + 1], hi);
+              h[2 * g] = remainder_of<0>(h[2 * g], part[c][g]);
+              h[2 * g + 1] = remainder_of<1>(h[2 * g + 1], part[c][g]);
             }
           }
         }
