@@ -343,6 +343,36 @@ __device__ __forceinline__ int output_row(const AttnFp8Params& p, const Item& it
   return (it.query0 + j) * p.num_q_heads + it.kvh * p.group + (row - j * p.group);
 }
 
+// One arrival for what every lane of the warp has done.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tbar.warp.sync 0xffffffff;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar))
+      : "memory");
+}
+
+// mbar_wait_warp for the warps that mostly wait: they sleep up to a millisecond
+// at a time instead of taking issue slots from the key warps.
+__device__ __forceinline__ bool sleep_until(uint64_t* bar, uint32_t parity, unsigned int* status) {
+  unsigned long long t0 = 0;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (__all_sync(0xffffffffu, done)) return true;
+    const unsigned long long now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (__any_sync(0xffffffffu, now - t0 > kWaitLimitNs || timed_out(status))) {
+      atomicOr(status, PKV_DEV_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // The items a warp goes through, in the order the item warp hands them out.
 struct ItemWalk {
   const Item* items;
@@ -354,7 +384,7 @@ struct ItemWalk {
   // False after the last one, or when the wait gave up (the whole warp agrees).
   __device__ __forceinline__ bool next(Item* it) {
     const int b = n % kItemBufs;
-    if (!mbar_wait_warp(&full[b], (n / kItemBufs) & 1, status)) return false;
+    if (!sleep_until(&full[b], (n / kItemBufs) & 1, status)) return false;
     *it = items[b];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[b]);
@@ -472,12 +502,6 @@ __device__ __forceinline__ void copy8_async(void* dst, const void* src, int byte
                : "memory");
 }
 
-// One arrival for what every lane of the warp has done.
-__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
 // Sixteen bytes, or zeros where `bytes` is 0.
 __device__ __forceinline__ void copy16_async(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
@@ -593,7 +617,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
       it = item_at<NH>(p, j, lane == 0);
       if (it.n_tiles > 0) {
         const int b = n % kItemBufs;
-        ok = n < kItemBufs || mbar_wait_warp(&i_free[b], (n / kItemBufs - 1) & 1, p.status);
+        ok = n < kItemBufs || sleep_until(&i_free[b], (n / kItemBufs - 1) & 1, p.status);
         if (ok && lane == 0) {
           sItems[b] = it;
           mbar_arrive(&i_full[b]);
@@ -605,7 +629,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
           reinterpret_cast<uint4*>(p.out)[(size_t)output_row(p, it, i / kWords) * kWords +
                                           i % kWords] = make_uint4(0, 0, 0, 0);
       }
-      if (!mbar_wait_warp(ticket, asked & 1, p.status)) {
+      if (!sleep_until(ticket, asked & 1, p.status)) {
         mbar_drain(ticket, asked & 1);
         ok = false;
         break;
@@ -616,7 +640,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
       __syncwarp();
     }
     const int b = n % kItemBufs;
-    if (ok && (n < kItemBufs || mbar_wait_warp(&i_free[b], (n / kItemBufs - 1) & 1, p.status)) &&
+    if (ok && (n < kItemBufs || sleep_until(&i_free[b], (n / kItemBufs - 1) & 1, p.status)) &&
         lane == 0) {
       sItems[b].n_tiles = 0;  // the end
       mbar_arrive(&i_full[b]);
@@ -651,7 +675,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
           phys = 0;
         }
         if ((unsigned)phys4 >= (unsigned)p.num_blocks) phys4 = 0;
-        if (kt >= S && !mbar_wait_warp(&empty[st], ((kt / S) - 1) & 1, p.status)) {
+        if (kt >= S && !sleep_until(&empty[st], ((kt / S) - 1) & 1, p.status)) {
           ok = false;
           break;
         }
@@ -709,8 +733,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (first == 0) {
-          ok = (k_item < QB || mbar_wait_warp(&q_free[b], (k_item / QB - 1) & 1, p.status)) &&
-               (k_item < 2 || mbar_wait_warp(&m_free[mb], (k_item / 2 - 1) & 1, p.status));
+          ok = (k_item < QB || sleep_until(&q_free[b], (k_item / QB - 1) & 1, p.status)) &&
+               (k_item < 2 || sleep_until(&m_free[mb], (k_item / 2 - 1) & 1, p.status));
           if (!ok) break;
         }
 #pragma unroll 1
@@ -771,11 +795,11 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
     while (ok && walk.next(&it)) {
       if (is_s) {
         const int k_item = walk.n - 1, b = k_item % QB;
-        if (!mbar_wait_warp(&q_full[b], (k_item / QB) & 1, p.status)) break;
+        if (!sleep_until(&q_full[b], (k_item / QB) & 1, p.status)) break;
         for (int i = 0; i < it.n_tiles; ++i, ++kt) {
           const int st = kt % S;
-          if (!mbar_wait_warp(&k_full[st], (kt / S) & 1, p.status) ||
-              (kt >= SB && !mbar_wait_warp(&s_free[kt % SB], ((kt / SB) - 1) & 1, p.status))) {
+          if (!sleep_until(&k_full[st], (kt / S) & 1, p.status) ||
+              (kt >= SB && !sleep_until(&s_free[kt % SB], ((kt / SB) - 1) & 1, p.status))) {
             ok = false;
             break;
           }
@@ -794,8 +818,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
       } else {
         for (int i = 0; i < it.n_tiles; ++i, ++kt) {
           const int st = kt % S;
-          if (!mbar_wait_warp(&v_full[st], (kt / S) & 1, p.status) ||
-              !mbar_wait_warp(&p_full[kt % PB], (kt / PB) & 1, p.status)) {
+          if (!sleep_until(&v_full[st], (kt / S) & 1, p.status) ||
+              !sleep_until(&p_full[kt % PB], (kt / PB) & 1, p.status)) {
             ok = false;
             break;
           }
