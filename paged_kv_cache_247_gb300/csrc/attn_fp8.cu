@@ -16,16 +16,17 @@
 //   x          = scale log2(e) 2^e k_scale (s1 + s2 / 16 + s3 / 256)
 //   y          = x + log2 v_scale: the V row's scale is an addend of the base-2
 //                logit, and the running reference m is one of y, which is what
-//                gets rounded: p = 2^(y - m) < 2^15, to fp16, which is c1 + c2 +
-//                c3 in e5m2: what each part leaves of 11 bits fits the next
-//                (3 bits and twice 3 and the sign), down to steps of 2^-16
+//                gets rounded: p = 2^(y - m) <= 2^12, to fp16, which is c1 +
+//                c2 / 64 + c3 / 1024 in e5m2: what each part leaves of 11 bits
+//                fits the next (3 bits and twice 3 and the sign), down to fp16's
+//                own smallest step, 2^-24
 //   O^T        [D x parts * rows] += V codes^T . parts
 //   l          += p / v_scale
-//   out        = (o1 + o2 + o3) / l
+//   out        = (o1 + o2 / 64 + o3 / 1024) / l
 //
-// m moves when some y is 15 above it, to 8 below that y: what is lost of a
-// weight is at most 2^-25 of the largest, and the largest has room to grow by
-// 2^7 before m moves again, which costs about as much as a tile.
+// m moves when some y is 12 above it, to that y: what is lost of a weight is at
+// most 2^-25 of the largest, and the largest has room to grow by 2^12 before m
+// moves again, which costs about as much as a tile.
 //
 // Orientation, pipeline and roles follow the 16-bit decode kernel: keys are the
 // first product's M, the D dimensions the second's (D = 64: an M of 64, whose
@@ -65,8 +66,9 @@ constexpr int kKeys = kTileKeys;  // keys per tile
 constexpr int kParts = 3;         // e5m2 parts of a softmax weight
 constexpr int kBufs = 2;          // buffers of the weights
 constexpr int kItemBufs = 2;      // items handed out ahead
-constexpr float kRaise = 8.f;     // a moved reference lies this far below the tile's maximum
-constexpr float kExceed = 15.f;   // weights reach 2^15 (e5m2 and fp16 hold them) before it moves
+constexpr float kExceed = 12.f;   // weights reach 2^12 before the reference moves
+constexpr float kStep2 = 64.f;    // what a part of a weight leaves comes 64 and 16 times as
+constexpr float kStep3 = 16.f;    // large: at most 2^15, which e5m2 holds
 constexpr float kNoRef = -3e38f;  // the reference before any
 constexpr int kMinVExponent = -60;  // V rows below 448 * 2^-60 count as zero
 
@@ -81,8 +83,8 @@ struct Shape {
   static constexpr int KG = NH > 16 ? 2 : 1;     // key warpgroups
   static constexpr int NHW = NH / KG;            // rows per key warpgroup
   static constexpr int kQWarps = KG;
-  static constexpr int kQBufs = KG == 1 ? 2 : 1;                // items' parts of q held
-  static constexpr int SB = KG == 2 && kQParts == 3 ? 1 : 2;    // S^T buffers
+  static constexpr int kQBufs = KG == 2 && kQParts == 3 ? 1 : 2;  // items' parts of q held
+  static constexpr int SB = KG == 2 && kQParts == 3 ? 1 : 2;      // S^T buffers
   static constexpr int kKWarp = 4 * KG;
   static constexpr int kVWarp = kKWarp + 1;
   static constexpr int kSWarp = kKWarp + 2;  // owns tensor memory
@@ -96,11 +98,11 @@ struct Shape {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTile = kKeys * D;     // bytes of a K or V tile
   static constexpr int kQBytes = NS * D;
-  static constexpr int kRawRows = NH < 16 ? NH : 16;
+  static constexpr int kRawRows = KG == 2 ? (kQBufs == 2 ? 8 : 16) : NH;
   static constexpr int kRaw = kRawRows * D * 2;  // q rows as they are, some at a time
   static constexpr int kPBuf = kKeys * NO;
   // scales, an item's rows, reductions, items, barriers; alignment
-  static constexpr int kMaxStages = 384 / D;  // (no more fit beside two CTAs' other needs)
+  static constexpr int kMaxStages = (KG == 2 ? 256 : 384) / D;  // (no more fit beside two CTAs' other needs)
   static constexpr int kSmall = (kMaxStages + SB) * kKeys * 4 + 2 * NH * 16 + 4 * 4 * NH * 4 + 1024;
   static constexpr int kFixed = kQBufs * kQBytes + kRaw + kBufs * kPBuf + kSmall + 1024;
   static constexpr int kRoom = 113 * 1024;  // two CTAs per SM
@@ -193,49 +195,18 @@ __device__ __forceinline__ void tmem_wait(float* v) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-// Two floats that one instruction works on.
-struct Pair {
-  unsigned long long v;
-};
-
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 both(Pair a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-
 // Values 2 g and 2 g + 1 of an array at a 16-byte boundary, read four at a time.
 __device__ __forceinline__ Pair pair_at(const float* x, int g) {
   const float4 v = *reinterpret_cast<const float4*>(x + (g & ~1) * 2);
   return g & 1 ? pair(v.z, v.w) : pair(v.x, v.y);
 }
 
-// v = the sum over PARTS parts, part c in columns c * NH ..., weighted 16^-c
-// where they are scaled.
-template <int PARTS, int NH, int NHW, bool SCALED>
-__device__ __forceinline__ void load_parts(uint32_t taddr, Pair* v) {
+// v = the sum over PARTS parts, part c in columns c * NH ..., of part 0, part 1 /
+// step2 and part 2 / (step2 step3).
+template <int PARTS, int NH, int NHW>
+__device__ __forceinline__ void load_parts(uint32_t taddr, float step2, float step3, Pair* v) {
   constexpr int kOnce = NHW < 8 ? NHW : 8;  // more would not fit the registers
-  const Pair step = pair(0.0625f, 0.0625f);
+  const Pair by2 = pair(1.f / step2, 1.f / step2), by3 = pair(1.f / step3, 1.f / step3);
 #pragma unroll
   for (int first = 0; first < NHW; first += kOnce) {
     float part[PARTS * kOnce];
@@ -248,7 +219,7 @@ __device__ __forceinline__ void load_parts(uint32_t taddr, Pair* v) {
 #pragma unroll
       for (int c = PARTS - 2; c >= 0; --c) {
         const Pair next = pair(part[c * kOnce + 2 * g], part[c * kOnce + 2 * g + 1]);
-        x = SCALED ? fma2(x, step, next) : add2(x, next);
+        x = fma2(x, c == 1 ? by3 : by2, next);
       }
       v[first / 2 + g] = x;
     }
@@ -273,13 +244,14 @@ __device__ __forceinline__ uint32_t e5m2x4(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// h - the lower or upper two codes (a code is the upper byte of its fp16
-// value): exact.
+// step (h - the lower or upper two codes): exact (a code is the upper byte of its
+// fp16 value).
 template <int UPPER>
-__device__ __forceinline__ uint32_t remainder_of(uint32_t h2, uint32_t codes) {
+__device__ __forceinline__ uint32_t remainder_of(uint32_t h2, uint32_t codes, float step) {
   const uint32_t back = __byte_perm(codes, 0u, UPPER ? 0x3424 : 0x1404);
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h2),
-                            *reinterpret_cast<const __half2*>(&back));
+  const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h2),
+                                    *reinterpret_cast<const __half2*>(&back)),
+                            __float2half2_rn(step));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
@@ -315,10 +287,10 @@ __device__ __forceinline__ Item item_at(const AttnFp8Params& p, int j, bool repo
   Item it{};
   const int chunk = j % p.chunks;
   int r = j / p.chunks;
-  it.part = r % p.num_parts;
-  r /= p.num_parts;
   it.kvh = r % p.num_kv_heads;
-  it.s = r / p.num_kv_heads;
+  r /= p.num_kv_heads;
+  it.s = r % p.num_seqs;
+  it.part = r / p.num_seqs;  // last: a shorter last partition fills what is left
   const int raw = __ldg(p.context_lens + it.s);
   const long long cap = min((long long)p.max_context_len,
                             (long long)p.max_blocks_per_seq * p.block_size);
@@ -903,7 +875,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
         const float ks = scale_value(scales[0]);
         const uint32_t vbits = scales[kKeys];
         Pair y[NHW / 2];
-        load_parts<L::kQParts, NH, NHW, true>(tmem + sb * L::NS + hb + lane_base, y);
+        load_parts<L::kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, 16.f, 16.f, y);
         tc_fence_before();
         arrive_warp(&s_free[sb]);
 
@@ -982,9 +954,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
           named_barrier_sync(1 + kg, 128);
           const float mt = fmax3(fmaxf(tops[row], tops[NHW + row]), tops[2 * NHW + row],
                                  tops[3 * NHW + row]);
-          const bool moves = mt + nm > kRaise;  // (all that have grown, now that some must)
-          const float alpha = moves ? ex2(kRaise - mt - nm) : 1.f;
-          if (moves) nm = kRaise - mt;
+          const bool moves = mt + nm > 0.f;  // (all that have grown, now that some must)
+          const float alpha = moves ? ex2(-mt - nm) : 1.f;
+          if (moves) nm = -mt;
           if (lane < NHW) {
             refs[row] = nm;
             alphas[row] = alpha;
@@ -1036,8 +1008,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
           for (int c = 0; c < kParts; ++c) {
             part[c][g] = e5m2x4(h[2 * g], h[2 * g + 1]);
             if (c + 1 < kParts) {
-              h[2 * g] = remainder_of<0>(h[2 * g], part[c][g]);
-              h[2 * g + 1] = remainder_of<1>(h[2 * g + 1], part[c][g]);
+              h[2 * g] = remainder_of<0>(h[2 * g], part[c][g], c == 0 ? kStep2 : kStep3);
+              h[2 * g + 1] = remainder_of<1>(h[2 * g + 1], part[c][g], c == 0 ? kStep2 : kStep3);
             }
           }
         }
@@ -1091,15 +1063,15 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
       const float l = (sums[row] + sums[NHW + row]) + (sums[2 * NHW + row] + sums[3 * NHW + row]);
       if (lane < NHW) alphas[row] = l == 0.f ? 0.f : __fdividef(1.f, l);
       __syncwarp();
+      constexpr int kOut = NHW < 8 ? NHW : 8;
 #pragma unroll 1
-      for (int g = 0; g < NHW && g < there; g += 4) {
-        Pair o[2];
-        load_parts<kParts, NH, 4, false>(tmem + L::kColO + hb + g + lane_base, o);
-        const float2 lo = both(o[0]), hi = both(o[1]);
-        const float v[4] = {lo.x, lo.y, hi.x, hi.y};
+      for (int g = 0; g < NHW && g < there; g += kOut) {
+        Pair o[kOut / 2];
+        load_parts<kParts, NH, kOut>(tmem + L::kColO + hb + g + lane_base, kStep2, kStep3, o);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float inv = alphas[g + u], x = inv == 0.f ? 0.f : v[u] * inv;
+        for (int u = 0; u < kOut; ++u) {
+          const float2 v = both(o[u / 2]);
+          const float inv = alphas[g + u], x = inv == 0.f ? 0.f : (u & 1 ? v.y : v.x) * inv;
           if (!ok || !has_d || g + u >= there) continue;
           if (it.nparts_seq == 1)
             static_cast<T*>(p.out)[(size_t)rows[g + u] * D + d] = static_cast<T>(x);

@@ -92,49 +92,66 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Sixteen codes times the row's scale, rounded once to T (bf16 holds every
+// Eight codes times the row's scale, rounded once to T (bf16 holds every
 // product of a normal size exactly).
 template <typename T>
-__device__ __forceinline__ void widen(uint4 codes, float scale, uint4 out[2]) {
-  const uint32_t in[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t* o = reinterpret_cast<uint32_t*>(out);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = decode2(in[i]), b = decode2(in[i] >> 16);
-    o[2 * i] = Cvt<T>::from_float2(a.x * scale, a.y * scale);
-    o[2 * i + 1] = Cvt<T>::from_float2(b.x * scale, b.y * scale);
-  }
+__device__ __forceinline__ uint4 widen(uint2 codes, float scale) {
+  const float2 a = decode2(codes.x), b = decode2(codes.x >> 16), c = decode2(codes.y),
+               d = decode2(codes.y >> 16);
+  return make_uint4(Cvt<T>::from_float2(a.x * scale, a.y * scale),
+                    Cvt<T>::from_float2(b.x * scale, b.y * scale),
+                    Cvt<T>::from_float2(c.x * scale, c.y * scale),
+                    Cvt<T>::from_float2(d.x * scale, d.y * scale));
 }
 
-// The (pair, 16-element part of the block) pairs form one index space.
+__device__ __forceinline__ uint2 load_once2(const uint2* p) {
+  uint2 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(r.x), "=r"(r.y)
+               : "l"(p));
+  return r;
+}
+
+// The (pair, 16-element part of the block) pairs form one index space, two
+// threads to a part, so that a warp's 8-byte loads and 16-byte stores are
+// contiguous.  A thread takes kEach shares and has all their loads on the way
+// before the first is used.
+constexpr int kEach = 2;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     block_read_fp8_kernel(const ReadFp8Params p, unsigned total, unsigned block_parts) {
   grid_dep_wait();
   grid_dep_launch_dependents();
-  constexpr int kLanes = D / 16;
-  const unsigned i = blockIdx.x * (unsigned)kThreads + threadIdx.x;
-  if (i >= total) return;
-  const unsigned pair = i / block_parts, c = i - pair * block_parts;
-  const long long src = p.pairs[2ll * pair], dst = p.pairs[2ll * pair + 1];
-  if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_out_blocks) {
-    if (c == 0) atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
-    return;
+  constexpr int kParts = D / 16;  // of a row
+  const unsigned half = threadIdx.x % 2;
+  uint2 k[kEach], v[kEach];
+  uint16_t ks[kEach], vs[kEach];
+  long long to[kEach];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const unsigned i = (blockIdx.x * kEach + u) * (unsigned)(kThreads / 2) + threadIdx.x / 2;
+    to[u] = -1;
+    if (i >= total) continue;
+    const unsigned pair = i / block_parts, c = i - pair * block_parts;
+    const long long src = p.pairs[2ll * pair], dst = p.pairs[2ll * pair + 1];
+    if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_out_blocks) {
+      if (c == 0) atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
+      continue;
+    }
+    const long long from = src * block_parts + c;
+    to[u] = 2 * (dst * block_parts + c) + half;
+    k[u] = load_once2(reinterpret_cast<const uint2*>(p.k_cache) + 2 * from + half);
+    v[u] = load_once2(reinterpret_cast<const uint2*>(p.v_cache) + 2 * from + half);
+    ks[u] = p.k_scales[from / kParts];
+    vs[u] = p.v_scales[from / kParts];
   }
-  const long long from = src * block_parts + c, to = dst * block_parts + c;
-  const uint4 k = load_once(reinterpret_cast<const uint4*>(p.k_cache) + from);
-  const uint4 v = load_once(reinterpret_cast<const uint4*>(p.v_cache) + from);
-  const float ks = scale_value(p.k_scales[from / kLanes]);
-  const float vs = scale_value(p.v_scales[from / kLanes]);
-  uint4 o[2];
-  widen<T>(k, ks, o);
-  uint4* ko = reinterpret_cast<uint4*>(p.k_out) + 2 * to;
-  ko[0] = o[0];
-  ko[1] = o[1];
-  widen<T>(v, vs, o);
-  uint4* vo = reinterpret_cast<uint4*>(p.v_out) + 2 * to;
-  vo[0] = o[0];
-  vo[1] = o[1];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    if (to[u] < 0) continue;
+    reinterpret_cast<uint4*>(p.k_out)[to[u]] = widen<T>(k[u], scale_value(ks[u]));
+    reinterpret_cast<uint4*>(p.v_out)[to[u]] = widen<T>(v[u], scale_value(vs[u]));
+  }
 }
 
 template <typename T, int D>
@@ -149,9 +166,10 @@ template <typename T, int D>
 cudaError_t read_typed(const ReadFp8Params& p, long long num_pairs, cudaStream_t stream) {
   const long long parts = (long long)p.num_kv_heads * p.block_size * (D / 16);
   const long long total = num_pairs * parts;
+  constexpr int kPer = kThreads / 2 * kEach;
   return launch_overlapped(block_read_fp8_kernel<T, D>,
-                           dim3((unsigned)((total + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                           stream, p, (unsigned)total, (unsigned)parts);
+                           dim3((unsigned)((total + kPer - 1) / kPer)), dim3(kThreads), 0, stream,
+                           p, (unsigned)total, (unsigned)parts);
 }
 
 }  // namespace

@@ -23,36 +23,35 @@ constexpr int kTokens = 8;  // most tokens per CTA
 
 enum Layout { kInterleaved = 0, kHalf = 1, kHalfAny = 2 };
 
-// Plain loads (the outputs may be the inputs), not kept in L1.
-__device__ __forceinline__ uint4 load_once(const uint4* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
+__device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
+               : "memory");
 }
 
-__device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
-  const float x = a * cs.x - b * cs.y;
-  b = a * cs.y + b * cs.x;
-  a = x;
+__device__ __forceinline__ Pair rotated(Pair v, float2 cs) {
+  const float2 x = both(v);
+  return pair(x.x * cs.x - x.y * cs.y, x.x * cs.y + x.y * cs.x);
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack(uint4 w, float* f) {
+__device__ __forceinline__ void unpack(uint4 w, Pair* f) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 x = Cvt<T>::to_float2(u[j]);
-    f[2 * j] = x.x;
-    f[2 * j + 1] = x.y;
+    f[j] = pair(x.x, x.y);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 pack(const float* f) {
-  return make_uint4(Cvt<T>::from_float2(f[0], f[1]), Cvt<T>::from_float2(f[2], f[3]),
-                    Cvt<T>::from_float2(f[4], f[5]), Cvt<T>::from_float2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack(const Pair* f) {
+  uint32_t u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = both(f[j]);
+    u[j] = Cvt<T>::from_float2(x.x, x.y);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // A unit is two 16-byte chunks of a head row; D / 16 neighbouring threads hold
@@ -61,120 +60,180 @@ __device__ __forceinline__ uint4 pack(const float* f) {
 // can turn alone.  Halves that do not fill chunks (R not a multiple of 16) meet
 // in shared memory.  Each element is read and written by one thread, so the
 // outputs may be the inputs.
+//
+// The warps of a token go through its heads 512 / D at a time.  A thread's
+// pairs and dimensions are the same in every head, so their sines, cosines and
+// weights stay in registers.  The rows of the next turns are on their way into
+// shared memory, each thread's own chunks, so that nothing waits on other warps.
 template <typename T, int D, int LAYOUT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     qk_norm_rope_kernel(const NormRopeParams p, int num_tokens, int tokens_per_cta) {
   grid_dep_wait();
   grid_dep_launch_dependents();
-  constexpr int kUpr = D / 16;  // units per head row
+  constexpr int kUpr = D / 16;       // units per head row
+  constexpr int kHeads = 32 / kUpr;  // heads a warp works on at once
+  constexpr int kDepth = LAYOUT == kHalfAny ? 2 : 4;  // turns of heads on their way
   __shared__ float2 cs[kTokens][64];
-  __shared__ int padding[kTokens];
+  __shared__ uint4 stages[kDepth][2][kThreads];
   __shared__ float rows[LAYOUT == kHalfAny ? kThreads / kUpr : 1][D + 1];
   const int t0 = blockIdx.x * tokens_per_cta;
   const int n = min(tokens_per_cta, num_tokens - t0);
   const int pairs = p.rot_dim / 2;
+  // The first heads' rows are on their way while the angles are worked out.
+  const int warps = kThreads / 32 / tokens_per_cta;  // of each token
+  const int tok = (threadIdx.x >> 5) / warps, part = (threadIdx.x >> 5) % warps;
+  const int lane = threadIdx.x & 31;
+  const int turned = LAYOUT == kHalf ? p.rot_dim / 16 : 0;
+  const int w = lane % kUpr;
+  const int c0 = LAYOUT != kHalf || w < turned ? w : 2 * w;
+  const int c1 = LAYOUT != kHalf ? w + kUpr : (w < turned ? w + turned : 2 * w + 1);
+  const long long tt = t0 + tok;
+  const bool real = tok < n && p.positions[tt] >= 0;
+  // A turn of heads is of q or of k.
+  const int q_turns = (p.num_q_heads + kHeads - 1) / kHeads;
+  const int turns = q_turns + (p.num_kv_heads + kHeads - 1) / kHeads;
+  auto head_of = [&](int turn) {
+    return (turn < q_turns ? turn : turn - q_turns) * kHeads + lane / kUpr;
+  };
+  const T* q_row = static_cast<const T*>(p.q) + tt * p.q_stride;
+  const T* k_row = static_cast<const T*>(p.k) + tt * p.k_stride;
+  auto load = [&](int turn, int stage) {
+    const int h = head_of(turn);
+    const bool there =
+        real && turn < turns && h < (turn < q_turns ? p.num_q_heads : p.num_kv_heads);
+    if (there) {
+      const uint4* row = reinterpret_cast<const uint4*>((turn < q_turns ? q_row : k_row) +
+                                                        (long long)h * D);
+      copy_async(&stages[stage][0][threadIdx.x], row + c0);
+      copy_async(&stages[stage][1][threadIdx.x], row + c1);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) load(part + i * warps, i);
+
   for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
-    const int tok = i / pairs, pair = i - tok * pairs;
-    const int pos = p.positions[(long long)p.pair_axes[pair] * p.positions_stride + t0 + tok];
+    const int at = i / pairs, pair = i - at * pairs;
+    const int pos = p.positions[(long long)p.pair_axes[pair] * p.positions_stride + t0 + at];
     const double turns = (double)pos * (p.inv_freq[pair] * 0.15915494309189533577);
     float s, c;
     sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    cs[tok][pair] = make_float2(c * p.factor, s * p.factor);
+    cs[at][pair] = make_float2(c * p.factor, s * p.factor);
   }
-  if (threadIdx.x < n) padding[threadIdx.x] = p.positions[t0 + threadIdx.x] < 0;
   __syncthreads();
+  if (!real) return;  // (whole warps)
 
-  const int heads = p.num_q_heads + p.num_kv_heads;
-  const int units = heads * kUpr, total = n * units;
-  const int turned = LAYOUT == kHalf ? p.rot_dim / 16 : 0;
-  const int w = threadIdx.x % kUpr;
-  const int c0 = LAYOUT != kHalf || w < turned ? w : 2 * w;
-  const int c1 = LAYOUT != kHalf ? w + kUpr : (w < turned ? w + turned : 2 * w + 1);
-  for (int base = 0; base < total; base += kThreads) {
-    const int g = base + threadIdx.x;
-    const bool there = g < total;
-    const int t = there ? g / units : 0;
-    const int h = there ? (g - t * units) / kUpr : 0;
-    const bool is_q = h < p.num_q_heads;
-    const int hh = is_q ? h : h - p.num_q_heads;
-    const long long tt = t0 + t;
-    float x[8], y[8];
-    if (there) {
-      const T* row = static_cast<const T*>(is_q ? p.q : p.k) +
-                     tt * (is_q ? p.q_stride : p.k_stride) + (long long)hh * D;
-      unpack<T>(load_once(reinterpret_cast<const uint4*>(row) + c0), x);
-      unpack<T>(load_once(reinterpret_cast<const uint4*>(row) + c1), y);
-    } else {
+  const float2* a = cs[tok];
+  float2 mine[LAYOUT == kInterleaved ? 8 : 1];
+  Pair c2[4], s2[4], n2[4];  // cosines, sines and minus the sines of two pairs
+  if (LAYOUT == kInterleaved) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.f;
+    for (int j = 0; j < 8; ++j) mine[j] = a[j < 4 ? 4 * c0 + j : 4 * c1 + j - 4];
+  } else if (LAYOUT == kHalf) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 u = a[8 * w + 2 * j], v = a[8 * w + 2 * j + 1];
+      c2[j] = pair(u.x, v.x);
+      s2[j] = pair(u.y, v.y);
+      n2[j] = pair(-u.y, -v.y);
     }
-    const T* weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-    float sum = 0.f;
+  }
+  T* q_out = static_cast<T*>(p.q_out) + tt * p.q_out_stride;
+  T* k_out = static_cast<T*>(p.k_out) + tt * p.k_out_stride;
+  Pair wx[4], wy[4];  // the weights of this thread's dimensions, of q or of k
+  const T* weights = nullptr;
+  int stage = 0;
+  for (int turn = part; turn < turns; turn += warps) {
+    const bool is_q = turn < q_turns;
+    const int h = head_of(turn);
+    Pair x[4], y[4];
+    load(turn + (kDepth - 1) * warps, (stage + kDepth - 1) % kDepth);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    unpack<T>(stages[stage][0][threadIdx.x], x);
+    unpack<T>(stages[stage][1][threadIdx.x], y);
+    stage = (stage + 1) % kDepth;
+    const T* now = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+    if (now) {
+      if (now != weights) {
+        weights = now;
+        unpack<T>(__ldg(reinterpret_cast<const uint4*>(now) + c0), wx);
+        unpack<T>(__ldg(reinterpret_cast<const uint4*>(now) + c1), wy);
+      }
+      Pair sq = pair(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum += x[j] * x[j] + y[j] * y[j];
+      for (int j = 0; j < 4; ++j) sq = fma2(x[j], x[j], fma2(y[j], y[j], sq));
+      float sum = both(sq).x + both(sq).y;
 #pragma unroll
-    for (int mk = kUpr / 2; mk >= 1; mk >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mk);
-    if (weight) {
+      for (int mk = kUpr / 2; mk >= 1; mk >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mk);
       const float r = rsqrtf(sum * (1.f / D) + p.eps);
-      float wx[8], wy[8];
-      unpack<T>(__ldg(reinterpret_cast<const uint4*>(weight) + c0), wx);
-      unpack<T>(__ldg(reinterpret_cast<const uint4*>(weight) + c1), wy);
+      const Pair r2 = pair(r, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] *= r * wx[j];
-        y[j] *= r * wy[j];
+      for (int j = 0; j < 4; ++j) {
+        x[j] = mul2(x[j], mul2(r2, wx[j]));
+        y[j] = mul2(y[j], mul2(r2, wy[j]));
       }
     }
-    const float2* a = cs[t];
     if (LAYOUT == kInterleaved) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (4 * c0 + j < pairs) rotate(x[2 * j], x[2 * j + 1], a[4 * c0 + j]);
-        if (4 * c1 + j < pairs) rotate(y[2 * j], y[2 * j + 1], a[4 * c1 + j]);
+        if (4 * c0 + j < pairs) x[j] = rotated(x[j], mine[j]);
+        if (4 * c1 + j < pairs) y[j] = rotated(y[j], mine[4 + j]);
       }
     } else if (LAYOUT == kHalf) {
       if (w < turned) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) rotate(x[j], y[j], a[8 * w + j]);
+        for (int j = 0; j < 4; ++j) {  // as rotated() does it, two pairs at once
+          const Pair t = fma2(x[j], c2[j], mul2(y[j], n2[j]));
+          y[j] = fma2(x[j], s2[j], mul2(y[j], c2[j]));
+          x[j] = t;
+        }
       }
     } else {
       float* row = rows[threadIdx.x / kUpr];
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        row[8 * c0 + j] = x[j];
-        row[8 * c1 + j] = y[j];
+      for (int j = 0; j < 4; ++j) {
+        const float2 u = both(x[j]), v = both(y[j]);
+        row[8 * c0 + 2 * j] = u.x;
+        row[8 * c0 + 2 * j + 1] = u.y;
+        row[8 * c1 + 2 * j] = v.x;
+        row[8 * c1 + 2 * j + 1] = v.y;
       }
       __syncwarp();
-      auto turn = [&](float v, int i) {  // element i < R of its pair, the other from its owner
+      auto turned_at = [&](float v, int i) {  // the other element of the pair from its owner
+        if (i >= p.rot_dim) return v;
         const float2 c = a[i < pairs ? i : i - pairs];
         return i < pairs ? v * c.x - row[i + pairs] * c.y : row[i - pairs] * c.y + v * c.x;
       };
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (8 * c0 + j < p.rot_dim) x[j] = turn(x[j], 8 * c0 + j);
-        if (8 * c1 + j < p.rot_dim) y[j] = turn(y[j], 8 * c1 + j);
+      for (int j = 0; j < 4; ++j) {
+        const float2 u = both(x[j]), v = both(y[j]);
+        x[j] = pair(turned_at(u.x, 8 * c0 + 2 * j), turned_at(u.y, 8 * c0 + 2 * j + 1));
+        y[j] = pair(turned_at(v.x, 8 * c1 + 2 * j), turned_at(v.y, 8 * c1 + 2 * j + 1));
       }
     }
-    if (!there || padding[t]) continue;
-    T* out = static_cast<T*>(is_q ? p.q_out : p.k_out) +
-             tt * (is_q ? p.q_out_stride : p.k_out_stride) + (long long)hh * D;
-    reinterpret_cast<uint4*>(out)[c0] = pack<T>(x);
-    reinterpret_cast<uint4*>(out)[c1] = pack<T>(y);
+    if (h >= (is_q ? p.num_q_heads : p.num_kv_heads)) continue;
+    uint4* out = reinterpret_cast<uint4*>((is_q ? q_out : k_out) + (long long)h * D);
+    out[c0] = pack<T>(x);
+    out[c1] = pack<T>(y);
   }
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(const NormRopeParams& p, int num_tokens, cudaStream_t stream) {
-  const dim3 grid(num_tokens), block(kThreads);
+  // Eight tokens per CTA share its sines and cosines evenly; fewer where that
+  // would leave SMs without a CTA.
+  int tokens = kTokens;
+  while (tokens > 1 && num_tokens < 2 * 152 * tokens) tokens /= 2;
+  const dim3 grid((num_tokens + tokens - 1) / tokens), block(kThreads);
   if (p.interleaved)
     return launch_overlapped(qk_norm_rope_kernel<T, D, kInterleaved>, grid, block, 0, stream, p,
-                             num_tokens, 1);
+                             num_tokens, tokens);
   if (p.rot_dim % 16 == 0)
     return launch_overlapped(qk_norm_rope_kernel<T, D, kHalf>, grid, block, 0, stream, p,
-                             num_tokens, 1);
+                             num_tokens, tokens);
   return launch_overlapped(qk_norm_rope_kernel<T, D, kHalfAny>, grid, block, 0, stream, p,
-                           num_tokens, 1);
+                           num_tokens, tokens);
 }
 
 }  // namespace
