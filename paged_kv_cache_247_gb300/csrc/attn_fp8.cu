@@ -31,7 +31,7 @@
 // Orientation, pipeline and roles follow the 16-bit decode kernel: keys are the
 // first product's M, the D dimensions the second's (D = 64: an M of 64, whose
 // row i lies in tensor-memory lane 32 (i / 16) + i % 16).  A work item is
-// (sequence, KV head, partition of the context, up to 32 rows), a row being a
+// (sequence, KV head, partition of the context, up to 64 rows), a row being a
 // query head of the group and one of the sequence's queries.  One persistent CTA
 // per SM walks the items; its rings, barriers and tensor memory flow from item
 // to item.  Warps:
@@ -80,11 +80,13 @@ struct Shape {
   static constexpr int kQParts = std::is_same<T, __half>::value ? 3 : 2;
   static constexpr int NS = up16(kQParts * NH);  // columns of S^T
   static constexpr int NO = up16(kParts * NH);   // columns of O^T
-  static constexpr int KG = NH > 16 ? 2 : 1;     // key warpgroups
-  static constexpr int NHW = NH / KG;            // rows per key warpgroup
-  static constexpr int kQWarps = KG;
-  static constexpr int kQBufs = KG == 2 && kQParts == 3 ? 1 : 2;  // items' parts of q held
-  static constexpr int SB = KG == 2 && kQParts == 3 ? 1 : 2;      // S^T buffers
+  static constexpr int KG = NH > 16 ? NH / 16 : 1;  // key warpgroups
+  static constexpr int NHW = NH / KG;               // rows per key warpgroup
+  static constexpr int kPerSm = KG == 4 ? 1 : 2;    // CTAs per SM
+  static constexpr int kQWarps = KG == 1 ? 1 : 2;
+  // items' parts of q held, and buffers of S^T
+  static constexpr int kQBufs = KG == 2 && kQParts == 3 ? 1 : 2;
+  static constexpr int SB = KG >= 2 && kQParts == 3 ? 1 : 2;
   static constexpr int kKWarp = 4 * KG;
   static constexpr int kVWarp = kKWarp + 1;
   static constexpr int kSWarp = kKWarp + 2;  // owns tensor memory
@@ -92,20 +94,20 @@ struct Shape {
   static constexpr int kItemWarp = kKWarp + 4;
   static constexpr int kQWarp = kKWarp + 5;
   static constexpr int kReaders = kQWarp + kQWarps - 1;  // warps that read the items
-  // Two key warpgroups take most of the registers, which warpgroups give and
-  // take as a whole: one warp more, idle, fills the last.
-  static constexpr int kWarps = KG == 1 ? kQWarp + kQWarps : 16;
+  // Several key warpgroups take most of the registers, which warpgroups give
+  // and take as a whole: one warp more, idle, fills the last.
+  static constexpr int kWarps = KG == 1 ? kQWarp + kQWarps : 4 * KG + 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTile = kKeys * D;     // bytes of a K or V tile
   static constexpr int kQBytes = NS * D;
-  static constexpr int kRawRows = KG == 2 ? (kQBufs == 2 ? 8 : 16) : NH;
+  static constexpr int kRawRows = NH < 16 ? NH : (KG == 2 && kQBufs == 2 ? 8 : 16);
   static constexpr int kRaw = kRawRows * D * 2;  // q rows as they are, some at a time
   static constexpr int kPBuf = kKeys * NO;
   // scales, an item's rows, reductions, items, barriers; alignment
-  static constexpr int kMaxStages = (KG == 2 ? 256 : 384) / D;  // (no more fit beside two CTAs' other needs)
+  static constexpr int kMaxStages = (KG == 2 ? 256 : KG == 4 ? 512 : 384) / D;  // (no more fit)
   static constexpr int kSmall = (kMaxStages + SB) * kKeys * 4 + 2 * NH * 16 + 4 * 4 * NH * 4 + 1024;
   static constexpr int kFixed = kQBufs * kQBytes + kRaw + kBufs * kPBuf + kSmall + 1024;
-  static constexpr int kRoom = 113 * 1024;  // two CTAs per SM
+  static constexpr int kRoom = (kPerSm == 1 ? 227 : 113) * 1024;
   static constexpr int kFit = (kRoom - kFixed) / (2 * kTile);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kQ = 2 * kStages * kTile;  // after the K and V rings
@@ -134,7 +136,7 @@ struct Shape {
                 "shared memory overflow");
   static constexpr int kColO = SB * NS;
   static constexpr int kTmemCols = pow2_at_least(SB * NS + NO);
-  static_assert(kTmemCols <= 256, "tensor memory overflow");
+  static_assert(kTmemCols <= 512 / kPerSm, "tensor memory overflow");
   static constexpr int kSwizzle = D == 128 ? 2 : 4;  // descriptor code of the D-byte swizzle
 };
 
@@ -482,7 +484,7 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src, int byt
 }
 
 template <typename T, int NH, int D>
-__global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
+__global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kPerSm)
     attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap) {
   using L = Shape<T, NH, D>;
@@ -566,9 +568,10 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
   ItemWalk walk{sItems, i_full, i_free, p.status};
   Item it;
   // Two key warpgroups: 256 threads of 88 registers and 256 of 40, out of 512 of
-  // 64.  (Said in each branch: where they meet, the compiler counts on the least.)
+  // 64; four: 512 of 96 and 256 of 40, out of 768 of 80.  (Said in each branch:
+  // where they meet, the compiler counts on the least.)
   auto few_registers = [] {
-    if constexpr (L::KG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (L::KG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   };
 
   if (warp > L::kReaders) {
@@ -685,10 +688,10 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
     unsigned char* raw = smem + L::kQRaw + w * kRound * D * 2;
     while (walk.next(&it)) {
       const int k_item = walk.n - 1, b = k_item % QB, mb = k_item & 1;
-      const int my_row = min(lane, it.rows - 1);  // lane l knows row l
-      const int my_out = output_row(p, it, my_row);
+      const int my_row = w * kMine + lane;  // lane l knows the warp's row l
+      const int my_out = output_row(p, it, min(my_row, it.rows - 1));
       unsigned long long mask = 0;
-      if (p.tree_masks && w == 0)
+      if (p.tree_masks)
         mask = (unsigned long long)__ldg(reinterpret_cast<const long long*>(p.tree_masks) +
                                          my_out / p.num_q_heads);
       bool ok = true;
@@ -698,7 +701,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
 #pragma unroll 1
         for (int r = lane / kLanes; r < kRound; r += kAtOnce) {
           const int row = w * kMine + first + r;
-          const int from = __shfl_sync(0xffffffffu, my_out, row);
+          const int from = __shfl_sync(0xffffffffu, my_out, first + r);
           copy16_async(raw + (r * kLanes + c) * 16,
                        static_cast<const T*>(p.q) + (size_t)from * D + c * 8,
                        row < it.rows ? 16 : 0);
@@ -747,9 +750,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
         }
       }
       if (!ok) break;
-      if (w == 0 && lane < NH) {
-        sRows[mb * NH + lane] = my_out;
-        sMasks[mb * NH + lane] = mask;
+      if (lane < kMine) {
+        sRows[mb * NH + my_row] = my_out;
+        sMasks[mb * NH + my_row] = mask;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       arrive_warp(&q_full[b]);
@@ -816,6 +819,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
     __syncwarp();
   } else {
     if constexpr (L::KG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    if constexpr (L::KG == 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // ----------------------------------------------------- key warpgroups
     // Code that runs once per item or seldom is kept short (loops that stay
     // loops): straight-line code met for the first time runs at the latency of
@@ -842,6 +846,23 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, 2)
       const int k_item = walk.n - 1, mb = k_item & 1;
       ok = ok && mbar_wait(&q_full[k_item % QB], (k_item / QB) & 1, p.status);
       const float* factors = sFactors + mb * NH + hb;
+      if (L::KG > 1 && hb >= it.rows) {
+        // None of this warpgroup's rows is there: it only hands the buffers on.
+        // (What they hold for its rows comes to nothing that is stored.)
+        for (int i = 0; i < it.n_tiles; ++i, ++kt) {
+          const int sb = kt % SB, pb = kt % PB;
+          ok = ok && mbar_wait(&s_full[sb], (kt / SB) & 1, p.status);
+          arrive_warp(&s_free[sb]);
+          if (p.tree_masks != nullptr && min(it.t_begin + (i + 1) * kKeys, it.t_end) > it.base)
+            named_barrier_sync(1 + L::KG, 128 * L::KG);
+          if (kt >= PB) ok = ok && mbar_wait(&p_free[pb], ((kt / PB) & 1) ^ 1, p.status);
+          arrive_warp(&p_full[pb]);
+        }
+        sc = kt % SC;
+        sc_phase = (kt / SC) & 1;
+        arrive_warp(&m_free[mb]);
+        continue;
+      }
       // Rows past the item's get weights of zero by their reference.
       float nm = hb + row < it.rows ? -kNoRef : -CUDART_INF_F;
       if (lane < NHW) refs[row] = nm;
@@ -1197,12 +1218,13 @@ cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CU
 template <typename T, int D>
 cudaError_t launch_rows(const AttnFp8Params& p, const CUtensorMap& km, const CUtensorMap& vm,
                         cudaStream_t stream) {
-  static_assert(kFp8Rows == 32, "the instantiations cover items of up to 32 rows");
+  static_assert(kFp8Rows == 64, "the instantiations cover items of up to 64 rows");
   const int rows = p.max_query_len * p.group;
   if (rows <= 4) return launch_shape<T, 4, D>(p, km, vm, stream);
   if (rows <= 8) return launch_shape<T, 8, D>(p, km, vm, stream);
   if (rows <= 16) return launch_shape<T, 16, D>(p, km, vm, stream);
-  return launch_shape<T, 32, D>(p, km, vm, stream);
+  if (rows <= 32) return launch_shape<T, 32, D>(p, km, vm, stream);
+  return launch_shape<T, 64, D>(p, km, vm, stream);
 }
 
 }  // namespace

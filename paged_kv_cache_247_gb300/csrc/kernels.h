@@ -315,7 +315,7 @@ cudaError_t launch_qk_norm_rope(const NormRopeParams& p, int num_tokens, int hea
 // sequence, the whole context seen.  Otherwise the last positions of each
 // context are drafted tokens, seen as tree_masks says.
 constexpr int kMaxDrafts = 64;
-constexpr int kFp8Rows = 32;  // query rows (query, head of the group) a work item takes at most
+constexpr int kFp8Rows = 64;  // query rows (query, head of the group) a work item takes at most
 
 struct AttnFp8Params {
   void* out;      // [total_queries, Hq, D]
