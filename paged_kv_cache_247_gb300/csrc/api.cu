@@ -1025,6 +1025,44 @@ struct Fp8Plan {
   long long parts;
 };
 
+// Tiles per partition for `units` (sequence, KV head, chunk of rows) triples of
+// `rows` query rows each over contexts of `tiles` tiles: the split whose rounds of
+// items are done soonest on the CTAs the device holds (two per SM up to 32 rows,
+// else one).  An item costs its tiles and some more; a round that leaves CTAs out
+// is faster, down to `alone`; a split call pays for its partial outputs, written
+// and read again, and a launch.  Measured over all splits of a context (us, the
+// chosen one first): 4 x 8,192 positions, 8 heads of 64 rows, 16 tiles 43, 8 tiles
+// 51, 64 96; 1 x 32,768, 8 heads of 4 rows, 16 tiles 30, 64 57, 256 186; 32 x
+// 4,096, 8 heads of 64 rows, unsplit 108, 16 tiles 125; 64 x 8,192, 8 heads of 4
+// rows, unsplit 158, 32 tiles 171; 32 x 4,096, 4 heads of 16 rows, unsplit 45, 16
+// tiles 53.
+long long fp8_partition_tiles(double units, double rows, int head_dim, long long tiles) {
+  const bool wide = rows > 32;
+  const double slots = (wide ? 1.0 : 2.0) * device_sms();
+  const double alone = wide ? 0.75 : rows > 8 && rows <= 16 ? 0.45 : 0.6;
+  const double item = rows > 16 ? 2.5 : 1.0;
+  const double tile_us = head_dim == 128 ? 1.5 : (rows > 16 ? 1.2 : 0.8);
+  const double part_us = units * std::min(rows, (double)pkv::kFp8Rows) * head_dim * 8.0 / 6.8e6;
+  double best_cost = 0.0;
+  long long best = tiles;
+  // more than about three rounds of items never pays: the search stops there
+  const long long most = std::min(tiles, (long long)(3.0 * slots / units) + 1);
+  for (long long parts = 1; parts <= most; ++parts) {
+    const long long pt = (tiles + parts - 1) / parts;
+    if ((tiles + pt - 1) / pt != parts) continue;  // the same partition as fewer parts
+    const double items = units * (double)parts, rounds = floor(items / slots);
+    const double rest = items - rounds * slots;
+    const double cost = ((double)tiles / (double)parts + item) *
+                            (rounds + (rest > 0.0 ? fmax(rest / slots, alone) : 0.0)) +
+                        (parts > 1 ? (3.0 + (double)parts * part_us) / tile_us : 0.0);
+    if (parts == 1 || cost < best_cost) {
+      best_cost = cost;
+      best = pt;
+    }
+  }
+  return best;
+}
+
 // The split of a call over an 8-bit cache; false for sizes it does not take.
 bool fp8_plan(int total_queries, int max_query_len, int num_seqs, int num_q_heads,
               int num_kv_heads, int head_dim, int max_context_len, int partition_size,
@@ -1038,7 +1076,13 @@ bool fp8_plan(int total_queries, int max_query_len, int num_seqs, int num_q_head
   const long long units = chunks * num_kv_heads * std::max(num_seqs, 1);
   if (units > 0x7fffffffLL) return false;
   plan->chunks = (int)chunks;
-  plan->partition = partition_size ? partition_size : tc_partition(1, (int)units, max_context_len);
+  plan->partition = partition_size;
+  if (partition_size == 0) {
+    constexpr int kQuantum = pkv::kTcPartitionQuantum;
+    const long long tiles = std::max(1, (max_context_len + kQuantum - 1) / kQuantum);
+    plan->partition =
+        (int)(fp8_partition_tiles((double)units, (double)rows, head_dim, tiles) * kQuantum);
+  }
   plan->parts = num_parts_for(max_context_len, plan->partition);
   return plan->parts <= 0x7fffffffLL / units;
 }

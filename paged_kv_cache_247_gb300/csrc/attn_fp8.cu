@@ -72,6 +72,11 @@ constexpr float kStep3 = 16.f;    // large: at most 2^15, which e5m2 holds
 constexpr float kNoRef = -3e38f;  // the reference before any
 constexpr int kMinVExponent = -60;  // V rows below 448 * 2^-60 count as zero
 
+// Registers with several key warpgroups.  Two: 256 threads of 88 and 256 of 40, out
+// of 512 of 64; four: 512 of 96 and 256 of 40, out of 768 of 80.
+constexpr int kFewRegs = 40;
+constexpr int key_regs(int warpgroups) { return warpgroups == 2 ? 88 : 96; }
+
 constexpr int up16(int x) { return (x + 15) / 16 * 16; }
 constexpr int pow2_at_least(int x, int p = 32) { return p >= x ? p : pow2_at_least(x, 2 * p); }
 
@@ -292,7 +297,7 @@ __device__ __forceinline__ Item item_at(const AttnFp8Params& p, int j, bool repo
   it.kvh = r % p.num_kv_heads;
   r /= p.num_kv_heads;
   it.s = r % p.num_seqs;
-  it.part = r / p.num_seqs;  // last: a shorter last partition fills what is left
+  it.part = r / p.num_seqs;  // last: the shorter last partitions fill what is left
   const int raw = __ldg(p.context_lens + it.s);
   const long long cap = min((long long)p.max_context_len,
                             (long long)p.max_blocks_per_seq * p.block_size);
@@ -325,22 +330,14 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
       : "memory");
 }
 
-// mbar_wait_warp for the warps that mostly wait: they sleep up to a millisecond
-// at a time instead of taking issue slots from the key warps.
-__device__ __forceinline__ bool sleep_until(uint64_t* bar, uint32_t parity, unsigned int* status) {
-  unsigned long long t0 = 0;
-  for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    if (__all_sync(0xffffffffu, done)) return true;
-    const unsigned long long now = global_ns();
-    if (t0 == 0) t0 = now;
-    if (__any_sync(0xffffffffu, now - t0 > kWaitLimitNs || timed_out(status))) {
+// mbar_wait_warp that looks at the clock and the status only now and then.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, unsigned int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = global_ns();
+  for (uint32_t asked = 1;; ++asked) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (asked % 64 == 0 &&
+        __any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs || timed_out(status))) {
       atomicOr(status, PKV_DEV_WAIT_TIMEOUT);
       return false;
     }
@@ -358,7 +355,7 @@ struct ItemWalk {
   // False after the last one, or when the wait gave up (the whole warp agrees).
   __device__ __forceinline__ bool next(Item* it) {
     const int b = n % kItemBufs;
-    if (!sleep_until(&full[b], (n / kItemBufs) & 1, status)) return false;
+    if (!wait_warp(&full[b], (n / kItemBufs) & 1, status)) return false;
     *it = items[b];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[b]);
@@ -567,11 +564,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
   const uint32_t tmem = *tmem_slot;
   ItemWalk walk{sItems, i_full, i_free, p.status};
   Item it;
-  // Two key warpgroups: 256 threads of 88 registers and 256 of 40, out of 512 of
-  // 64; four: 512 of 96 and 256 of 40, out of 768 of 80.  (Said in each branch:
-  // where they meet, the compiler counts on the least.)
+  // (Said in each branch: where they meet, the compiler counts on the least.)
   auto few_registers = [] {
-    if constexpr (L::KG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (L::KG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
   };
 
   if (warp > L::kReaders) {
@@ -592,7 +587,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       it = item_at<NH>(p, j, lane == 0);
       if (it.n_tiles > 0) {
         const int b = n % kItemBufs;
-        ok = n < kItemBufs || sleep_until(&i_free[b], (n / kItemBufs - 1) & 1, p.status);
+        ok = n < kItemBufs || wait_warp(&i_free[b], (n / kItemBufs - 1) & 1, p.status);
         if (ok && lane == 0) {
           sItems[b] = it;
           mbar_arrive(&i_full[b]);
@@ -604,7 +599,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           reinterpret_cast<uint4*>(p.out)[(size_t)output_row(p, it, i / kWords) * kWords +
                                           i % kWords] = make_uint4(0, 0, 0, 0);
       }
-      if (!sleep_until(ticket, asked & 1, p.status)) {
+      if (!wait_warp(ticket, asked & 1, p.status)) {
         mbar_drain(ticket, asked & 1);
         ok = false;
         break;
@@ -615,7 +610,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       __syncwarp();
     }
     const int b = n % kItemBufs;
-    if (ok && (n < kItemBufs || sleep_until(&i_free[b], (n / kItemBufs - 1) & 1, p.status)) &&
+    if (ok && (n < kItemBufs || wait_warp(&i_free[b], (n / kItemBufs - 1) & 1, p.status)) &&
         lane == 0) {
       sItems[b].n_tiles = 0;  // the end
       mbar_arrive(&i_full[b]);
@@ -650,7 +645,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
           phys = 0;
         }
         if ((unsigned)phys4 >= (unsigned)p.num_blocks) phys4 = 0;
-        if (kt >= S && !sleep_until(&empty[st], ((kt / S) - 1) & 1, p.status)) {
+        if (kt >= S && !wait_warp(&empty[st], ((kt / S) - 1) & 1, p.status)) {
           ok = false;
           break;
         }
@@ -708,8 +703,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (first == 0) {
-          ok = (k_item < QB || sleep_until(&q_free[b], (k_item / QB - 1) & 1, p.status)) &&
-               (k_item < 2 || sleep_until(&m_free[mb], (k_item / 2 - 1) & 1, p.status));
+          ok = (k_item < QB || wait_warp(&q_free[b], (k_item / QB - 1) & 1, p.status)) &&
+               (k_item < 2 || wait_warp(&m_free[mb], (k_item / 2 - 1) & 1, p.status));
           if (!ok) break;
         }
 #pragma unroll 1
@@ -770,11 +765,11 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     while (ok && walk.next(&it)) {
       if (is_s) {
         const int k_item = walk.n - 1, b = k_item % QB;
-        if (!sleep_until(&q_full[b], (k_item / QB) & 1, p.status)) break;
+        if (!wait_warp(&q_full[b], (k_item / QB) & 1, p.status)) break;
         for (int i = 0; i < it.n_tiles; ++i, ++kt) {
           const int st = kt % S;
-          if (!sleep_until(&k_full[st], (kt / S) & 1, p.status) ||
-              (kt >= SB && !sleep_until(&s_free[kt % SB], ((kt / SB) - 1) & 1, p.status))) {
+          if (!wait_warp(&k_full[st], (kt / S) & 1, p.status) ||
+              (kt >= SB && !wait_warp(&s_free[kt % SB], ((kt / SB) - 1) & 1, p.status))) {
             ok = false;
             break;
           }
@@ -793,8 +788,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       } else {
         for (int i = 0; i < it.n_tiles; ++i, ++kt) {
           const int st = kt % S;
-          if (!sleep_until(&v_full[st], (kt / S) & 1, p.status) ||
-              !sleep_until(&p_full[kt % PB], (kt / PB) & 1, p.status)) {
+          if (!wait_warp(&v_full[st], (kt / S) & 1, p.status) ||
+              !wait_warp(&p_full[kt % PB], (kt / PB) & 1, p.status)) {
             ok = false;
             break;
           }
@@ -818,8 +813,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     mbar_drain(d, 0);
     __syncwarp();
   } else {
-    if constexpr (L::KG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
-    if constexpr (L::KG == 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    if constexpr (L::KG > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(key_regs(L::KG)));
     // ----------------------------------------------------- key warpgroups
     // Code that runs once per item or seldom is kept short (loops that stay
     // loops): straight-line code met for the first time runs at the latency of
@@ -1009,7 +1003,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         }
         // The weights of this key: rounded to fp16, then split in three.  The
         // buffer was last read by the MMAs of tile kt - PB.
-        const bool p_here = kt < PB || mbar_test_wait(&p_free[pb], p_phase ^ 1);
+        // (Nothing to wait for in the first PB: their phase before the first counts
+        // as completed.)
+        const bool p_here = mbar_test_wait(&p_free[pb], p_phase ^ 1);
         const Pair inv2 = pair(inv_v, inv_v);
         uint32_t h[NHW / 2];
 #pragma unroll
@@ -1132,12 +1128,26 @@ __global__ void __launch_bounds__(128) attn_fp8_reduce_kernel(const AttnFp8Param
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (row >= (long long)p.total_queries * p.num_q_heads) return;
   const int query = (int)(row / p.num_q_heads);
+  const float* mrow = p.ws_m + row * p.num_parts;
+  const float* lrow = p.ws_l + row * p.num_parts;
+  const float* orow = p.ws_o + row * p.num_parts * D + lane * E;
+  // On their way while the sequence is looked for; of partitions that are none
+  // they are not used.
+  float m0 = -CUDART_INF_F, l0 = 0.f;
+  if (lane < p.num_parts) {
+    m0 = __ldcg(mrow + lane);
+    l0 = __ldcg(lrow + lane);
+  }
   int s = query;
   if (p.query_start) {  // the last sequence that starts at or before the query
-    int lo = 0, hi = p.num_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (__ldg(p.query_start + mid) <= query) lo = mid; else hi = mid;
+    int lo = 0, n = p.num_seqs;
+    while (n > 1) {  // 32 of the candidates at a time
+      const int step = (n + 31) / 32;
+      const int i = lo + lane * step;
+      const bool before = lane * step < n && __ldg(p.query_start + i) <= query;
+      const int k = max(31 - __clz(__ballot_sync(0xffffffffu, before)), 0);
+      lo += k * step;
+      n = min(step, n - k * step);
     }
     s = lo;
   }
@@ -1151,23 +1161,30 @@ __global__ void __launch_bounds__(128) attn_fp8_reduce_kernel(const AttnFp8Param
   if (query < it.query0 || query >= it.query0 + it.queries) return;
   const int np = context_partitions(ctx, p.partition_size);
   if (np <= 1) return;  // written by the attention kernel
-  const float* mrow = p.ws_m + row * p.num_parts;
-  const float* lrow = p.ws_l + row * p.num_parts;
-  const float* orow = p.ws_o + row * p.num_parts * D + lane * E;
-  float M = -CUDART_INF_F;
-  for (int i = lane; i < np; i += 32) M = fmaxf(M, mrow[i]);
-#pragma unroll
-  for (int mk = 16; mk >= 1; mk >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, mk));
+  float M = lane < np ? m0 : -CUDART_INF_F;
+  for (int i = lane + 32; i < np; i += 32) M = fmaxf(M, __ldcg(mrow + i));
+  M = warp_max(M);
   float sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int base = 0; base < np; base += 32) {
+    const int i = base + lane;
+    const float l = base == 0 ? l0 : (i < np ? __ldcg(lrow + i) : 0.f);
+    const float m = base == 0 ? m0 : (i < np ? __ldcg(mrow + i) : 0.f);
+    const float mine = i >= np || l == 0.f ? 0.f : l * exp2f(m - M);
+    const int n = min(32, np - base);
 #pragma unroll 4
-  for (int i = 0; i < np; ++i) {
-    const float l = lrow[i];
-    const float w = l == 0.f ? 0.f : l * exp2f(mrow[i] - M);
-    sum += w;
+    for (int k = 0; k < n; ++k) {
+      const float w = __shfl_sync(0xffffffffu, mine, k);
+      sum += w;
+      const float2* o = reinterpret_cast<const float2*>(orow + (size_t)(base + k) * D);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, orow[(size_t)i * D + e], acc[e]);
+      for (int e = 0; e < E / 2; ++e) {
+        const float2 v = __ldcg(o + e);
+        acc[2 * e] = fmaf(w, v.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(w, v.y, acc[2 * e + 1]);
+      }
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * E);
@@ -1204,6 +1221,15 @@ cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CU
     err = cudaFuncSetAttribute(attn_fp8_kernel<T, NH, D>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
     if (err != cudaSuccess) return err;
+    if constexpr (L::KG > 1) {  // the warpgroups' shares come out of what the launch gives
+      cudaFuncAttributes attr;
+      err = cudaFuncGetAttributes(&attr, attn_fp8_kernel<T, NH, D>);
+      if (err != cudaSuccess) return err;
+      if (attr.numRegs < kFewRegs ||
+          (attr.numRegs + 7) / 8 * 8 * L::kThreads <
+              128 * L::KG * key_regs(L::KG) + (L::kThreads - 128 * L::KG) * kFewRegs)
+        return cudaErrorInvalidConfiguration;
+    }
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
   const int items = p.num_seqs * p.num_kv_heads * p.num_parts * p.chunks;
