@@ -65,7 +65,7 @@ using namespace tc;
 constexpr int kKeys = kTileKeys;  // keys per tile
 constexpr int kParts = 3;         // e5m2 parts of a softmax weight
 constexpr int kBufs = 2;          // buffers of the weights
-constexpr int kItemBufs = 2;      // items handed out ahead
+constexpr int kItemBufs = 1;      // items handed out ahead (2 and 4: 64 short requests 1 and 4 us slower)
 constexpr float kExceed = 12.f;   // weights reach 2^12 before the reference moves
 constexpr float kStep2 = 64.f;    // what a part of a weight leaves comes 64 and 16 times as
 constexpr float kStep3 = 16.f;    // large: at most 2^15, which e5m2 holds
@@ -89,6 +89,7 @@ struct Shape {
   static constexpr int NHW = NH / KG;               // rows per key warpgroup
   static constexpr int kPerSm = KG == 4 ? 1 : 2;    // CTAs per SM
   static constexpr int kQWarps = KG == 1 ? 1 : 2;
+  static constexpr bool kKeysSplit = KG > 1;        // the first item's rows: see there
   // items' parts of q held, and buffers of S^T
   static constexpr int kQBufs = KG == 2 && kQParts == 3 ? 1 : 2;
   static constexpr int SB = KG >= 2 && kQParts == 3 ? 1 : 2;
@@ -134,7 +135,7 @@ struct Shape {
   static constexpr int kTicket = kItems + kItemBufs * 64;
   static constexpr int kBar = kTicket + 16;
   static constexpr int kBars =
-      4 * kStages + 2 * SB + 2 * kBufs + kScaleStages + 2 * kQBufs + 4 + 2 * kItemBufs + 1;
+      4 * kStages + 2 * SB + 2 * kBufs + kScaleStages + 2 * kQBufs + 4 + 2 * kItemBufs + 2;
   static constexpr int kTmemSlot = kBar + kBars * 8;
   static constexpr int kBytes = kTmemSlot + 16 + 1024;
   static_assert(kItemBufs * 64 + kBars * 8 + 32 <= 1024 && kBytes <= kRoom && kStages >= 2,
@@ -480,6 +481,47 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src, int byt
                : "memory");
 }
 
+// The e4m3 parts of a query row that D / 8 neighbouring lanes hold, lane c its
+// elements 8 c ..., as row `row` of each part in shared memory; returns the power
+// of two that they are to be multiplied with (NaN for a row with a NaN or an
+// infinity).
+template <typename T, int NH, int D, int PARTS>
+__device__ __forceinline__ float split_row(uint4 x, int row, int c, unsigned char* dst) {
+  constexpr int kLanes = D / 8;
+  uint32_t top = max_magnitude(x);
+#pragma unroll
+  for (int mk = kLanes / 2; mk >= 1; mk >>= 1)
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, mk));
+  top = max(top & 0xffffu, top >> 16);
+  const bool finite = top < Magnitude<T>::kInf;
+  const int e = row_exponent(finite ? Magnitude<T>::value(top) : 0.f);
+  const float inv = finite ? pow2(-e) : 0.f;
+  const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Cvt<T>::to_float2(words[i]);
+    y[2 * i] = finite ? f.x * inv : 0.f;
+    y[2 * i + 1] = finite ? f.y * inv : 0.f;
+  }
+#pragma unroll
+  for (int part = 0; part < PARTS; ++part) {
+    uint32_t codes[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_SATFINITE,
+                                          __NV_E4M3);
+      const float2 back = decode2(codes[i]);
+      y[2 * i] = (y[2 * i] - back.x) * 16.f;
+      y[2 * i + 1] = (y[2 * i + 1] - back.y) * 16.f;
+    }
+    if (row < NH)
+      *reinterpret_cast<uint2*>(dst + swizzled<D>(part * NH + row, c * 8)) =
+          make_uint2(codes[0] | codes[1] << 16, codes[2] | codes[3] << 16);
+  }
+  return finite ? pow2(e) : CUDART_NAN_F;
+}
+
 template <typename T, int NH, int D>
 __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kPerSm)
     attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
@@ -516,6 +558,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
   uint64_t* i_full = drain + 2;     // [kItemBufs] item written
   uint64_t* i_free = i_full + kItemBufs;  // [kItemBufs] read by every warp
   uint64_t* ticket = i_free + kItemBufs;  // the answer landed
+  uint64_t* q_first = ticket + 1;         // q_full of the first item
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
 
   const int warp = threadIdx.x >> 5;
@@ -550,6 +593,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       mbar_init(&i_free[b], L::kReaders);
     }
     mbar_init(ticket, 1);
+    mbar_init(q_first, 4 * L::KG);
     fence_barrier_init();
   }
   if (warp == L::kSWarp) {
@@ -676,13 +720,16 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     few_registers();
     // -------------------------------------------------------------- Q warps
     // Warp w brings its rows into shared memory as they are, then splits them:
-    // a row lies in D / 8 lanes.  Rows past the item's are zeros.
+    // a row lies in D / 8 lanes.  Rows past the item's are zeros.  With many rows
+    // the first item, which nothing hides, is split by all the key warps (8
+    // sequences with trees of 64 over groups of three 64 -> 60 us).
     constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = NH / L::kQWarps,
                   kRound = L::kRawRows / L::kQWarps;
     const int w = warp - L::kQWarp, c = lane % kLanes;
     unsigned char* raw = smem + L::kQRaw + w * kRound * D * 2;
     while (walk.next(&it)) {
       const int k_item = walk.n - 1, b = k_item % QB, mb = k_item & 1;
+      if (L::kKeysSplit && k_item == 0) continue;  // the key warps' own
       const int my_row = w * kMine + lane;  // lane l knows the warp's row l
       const int my_out = output_row(p, it, min(my_row, it.rows - 1));
       unsigned long long mask = 0;
@@ -710,38 +757,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
 #pragma unroll 1
         for (int r = lane / kLanes; r < kRound; r += kAtOnce) {
           const uint4 x = *reinterpret_cast<const uint4*>(raw + (r * kLanes + c) * 16);
-          uint32_t top = max_magnitude(x);
-#pragma unroll
-          for (int mk = kLanes / 2; mk >= 1; mk >>= 1)
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, mk));
-          top = max(top & 0xffffu, top >> 16);
-          const bool finite = top < Magnitude<T>::kInf;
-          const int e = row_exponent(finite ? Magnitude<T>::value(top) : 0.f);
-          const float inv = finite ? pow2(-e) : 0.f;
-          const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-          float y[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = Cvt<T>::to_float2(words[i]);
-            y[2 * i] = finite ? f.x * inv : 0.f;
-            y[2 * i + 1] = finite ? f.y * inv : 0.f;
-          }
-#pragma unroll
-          for (int part = 0; part < L::kQParts; ++part) {
-            uint32_t codes[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]),
-                                                  __NV_SATFINITE, __NV_E4M3);
-              const float2 back = decode2(codes[i]);
-              y[2 * i] = (y[2 * i] - back.x) * 16.f;
-              y[2 * i + 1] = (y[2 * i + 1] - back.y) * 16.f;
-            }
-            *reinterpret_cast<uint2*>(dst + swizzled<D>(part * NH + w * kMine + first + r, c * 8)) =
-                make_uint2(codes[0] | codes[1] << 16, codes[2] | codes[3] << 16);
-          }
-          if (c == 0)
-            sFactors[mb * NH + w * kMine + first + r] = finite ? p.qscale * pow2(e) : CUDART_NAN_F;
+          const int row = w * kMine + first + r;
+          const float factor = split_row<T, NH, D, L::kQParts>(x, row, c, dst);
+          if (c == 0) sFactors[mb * NH + row] = p.qscale * factor;
         }
       }
       if (!ok) break;
@@ -765,7 +783,9 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
     while (ok && walk.next(&it)) {
       if (is_s) {
         const int k_item = walk.n - 1, b = k_item % QB;
-        if (!wait_warp(&q_full[b], (k_item / QB) & 1, p.status)) break;
+        const bool own = L::kKeysSplit && k_item == 0;
+        const int filled = own ? 0 : k_item / QB - (L::kKeysSplit && b == 0);
+        if (!wait_warp(own ? q_first : &q_full[b], filled & 1, p.status)) break;
         for (int i = 0; i < it.n_tiles; ++i, ++kt) {
           const int st = kt % S;
           if (!wait_warp(&k_full[st], (kt / S) & 1, p.status) ||
@@ -838,7 +858,35 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       const bool more = walk.next(&it);
       if (keys_any<L::KG>(!more)) break;  // the key warps leave together
       const int k_item = walk.n - 1, mb = k_item & 1;
-      ok = ok && mbar_wait(&q_full[k_item % QB], (k_item / QB) & 1, p.status);
+      if (L::kKeysSplit && k_item == 0) {
+        // Each key warp splits its share of the rows, one or two at a time.
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kShare = NHW / 4;
+        const int c = lane % kLanes;
+#pragma unroll 1
+        for (int r = lane / kLanes; r - lane / kLanes < kShare; r += kAtOnce) {
+          const int q_row = r < kShare ? warp * kShare + r : NH;
+          const bool there = q_row < it.rows;
+          const int from = output_row(p, it, min(q_row, it.rows - 1));
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (there)
+            x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+                                                     (size_t)from * D) + c);
+          if (c == 0 && q_row < NH) {
+            sRows[q_row] = from;
+            if (p.tree_masks)
+              sMasks[q_row] = (unsigned long long)__ldg(
+                  reinterpret_cast<const long long*>(p.tree_masks) + from / p.num_q_heads);
+          }
+          const float factor = split_row<T, NH, D, L::kQParts>(x, q_row, c, sQ);
+          if (c == 0 && q_row < NH) sFactors[q_row] = p.qscale * factor;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        arrive_warp(q_first);
+        ok = ok && mbar_wait(q_first, 0, p.status);
+      } else {
+        const int b = k_item % QB;
+        ok = ok && mbar_wait(&q_full[b], (k_item / QB - (L::kKeysSplit && b == 0)) & 1, p.status);
+      }
       const float* factors = sFactors + mb * NH + hb;
       if (L::KG > 1 && hb >= it.rows) {
         // None of this warpgroup's rows is there: it only hands the buffers on.
