@@ -49,6 +49,7 @@
 
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -66,6 +67,7 @@ constexpr int kKeys = kTileKeys;  // keys per tile
 constexpr int kParts = 3;         // e5m2 parts of a softmax weight
 constexpr int kBufs = 2;          // buffers of the weights
 constexpr int kItemBufs = 1;      // items handed out ahead (2 and 4: 64 short requests 1 and 4 us slower)
+constexpr int kMostCtas = 8192;
 constexpr float kExceed = 12.f;   // weights reach 2^12 before the reference moves
 constexpr float kStep2 = 64.f;    // what a part of a weight leaves comes 64 and 16 times as
 constexpr float kStep3 = 16.f;    // large: at most 2^15, which e5m2 holds
@@ -525,7 +527,7 @@ __device__ __forceinline__ float split_row(uint4 x, int row, int c, unsigned cha
 template <typename T, int NH, int D>
 __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kPerSm)
     attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap vmap) {
+                    const __grid_constant__ CUtensorMap vmap, int num_items) {
   using L = Shape<T, NH, D>;
   constexpr int S = L::kStages, SB = L::SB, PB = kBufs, SC = L::kScaleStages, NHW = L::NHW,
                 QB = L::kQBufs;
@@ -628,23 +630,27 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         mbar_arrive_expect_tx(ticket, 16);
         take_cta(answer, ticket);
       }
-      it = item_at<NH>(p, j, lane == 0);
-      if (it.n_tiles > 0) {
-        const int b = n % kItemBufs;
-        ok = n < kItemBufs || wait_warp(&i_free[b], (n / kItemBufs - 1) & 1, p.status);
-        if (ok && lane == 0) {
-          sItems[b] = it;
-          mbar_arrive(&i_full[b]);
+      // (A CTA stands for more than one item where there are very many, most of
+      // them past the end of a context.)
+      for (int i = j; ok && i < num_items && i >= 0; i += gridDim.x) {
+        it = item_at<NH>(p, i, lane == 0);
+        if (it.n_tiles > 0) {
+          const int b = n % kItemBufs;
+          ok = n < kItemBufs || wait_warp(&i_free[b], (n / kItemBufs - 1) & 1, p.status);
+          if (ok && lane == 0) {
+            sItems[b] = it;
+            mbar_arrive(&i_full[b]);
+          }
+          ++n;
+        } else if (it.ctx == 0 && it.part == 0) {  // nothing to see: zeros
+          constexpr int kWords = D / 8;
+          for (int w = lane; w < it.rows * kWords; w += 32)
+            reinterpret_cast<uint4*>(p.out)[(size_t)output_row(p, it, w / kWords) * kWords +
+                                            w % kWords] = make_uint4(0, 0, 0, 0);
         }
-        ++n;
-      } else if (it.ctx == 0 && it.part == 0) {  // nothing to see: zeros
-        constexpr int kWords = D / 8;
-        for (int i = lane; i < it.rows * kWords; i += 32)
-          reinterpret_cast<uint4*>(p.out)[(size_t)output_row(p, it, i / kWords) * kWords +
-                                          i % kWords] = make_uint4(0, 0, 0, 0);
       }
-      if (!wait_warp(ticket, asked & 1, p.status)) {
-        mbar_drain(ticket, asked & 1);
+      if (!ok || !wait_warp(ticket, asked & 1, p.status)) {
+        mbar_drain(ticket, asked & 1);  // the answer lands before the CTA leaves
         ok = false;
         break;
       }
@@ -1281,8 +1287,9 @@ cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CU
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
   const int items = p.num_seqs * p.num_kv_heads * p.num_parts * p.chunks;
-  err = launch_overlapped(attn_fp8_kernel<T, NH, D>, dim3(items), dim3(L::kThreads), L::kBytes,
-                          stream, p, km, vm);
+  const int ctas = std::min(items, kMostCtas);
+  err = launch_overlapped(attn_fp8_kernel<T, NH, D>, dim3(ctas), dim3(L::kThreads), L::kBytes,
+                          stream, p, km, vm, items);
   if (err != cudaSuccess || p.num_parts <= 1) return err;
   const long long rows = (long long)p.total_queries * p.num_q_heads;
   return launch_overlapped(attn_fp8_reduce_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)),
