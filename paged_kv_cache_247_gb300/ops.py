@@ -676,9 +676,9 @@ def tree_fp8_workspace_size(total_queries, max_query_len, num_seqs, num_q_heads,
 
 
 def _fp8_attn(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-              max_context_len, max_query_len, partition_size, workspace, *more):
-    """Checks and workspace that the two attention calls over an 8-bit cache
-    share: the common device, the sizes, and the workspace's address and bytes."""
+              workspace, *more):
+    """Checks that the two attention calls over an 8-bit cache share: the common
+    device and the sizes."""
     _cuda(q, "q", ndim=3)
     if q.dtype not in _DTYPE_CODE:
         raise ValueError("q must be float16 or bfloat16")
@@ -694,20 +694,28 @@ def _fp8_attn(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, contex
         raise ValueError("block_tables / context_lens must have one row per sequence")
     dev = _same_device(q, out, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                        workspace, *more)
-    if workspace is None:
-        sizes = (T, max_query_len, S, Hq, Hkv, D, max_context_len, partition_size)
-        if dev == torch._C._cuda_getDevice():
-            size = tree_fp8_workspace_size(*sizes)
-        else:
-            with torch.cuda.device(dev):
-                size = tree_fp8_workspace_size(*sizes)
-        if size:
-            workspace = q.new_empty(size >> 1)
-    else:
+    if workspace is not None:
         _cuda(workspace, "workspace")
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size())
-    return dev, (S, Hq, Hkv, D, B, NB), ws, workspace
+    return dev, (S, Hq, Hkv, D, B, NB)
+
+
+def _launch_fp8_attn(name, dev, q, workspace, sizes, *args):
+    """_launch with the workspace last.  Without one the call is made as it is,
+    which is all there is to it unless the context is split; then it comes back
+    at once, before anything runs, and is made again with one of torch's."""
+    fn = getattr(_lib.load(), name)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _launch_fp8_attn(name, dev, q, workspace, sizes, *args)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if workspace is None:
+        st = fn(*args, None, 0, stream)
+        if st == _lib.PKV_ERR_WORKSPACE_TOO_SMALL:
+            workspace = q.new_empty(tree_fp8_workspace_size(*sizes) >> 1)
+    if workspace is not None:
+        st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    if st:
+        _lib.check(st, name)
 
 
 def paged_attn_decode_fp8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
@@ -717,16 +725,18 @@ def paged_attn_decode_fp8(out, q, k_cache, v_cache, k_scales, v_scales, block_ta
     ``workspace`` (any CUDA tensor of at least :func:`decode_fp8_workspace_size`
     bytes) is allocated here with torch if omitted and needed.  Writes ``out``
     ([S, Hq, D]) and returns it."""
-    dev, (S, Hq, Hkv, D, B, NB), ws, workspace = _fp8_attn(
-        out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-        max_context_len, 1, partition_size, workspace)
+    dev, (S, Hq, Hkv, D, B, NB) = _fp8_attn(out, q, k_cache, v_cache, k_scales, v_scales,
+                                            block_tables, context_lens, workspace)
     if q.shape[0] != S:
         raise ValueError("q must have one row per sequence")
-    _launch("pkv_paged_attn_decode_fp8", dev, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(),
-            _c_int(max_context_len, "max_context_len"), S, Hq, Hkv, D, B, NB, float(scale),
-            _DTYPE_CODE[q.dtype], _c_int(partition_size, "partition_size"), *ws)
+    max_context_len = _c_int(max_context_len, "max_context_len")
+    partition_size = _c_int(partition_size, "partition_size")
+    _launch_fp8_attn(
+        "pkv_paged_attn_decode_fp8", dev, q, workspace,
+        (S, 1, S, Hq, Hkv, D, max_context_len, partition_size), out.data_ptr(), q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), max_context_len,
+        S, Hq, Hkv, D, B, NB, float(scale), _DTYPE_CODE[q.dtype], partition_size)
     return out
 
 
@@ -747,18 +757,22 @@ def paged_attn_tree_fp8(out, q, query_start, tree_masks, k_cache, v_cache, k_sca
     rows behind the last sequence stay) and returns it."""
     _cuda(query_start, "query_start", torch.int32, 1)
     _cuda(tree_masks, "tree_masks", torch.int64, 1)
-    dev, (S, Hq, Hkv, D, B, NB), ws, workspace = _fp8_attn(
-        out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-        max_context_len, max_query_len, partition_size, workspace, query_start, tree_masks)
+    dev, (S, Hq, Hkv, D, B, NB) = _fp8_attn(out, q, k_cache, v_cache, k_scales, v_scales,
+                                            block_tables, context_lens, workspace, query_start,
+                                            tree_masks)
     T = q.shape[0]
     if query_start.shape[0] != S + 1 or tree_masks.shape[0] != T:
         raise ValueError("query_start / tree_masks must match context_lens / q")
-    _launch("pkv_paged_attn_tree_fp8", dev, out.data_ptr(), q.data_ptr(), T,
-            query_start.data_ptr(), _c_int(max_query_len, "max_query_len"), tree_masks.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
-            _c_int(max_context_len, "max_context_len"), S, Hq, Hkv, D, B, NB, float(scale),
-            _DTYPE_CODE[q.dtype], _c_int(partition_size, "partition_size"), *ws)
+    max_context_len = _c_int(max_context_len, "max_context_len")
+    max_query_len = _c_int(max_query_len, "max_query_len")
+    partition_size = _c_int(partition_size, "partition_size")
+    _launch_fp8_attn(
+        "pkv_paged_attn_tree_fp8", dev, q, workspace,
+        (T, max_query_len, S, Hq, Hkv, D, max_context_len, partition_size), out.data_ptr(),
+        q.data_ptr(), T, query_start.data_ptr(), max_query_len, tree_masks.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), max_context_len,
+        S, Hq, Hkv, D, B, NB, float(scale), _DTYPE_CODE[q.dtype], partition_size)
     return out
 
 
