@@ -32,11 +32,13 @@
 // first product's M, the D dimensions the second's (D = 64: an M of 64, whose
 // row i lies in tensor-memory lane 32 (i / 16) + i % 16).  A work item is
 // (sequence, KV head, partition of the context, up to 64 rows), a row being a
-// query head of the group and one of the sequence's queries.  One persistent CTA
-// per SM walks the items; its rings, barriers and tensor memory flow from item
-// to item.  Warps:
+// query head of the group and one of the sequence's queries.  Two CTAs per SM (one
+// from 33 rows on) go through the items; their rings, barriers and tensor memory
+// flow from item to item, and an SM whose items are short takes more of them:
+// the launch has a CTA per item, and a running one takes over those that have
+// not started.  Warps:
 //
-//   key warpgroups (one; two, each with half the rows, for more than 16 rows):
+//   key warpgroups (one; two and four, each with 16 rows, for more than 16 and 32):
 //              thread t has key t of the tile: scales, logits, weights, and at
 //              the end dimension t of the output.  Its parts of the weights are
 //              neighbouring bytes (MN-major operand, no swizzle): one 16-byte
@@ -46,6 +48,22 @@
 //   Q warps          rows split into their parts, an item ahead
 //   item warp        the next items, from the CTAs that have not started
 //   S, O issuers     four (D = 64: two, four) MMAs per tile
+//
+// Up to 8 rows the time is the cache's bytes: 64 x 8,192 positions, 8 heads of 128
+// with 4 rows 161 us, 6,780 GB/s; 64 contexts of 16-2,048, 40 heads of one row 69 us,
+// 5,470 GB/s, where the ends of items show.  More rows are bound by the key warps:
+// 32 x 4,096, 8 heads of 64 rows 100 us, 2,790 GB/s, issue slots 56 % used where an
+// SM works: 24 instructions a row and key warp for each tile, 4 of them the split in
+// three.  What it took, at those three cases (us):
+//   CUDA cores                                              2,406    349   3,998
+//   this form, one CTA per SM, items dealt out beforehand     201    127     392
+//   two floats per instruction, masks only in the last tiles  201    120     242
+//   two CTAs per SM, items taken as they come, seldom code
+//     kept short (met for the first time it runs at the
+//     latency of its fetch)                                   164     76     165
+//   weights in e5m2, one arrival per warp                     170     83     154
+//   two CTAs per SM with two key warpgroups each              156     70     125
+//   four key warpgroups: each tile once for 64 rows           161     69     100
 
 #include <math_constants.h>
 

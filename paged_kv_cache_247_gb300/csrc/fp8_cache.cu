@@ -7,7 +7,11 @@
 // bits, for the prompt-chunk attention, which reads those.
 //
 // Both are bound by HBM: 2 D bytes on the 16-bit side and D + 2 on the other
-// per row.
+// per row.  Append of 16,384 tokens of 8 heads of 128: 17.5 us, 5,780 GB/s (with 8
+// elements per thread, whose 16-byte loads are contiguous over a warp, 20.9: the
+// shuffles and addresses of twice the threads then fill 73 % of the issue slots).
+// Blocks of 8 x 4,096 positions read back: 33.1 us, 6,120 GB/s (16 elements per
+// thread, stores of 16 bytes at strides of 32: 36.3).
 
 #include "common.cuh"
 #include "fp8.cuh"
