@@ -546,6 +546,9 @@ pkv_status_t pkv_kv_compact(
  * and appended again it keeps its values.  A row with a NaN or an infinity is
  * held as NaN as a whole (scale NaN, codes 0).
  *
+ * The attention calls read scales as powers of two (or NaN): one of V that comes
+ * from elsewhere and is none counts as the power of two below it.
+ *
  * pkv_block_copy copies the codes (block_bytes = num_kv_heads * block_size *
  * head_dim) and, in a call of its own, the scales (num_kv_heads * block_size *
  * 2).  Prompt chunks attend over cached blocks read back by pkv_block_read_fp8

@@ -61,7 +61,7 @@
 //   two CTAs per SM, items taken as they come, seldom code
 //     kept short (met for the first time it runs at the
 //     latency of its fetch)                                   164     76     165
-//   weights in e5m2, one arrival per warp                     170     83     154
+//   weights in e5m2, one arrival per warp                     159     73     154
 //   two CTAs per SM with two key warpgroups each              156     70     125
 //   four key warpgroups: each tile once for 64 rows           161     69     100
 
