@@ -155,7 +155,7 @@ struct Shape {
   static constexpr int kTicket = kItems + kItemBufs * 64;
   static constexpr int kBar = kTicket + 16;
   static constexpr int kBars =
-      4 * kStages + 2 * SB + 2 * kBufs + kScaleStages + 2 * kQBufs + 4 + 2 * kItemBufs + 2;
+      4 * kStages + 2 * SB + 2 * kBufs + kScaleStages + 2 * kQBufs + 6 + 2 * kItemBufs + 2;
   static constexpr int kTmemSlot = kBar + kBars * 8;
   static constexpr int kBytes = kTmemSlot + 16 + 1024;
   static_assert(kItemBufs * 64 + kBars * 8 + 32 <= 1024 && kBytes <= kRoom && kStages >= 2,
@@ -571,9 +571,10 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
   uint64_t* p_full = s_free + SB;   // [PB] weights written (and O^T of the item before read)
   uint64_t* p_free = p_full + PB;   // [PB] their MMAs are done (commit)
   uint64_t* c_full = p_free + PB;   // [SC] the tile's scales landed
-  uint64_t* q_full = c_full + SC;   // [QB] an item's rows, factors and masks written
+  uint64_t* q_full = c_full + SC;   // [QB] the parts of an item's rows of q written
   uint64_t* q_free = q_full + QB;   // [QB] its S^T computed (commit)
-  uint64_t* m_free = q_free + QB;   // [2] its rows, factors and masks read
+  uint64_t* m_full = q_free + QB;   // [2] its output rows, factors and masks written
+  uint64_t* m_free = m_full + 2;    // [2] read
   uint64_t* drain = m_free + 2;     // [2] each issuer's last MMAs finished
   uint64_t* i_full = drain + 2;     // [kItemBufs] item written
   uint64_t* i_free = i_full + kItemBufs;  // [kItemBufs] read by every warp
@@ -605,6 +606,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       mbar_init(&q_free[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&m_full[b], L::kQWarps);
       mbar_init(&m_free[b], 4 * L::KG);
       mbar_init(&drain[b], 1);
     }
@@ -793,6 +795,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       arrive_warp(&q_full[b]);
+      arrive_warp(&m_full[mb]);
     }
     __syncwarp();
   } else if (warp == L::kSWarp || warp == L::kOWarp) {
@@ -908,8 +911,8 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         arrive_warp(q_first);
         ok = ok && mbar_wait(q_first, 0, p.status);
       } else {
-        const int b = k_item % QB;
-        ok = ok && mbar_wait(&q_full[b], (k_item / QB - (L::kKeysSplit && b == 0)) & 1, p.status);
+        // (Not q_full, which may be filled again before the last key warp looks.)
+        ok = ok && mbar_wait(&m_full[mb], (k_item / 2 - (L::kKeysSplit && mb == 0)) & 1, p.status);
       }
       const float* factors = sFactors + mb * NH + hb;
       if (L::KG > 1 && hb >= it.rows) {
