@@ -1031,8 +1031,8 @@ struct Fp8Plan {
 // else one).  An item costs its tiles and some more; a round that leaves CTAs out
 // is faster, down to `alone`; a split call pays for its partial outputs, written
 // and read again, and a launch.  Measured over all splits of a context (us, the
-// chosen one first): 4 x 8,192 positions, 8 heads of 64 rows, 16 tiles 43, 8 tiles
-// 51, 64 96; 1 x 32,768, 8 heads of 4 rows, 16 tiles 30, 64 57, 256 186; 32 x
+// chosen one first): 4 x 8,192 positions, 8 heads of 64 rows, 16 tiles 41, 8 tiles
+// 47, 64 94; 1 x 32,768, 8 heads of 4 rows, 16 tiles 29, 64 57, 256 186; 32 x
 // 4,096, 8 heads of 64 rows, unsplit 108, 16 tiles 125; 64 x 8,192, 8 heads of 4
 // rows, unsplit 158, 32 tiles 171; 32 x 4,096, 4 heads of 16 rows, unsplit 45, 16
 // tiles 53.

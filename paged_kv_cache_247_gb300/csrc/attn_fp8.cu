@@ -1206,8 +1206,16 @@ __global__ void __launch_bounds__(128) attn_fp8_reduce_kernel(const AttnFp8Param
   const float* mrow = p.ws_m + row * p.num_parts;
   const float* lrow = p.ws_l + row * p.num_parts;
   const float* orow = p.ws_o + row * p.num_parts * D + lane * E;
-  // On their way while the sequence is looked for; of partitions that are none
-  // they are not used.
+  // On their way while the sequence is looked for (a call that splits has two
+  // partitions at least); of partitions that are none they are not used.
+  auto load = [&](int i, float2* o) {
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e)
+      o[e] = __ldcg(reinterpret_cast<const float2*>(orow + (size_t)i * D) + e);
+  };
+  float2 early[2][E / 2];
+  load(0, early[0]);
+  load(1, early[1]);
   float m0 = -CUDART_INF_F, l0 = 0.f;
   if (lane < p.num_parts) {
     m0 = __ldcg(mrow + lane);
@@ -1248,17 +1256,24 @@ __global__ void __launch_bounds__(128) attn_fp8_reduce_kernel(const AttnFp8Param
     const float m = base == 0 ? m0 : (i < np ? __ldcg(mrow + i) : 0.f);
     const float mine = i >= np || l == 0.f ? 0.f : l * exp2f(m - M);
     const int n = min(32, np - base);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
+    auto add = [&](int k, const float2* o) {
       const float w = __shfl_sync(0xffffffffu, mine, k);
       sum += w;
-      const float2* o = reinterpret_cast<const float2*>(orow + (size_t)(base + k) * D);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
-        const float2 v = __ldcg(o + e);
-        acc[2 * e] = fmaf(w, v.x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(w, v.y, acc[2 * e + 1]);
+        acc[2 * e] = fmaf(w, o[e].x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(w, o[e].y, acc[2 * e + 1]);
       }
+    };
+    if (base == 0) {
+      add(0, early[0]);
+      add(1, early[1]);
+    }
+#pragma unroll 4
+    for (int k = base == 0 ? 2 : 0; k < n; ++k) {
+      float2 o[E / 2];
+      load(base + k, o);
+      add(k, o);
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
