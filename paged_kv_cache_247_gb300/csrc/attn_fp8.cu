@@ -6,12 +6,17 @@
 //
 // The codes go from HBM through shared memory into the tensor core as they are
 // (tcgen05.mma kind::f8f6f4); nothing is widened on the way.  The operands on
-// the other side are split into e4m3 parts instead, which cost only columns of
+// the other side are split into 8-bit parts instead, which cost only columns of
 // an N that is far from full:
 //
-//   q row      = 2^e (c1 + c2 / 16 + c3 / 256), e4m3 parts of 4 bits each: two
-//                hold a bf16 row exactly (8 bits), three an fp16 row (11), down
-//                to 2^-18 of the row's largest element;
+//   q row      = 2^e (c1 + c2 / 16 + c3 / 256), e4m3 parts of 4 bits each, 2^e
+//                as for a cache row: multiples of 2^(e - 17).  That is all of a
+//                bf16 element from 2^-17 of the row's largest on, of an fp16 one
+//                from 2^-14 on, and 2^-25 of the largest off at most for others.
+//                (bf16 rows in two parts: from 2^-14 on, and 2^-21, and no faster:
+//                32 x 4,096, 8 heads of 64 rows 106.2 us against 106.4 with three, of
+//                32 rows 81.9 and 81.9, 4 heads of 16 rows 45.7 and 47.1, 64 x 8,192,
+//                8 heads of 4 rows 186.4 and 184.3, each with the L2 cache flushed;)
 //   S^T        [128 keys x parts * rows] = K codes . parts^T
 //   x          = scale log2(e) 2^e k_scale (s1 + s2 / 16 + s3 / 256)
 //   y          = x + log2 v_scale: the V row's scale is an addend of the base-2
@@ -68,7 +73,6 @@
 #include <math_constants.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "common.cuh"
 #include "fp8.cuh"
@@ -82,6 +86,7 @@ namespace {
 using namespace tc;
 
 constexpr int kKeys = kTileKeys;  // keys per tile
+constexpr int kQParts = 3;        // e4m3 parts of a query row
 constexpr int kParts = 3;         // e5m2 parts of a softmax weight
 constexpr int kBufs = 2;          // buffers of the weights
 constexpr int kItemBufs = 1;      // items handed out ahead (2 and 4: 64 short requests 1 and 4 us slower)
@@ -100,9 +105,8 @@ constexpr int key_regs(int warpgroups) { return warpgroups == 2 ? 88 : 96; }
 constexpr int up16(int x) { return (x + 15) / 16 * 16; }
 constexpr int pow2_at_least(int x, int p = 32) { return p >= x ? p : pow2_at_least(x, 2 * p); }
 
-template <typename T, int NH, int D>
+template <int NH, int D>
 struct Shape {
-  static constexpr int kQParts = std::is_same<T, __half>::value ? 3 : 2;
   static constexpr int NS = up16(kQParts * NH);  // columns of S^T
   static constexpr int NO = up16(kParts * NH);   // columns of O^T
   static constexpr int KG = NH > 16 ? NH / 16 : 1;  // key warpgroups
@@ -111,8 +115,8 @@ struct Shape {
   static constexpr int kQWarps = KG == 1 ? 1 : 2;
   static constexpr bool kKeysSplit = KG > 1;        // the first item's rows: see there
   // items' parts of q held, and buffers of S^T
-  static constexpr int kQBufs = KG == 2 && kQParts == 3 ? 1 : 2;
-  static constexpr int SB = KG >= 2 && kQParts == 3 ? 1 : 2;
+  static constexpr int kQBufs = KG == 2 ? 1 : 2;
+  static constexpr int SB = KG >= 2 ? 1 : 2;
   static constexpr int kKWarp = 4 * KG;
   static constexpr int kVWarp = kKWarp + 1;
   static constexpr int kSWarp = kKWarp + 2;  // owns tensor memory
@@ -126,7 +130,7 @@ struct Shape {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTile = kKeys * D;     // bytes of a K or V tile
   static constexpr int kQBytes = NS * D;
-  static constexpr int kRawRows = NH < 16 ? NH : (KG == 2 && kQBufs == 2 ? 8 : 16);
+  static constexpr int kRawRows = NH < 16 ? NH : 16;
   static constexpr int kRaw = kRawRows * D * 2;  // q rows as they are, some at a time
   static constexpr int kPBuf = kKeys * NO;
   // scales, an item's rows, reductions, items, barriers; alignment
@@ -505,7 +509,7 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src, int byt
 // elements 8 c ..., as row `row` of each part in shared memory; returns the power
 // of two that they are to be multiplied with (NaN for a row with a NaN or an
 // infinity).
-template <typename T, int NH, int D, int PARTS>
+template <typename T, int NH, int D>
 __device__ __forceinline__ float split_row(uint4 x, int row, int c, unsigned char* dst) {
   constexpr int kLanes = D / 8;
   uint32_t top = max_magnitude(x);
@@ -525,7 +529,7 @@ __device__ __forceinline__ float split_row(uint4 x, int row, int c, unsigned cha
     y[2 * i + 1] = finite ? f.y * inv : 0.f;
   }
 #pragma unroll
-  for (int part = 0; part < PARTS; ++part) {
+  for (int part = 0; part < kQParts; ++part) {
     uint32_t codes[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -543,10 +547,10 @@ __device__ __forceinline__ float split_row(uint4 x, int row, int c, unsigned cha
 }
 
 template <typename T, int NH, int D>
-__global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kPerSm)
+__global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
     attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, int num_items) {
-  using L = Shape<T, NH, D>;
+  using L = Shape<NH, D>;
   constexpr int S = L::kStages, SB = L::SB, PB = kBufs, SC = L::kScaleStages, NHW = L::NHW,
                 QB = L::kQBufs;
   grid_dep_wait();
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         for (int r = lane / kLanes; r < kRound; r += kAtOnce) {
           const uint4 x = *reinterpret_cast<const uint4*>(raw + (r * kLanes + c) * 16);
           const int row = w * kMine + first + r;
-          const float factor = split_row<T, NH, D, L::kQParts>(x, row, c, dst);
+          const float factor = split_row<T, NH, D>(x, row, c, dst);
           if (c == 0) sFactors[mb * NH + row] = p.qscale * factor;
         }
       }
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
               sMasks[q_row] = (unsigned long long)__ldg(
                   reinterpret_cast<const long long*>(p.tree_masks) + from / p.num_q_heads);
           }
-          const float factor = split_row<T, NH, D, L::kQParts>(x, q_row, c, sQ);
+          const float factor = split_row<T, NH, D>(x, q_row, c, sQ);
           if (c == 0 && q_row < NH) sFactors[q_row] = p.qscale * factor;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -965,7 +969,7 @@ __global__ void __launch_bounds__(Shape<T, NH, D>::kThreads, Shape<T, NH, D>::kP
         const float ks = scale_value(scales[0]);
         const uint32_t vbits = scales[kKeys];
         Pair y[NHW / 2];
-        load_parts<L::kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, 16.f, 16.f, y);
+        load_parts<kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, 16.f, 16.f, y);
         tc_fence_before();
         arrive_warp(&s_free[sb]);
 
@@ -1302,7 +1306,7 @@ bool make_codes_map(CUtensorMap* map, const void* base, long long rows, int head
 template <typename T, int NH, int D>
 cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CUtensorMap& vm,
                          cudaStream_t stream) {
-  using L = Shape<T, NH, D>;
+  using L = Shape<NH, D>;
   static unsigned long long configured = 0;  // bit per device ordinal (< 64)
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
