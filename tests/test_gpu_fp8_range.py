@@ -10,6 +10,8 @@ of sum_t p_t |v_t|.
 
 import math
 
+import math
+
 import pytest
 import torch
 
