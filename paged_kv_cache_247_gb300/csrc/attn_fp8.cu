@@ -21,17 +21,20 @@
 //   x          = scale log2(e) 2^e k_scale (s1 + s2 / 16 + s3 / 256)
 //   y          = x + log2 v_scale: the V row's scale is an addend of the base-2
 //                logit, and the running reference m is one of y, which is what
-//                gets rounded: p = 2^(y - m) <= 2^12, to fp16, which is c1 +
-//                c2 / 64 + c3 / 1024 in e5m2: what each part leaves of 11 bits
-//                fits the next (3 bits and twice 3 and the sign), down to fp16's
-//                own smallest step, 2^-24
+//                gets rounded: p = 2^(y - m) <= 2^15, to fp16, which is c1 +
+//                c2 / 16 + c3 / 256 in e5m2: what each part leaves of 11 bits
+//                fits the next (3 bits and twice 3 and the sign; at most 2^15),
+//                down to fp16's own smallest step, 2^-24
 //   O^T        [D x parts * rows] += V codes^T . parts
 //   l          += p / v_scale
-//   out        = (o1 + o2 / 64 + o3 / 1024) / l
+//   out        = (o1 + o2 / 16 + o3 / 256) / l
 //
-// m moves when some y is 12 above it, to that y: what is lost of a weight is at
-// most 2^-25 of the largest, and the largest has room to grow by 2^12 before m
-// moves again, which costs about as much as a tile.
+// m moves when some y is 15 above it, to 6 below that y: half a step is at most
+// 2^-31 of the largest p, and the largest has room to grow by 2^9 before m moves
+// again, which costs about as much as a tile.  (Room for 2^12, 2^7 and 2^4, half a
+// step of 2^-28, 2^-33 and 2^-36: 32 x 4,096, 8 heads of 64 rows 106.5, 112.3 and
+// 117.4 us for 109.2, L2 flushed; decode the same.)  n positions lose at most n of
+// these half steps: l counts what they lose.
 //
 // Orientation, pipeline and roles follow the 16-bit decode kernel: keys are the
 // first product's M, the D dimensions the second's (D = 64: an M of 64, whose
@@ -91,9 +94,9 @@ constexpr int kParts = 3;         // e5m2 parts of a softmax weight
 constexpr int kBufs = 2;          // buffers of the weights
 constexpr int kItemBufs = 1;      // items handed out ahead (2 and 4: 64 short requests 1 and 4 us slower)
 constexpr int kMostCtas = 8192;
-constexpr float kExceed = 12.f;   // weights reach 2^12 before the reference moves
-constexpr float kStep2 = 64.f;    // what a part of a weight leaves comes 64 and 16 times as
-constexpr float kStep3 = 16.f;    // large: at most 2^15, which e5m2 holds
+constexpr float kExceed = 15.f;   // weights reach 2^15 before the reference moves,
+constexpr float kPlace = 6.f;     // to where the largest is 2^6
+constexpr float kStep = 16.f;     // what a part of a weight or a query leaves comes 16 times as large
 constexpr float kNoRef = -3e38f;  // the reference before any
 constexpr int kMinVExponent = -60;  // V rows below 448 * 2^-60 count as zero
 
@@ -233,12 +236,11 @@ __device__ __forceinline__ Pair pair_at(const float* x, int g) {
   return g & 1 ? pair(v.z, v.w) : pair(v.x, v.y);
 }
 
-// v = the sum over PARTS parts, part c in columns c * NH ..., of part 0, part 1 /
-// step2 and part 2 / (step2 step3).
+// v = the sum over PARTS parts, part c in columns c * NH ..., of part c / kStep^c.
 template <int PARTS, int NH, int NHW>
-__device__ __forceinline__ void load_parts(uint32_t taddr, float step2, float step3, Pair* v) {
+__device__ __forceinline__ void load_parts(uint32_t taddr, Pair* v) {
   constexpr int kOnce = NHW < 8 ? NHW : 8;  // more would not fit the registers
-  const Pair by2 = pair(1.f / step2, 1.f / step2), by3 = pair(1.f / step3, 1.f / step3);
+  const Pair by = pair(1.f / kStep, 1.f / kStep);
 #pragma unroll
   for (int first = 0; first < NHW; first += kOnce) {
     float part[PARTS * kOnce];
@@ -251,7 +253,7 @@ __device__ __forceinline__ void load_parts(uint32_t taddr, float step2, float st
 #pragma unroll
       for (int c = PARTS - 2; c >= 0; --c) {
         const Pair next = pair(part[c * kOnce + 2 * g], part[c * kOnce + 2 * g + 1]);
-        x = fma2(x, c == 1 ? by3 : by2, next);
+        x = fma2(x, by, next);
       }
       v[first / 2 + g] = x;
     }
@@ -276,14 +278,14 @@ __device__ __forceinline__ uint32_t e5m2x4(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// step (h - the lower or upper two codes): exact (a code is the upper byte of its
+// kStep (h - the lower or upper two codes): exact (a code is the upper byte of its
 // fp16 value).
 template <int UPPER>
-__device__ __forceinline__ uint32_t remainder_of(uint32_t h2, uint32_t codes, float step) {
+__device__ __forceinline__ uint32_t remainder_of(uint32_t h2, uint32_t codes) {
   const uint32_t back = __byte_perm(codes, 0u, UPPER ? 0x3424 : 0x1404);
   const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h2),
                                     *reinterpret_cast<const __half2*>(&back)),
-                            __float2half2_rn(step));
+                            __float2half2_rn(kStep));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
@@ -536,8 +538,8 @@ __device__ __forceinline__ float split_row(uint4 x, int row, int c, unsigned cha
       codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_SATFINITE,
                                           __NV_E4M3);
       const float2 back = decode2(codes[i]);
-      y[2 * i] = (y[2 * i] - back.x) * 16.f;
-      y[2 * i + 1] = (y[2 * i + 1] - back.y) * 16.f;
+      y[2 * i] = (y[2 * i] - back.x) * kStep;
+      y[2 * i + 1] = (y[2 * i + 1] - back.y) * kStep;
     }
     if (row < NH)
       *reinterpret_cast<uint2*>(dst + swizzled<D>(part * NH + row, c * 8)) =
@@ -969,7 +971,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
         const float ks = scale_value(scales[0]);
         const uint32_t vbits = scales[kKeys];
         Pair y[NHW / 2];
-        load_parts<kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, 16.f, 16.f, y);
+        load_parts<kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, y);
         tc_fence_before();
         arrive_warp(&s_free[sb]);
 
@@ -1048,9 +1050,9 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
           named_barrier_sync(1 + kg, 128);
           const float mt = fmax3(fmaxf(tops[row], tops[NHW + row]), tops[2 * NHW + row],
                                  tops[3 * NHW + row]);
-          const bool moves = mt + nm > 0.f;  // (all that have grown, now that some must)
-          const float alpha = moves ? ex2(-mt - nm) : 1.f;
-          if (moves) nm = -mt;
+          const bool moves = mt + nm > kPlace;  // (all that have grown, now that some must)
+          const float alpha = moves ? ex2(kPlace - mt - nm) : 1.f;
+          if (moves) nm = kPlace - mt;
           if (lane < NHW) {
             refs[row] = nm;
             alphas[row] = alpha;
@@ -1104,8 +1106,8 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
           for (int c = 0; c < kParts; ++c) {
             part[c][g] = e5m2x4(h[2 * g], h[2 * g + 1]);
             if (c + 1 < kParts) {
-              h[2 * g] = remainder_of<0>(h[2 * g], part[c][g], c == 0 ? kStep2 : kStep3);
-              h[2 * g + 1] = remainder_of<1>(h[2 * g + 1], part[c][g], c == 0 ? kStep2 : kStep3);
+              h[2 * g] = remainder_of<0>(h[2 * g], part[c][g]);
+              h[2 * g + 1] = remainder_of<1>(h[2 * g + 1], part[c][g]);
             }
           }
         }
@@ -1163,7 +1165,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
 #pragma unroll 1
       for (int g = 0; g < NHW && g < there; g += kOut) {
         Pair o[kOut / 2];
-        load_parts<kParts, NH, kOut>(tmem + L::kColO + hb + g + lane_base, kStep2, kStep3, o);
+        load_parts<kParts, NH, kOut>(tmem + L::kColO + hb + g + lane_base, o);
 #pragma unroll
         for (int u = 0; u < kOut; ++u) {
           const float2 v = both(o[u / 2]);

@@ -1,14 +1,17 @@
 """Attention over a cache held in 8 bits where the types' ranges are used: query
-elements far below the largest of their row.  Cases are those of test_gpu_fp8.
+elements far below the largest of their row, many weights far below the largest.
+Cases are those of test_gpu_fp8.
 
 Tolerance.  As there, |err| <= eps / 2 |out| + (2 dx + 2^-17 + 2^-11) sum_t p_t |v_t|,
-with the fp32 sums' roundings by the length: of O^T, which takes up 32 positions at a
-time, at most 2^-23 each, and of the weights, 128 of them side by side, 2^-24:
+but each position's lost weight by itself, and the fp32 sums' roundings with the
+length: of O^T, which takes up 32 positions at a time, at most 2^-23 each, and of the
+weights, 128 of them side by side, 2^-24:
   (n / 32) 2^-23 + (n / 128) 2^-24 <= n 2^-27
-of sum_t p_t |v_t|.
+of sum_t p_t |v_t|.  A weight times its V row's scale is rounded to fp16 where the
+largest such product stands at 2^6 or more: its own half step is 2^-25, so that a
+position loses at most 2^-31 of the largest product over its own scale:
+  lost_t = min(p_t, 2^-31 max_s p_s 2^e_s / 2^e_t).
 """
-
-import math
 
 import math
 
@@ -57,7 +60,10 @@ def reference(c, held=0.0):
         dx = abs(c.scale) * torch.where(seen, a, 0.0).amax(-1, keepdim=True)
         p = torch.softmax(x, -1).nan_to_num(0.0)                              # (nothing seen: zeros)
         o, size = p @ v[:, None], p @ v[:, None].abs()
-        b = torch.finfo(c.dt).eps / 2 * o.abs() + (2 * dx + 2.0 ** -17 + 2.0 ** -11 + n * 2.0 ** -27) * size
+        e2 = scales[:, None].transpose(-1, -2)                                # [H, 1, 1, n]
+        most = (p * e2).amax(-1, keepdim=True) / e2
+        lost = torch.minimum(p, 2.0 ** -31 * most) @ v[:, None].abs()
+        b = torch.finfo(c.dt).eps / 2 * o.abs() + (2 * dx + 2.0 ** -17 + 2.0 ** -11 + n * 2.0 ** -27) * size + lost
         b += 2.0 ** -25 if c.dt == torch.float16 else 2.0 ** -134              # half a subnormal step
         out[lo:hi] = o.permute(2, 0, 1, 3).reshape(L, hq, c.D)
         bound[lo:hi] = b.permute(2, 0, 1, 3).reshape(L, hq, c.D)
@@ -103,3 +109,32 @@ def test_query_elements_far_below_the_largest(cuda_device, dtype, down, held, ro
     c.k = c.k.to(c.dt)
     c.scale = 2.0 ** (down - 8)
     check(c, held)
+
+
+# ---- weights -----------------------------------------------------------------------------------
+
+
+def heavy(c, n, at, gap):
+    """Makes position `at` of sequence 0 outweigh the others by about 2^gap."""
+    rows, D = c.q.shape[1], c.D
+    c.q = (1 - torch.arange(rows, device="cuda") / (8 * rows))[None, :, None].expand(c.q.shape).to(c.dt).contiguous()
+    c.k = 0.002 * torch.randn((n, 1, D), generator=_gen(8), device="cuda")
+    c.k[at] = gap * math.log(2) / (D * c.scale)
+    c.k = c.k.to(c.dt)
+
+
+@pytest.mark.parametrize("rows,D", [(4, 64), (8, 128), (16, 128), (32, 64), (64, 128)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("gap", [24, 27])
+def test_a_flat_tail_of_weights(cuda_device, dtype, gap, rows, D):
+    """40,000 weights far below that of the first position, which alone they do
+    not share a dimension with: each is small, their sum is the output there."""
+    n = 40000
+    c = case(dtype, rows, D, [n])
+    heavy(c, n, 0, gap)
+    c.v = 0.5 + 0.4 * torch.rand((n, 1, D), generator=_gen(9), device="cuda")
+    c.v[..., 0] = 0
+    c.v[0] = 0
+    c.v[0, 0, 0] = 0.9
+    c.v = c.v.to(c.dt)
+    check(c, partition_size=-(-n // 128) * 128)
