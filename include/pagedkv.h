@@ -547,7 +547,15 @@ pkv_status_t pkv_kv_compact(
  * held as NaN as a whole (scale NaN, codes 0).
  *
  * The attention calls read scales as powers of two (or NaN): one of V that comes
- * from elsewhere and is none counts as the power of two below it.
+ * from elsewhere and is none counts as the power of two below it, an infinity as NaN.
+ *
+ * What the attention calls hold in less than 32 bits: a query element to 2^-25 of
+ * its row's largest (exactly from 2^-17 of it on in bf16, from 2^-14 on in fp16), a
+ * softmax weight to 11 bits, and to 2^-31 of its row's largest weight where the V rows
+ * have the same scale, 2^-24 where they have not.  So over n positions up to n 2^-31
+ * (n 2^-24) of the largest weight times |v| may be lost: 2^-14 over 128k positions of
+ * the same scale.  V rows may be of any sizes; what is below 2^-126 of the largest one
+ * may be lost.
  *
  * pkv_block_copy copies the codes (block_bytes = num_kv_heads * block_size *
  * head_dim) and, in a call of its own, the scales (num_kv_heads * block_size *

@@ -19,22 +19,33 @@
 //                8 heads of 4 rows 186.4 and 184.3, each with the L2 cache flushed;)
 //   S^T        [128 keys x parts * rows] = K codes . parts^T
 //   x          = scale log2(e) 2^e k_scale (s1 + s2 / 16 + s3 / 256)
-//   y          = x + log2 v_scale: the V row's scale is an addend of the base-2
-//                logit, and the running reference m is one of y, which is what
-//                gets rounded: p = 2^(y - m) <= 2^15, to fp16, which is c1 +
-//                c2 / 16 + c3 / 256 in e5m2: what each part leaves of 11 bits
-//                fits the next (3 bits and twice 3 and the sign; at most 2^15),
-//                down to fp16's own smallest step, 2^-24
+//   y          = x + lv, lv = log2 v_scale - E: the V row's scale, relative to a
+//                reference 2^E, is an addend of the base-2 logit, and the running
+//                reference m is one of y, which is what gets rounded: p =
+//                2^(y - m) <= 2^15, to fp16, which is c1 + c2 / 16 + c3 / 256 in
+//                e5m2: what each part leaves of 11 bits fits the next (3 bits and
+//                twice 3 and the sign; at most 2^15), down to fp16's own smallest
+//                step, 2^-24
 //   O^T        [D x parts * rows] += V codes^T . parts
-//   l          += p / v_scale
-//   out        = (o1 + o2 / 16 + o3 / 256) / l
+//   l          += p / 2^lv
+//   out        = 2^E (o1 + o2 / 16 + o3 / 256) / l
 //
 // m moves when some y is 15 above it, to 6 below that y: half a step is at most
 // 2^-31 of the largest p, and the largest has room to grow by 2^9 before m moves
 // again, which costs about as much as a tile.  (Room for 2^12, 2^7 and 2^4, half a
 // step of 2^-28, 2^-33 and 2^-36: 32 x 4,096, 8 heads of 64 rows 106.5, 112.3 and
-// 117.4 us for 109.2, L2 flushed; decode the same.)  n positions lose at most n of
-// these half steps: l counts what they lose.
+// 117.4 us for 109.2, L2 flushed; decode the same.)
+//
+// lv is kept within -6 and 1, so that of a softmax weight at most 2^-31 2^7 = 2^-24
+// of the largest is lost (2^-31 where the V rows' scales are the same), n times that
+// over n positions at most, since l counts what they lose.  E is the largest scale
+// of the item's first tile, and moves to a later tile's if that is more than twice
+// as large; the O^T so far shrinks by as much.  Rows below 2^-6 of it are added
+// apart, to an O^T of their own, in fp32 with their whole weights, and rows of zeros
+// not at all.  That takes 1.5 us a tile (3.4 with four warpgroups); where one token's V
+// is small in each context, a call takes 0 to 5 % more.  That the code is there
+// costs trees 4 % and decode nothing.  What is below 2^-126 of the largest row that
+// some query of the item sees may be lost.
 //
 // Orientation, pipeline and roles follow the 16-bit decode kernel: keys are the
 // first product's M, the D dimensions the second's (D = 64: an M of 64, whose
@@ -97,8 +108,19 @@ constexpr int kMostCtas = 8192;
 constexpr float kExceed = 15.f;   // weights reach 2^15 before the reference moves,
 constexpr float kPlace = 6.f;     // to where the largest is 2^6
 constexpr float kStep = 16.f;     // what a part of a weight or a query leaves comes 16 times as large
-constexpr float kNoRef = -3e38f;  // the reference before any
-constexpr int kMinVExponent = -60;  // V rows below 448 * 2^-60 count as zero
+constexpr float kNoRef = -3e38f;  // the reference of a row that saw nothing
+// V scales are taken relative to a reference 2^E: rows from 2^(E - kBelow) to
+// 2^(E + kAbove) go into the second product, smaller ones are added apart, larger
+// ones move E.  E is held as the bits of the bfloat16 number 2^(E - kBelow).
+constexpr int kAbove = 1, kBelow = 6;
+constexpr int kBand = (kAbove + kBelow) * 128;
+constexpr int kNoScale = 0x10000;  // before any: no scale's bits are in its band
+
+// E from the bits of a scale that is to be 2^up below it (down to 2^-126: a band that
+// leaves out a scale of zero).
+__device__ __forceinline__ int reference_above(int bits, int up) {
+  return max(bits + (up - kBelow) * 128, 0x80);
+}
 
 // Registers with several key warpgroups.  Two: 256 threads of 88 and 256 of 40, out
 // of 512 of 64; four: 512 of 96 and 256 of 40, out of 768 of 80.
@@ -138,7 +160,7 @@ struct Shape {
   static constexpr int kPBuf = kKeys * NO;
   // scales, an item's rows, reductions, items, barriers; alignment
   static constexpr int kMaxStages = (KG == 2 ? 256 : KG == 4 ? 512 : 384) / D;  // (no more fit)
-  static constexpr int kSmall = (kMaxStages + SB) * kKeys * 4 + 2 * NH * 16 + 4 * 4 * NH * 4 + 1024;
+  static constexpr int kSmall = (kMaxStages + SB) * kKeys * 4 + 2 * NH * 16 + 5 * 4 * NH * 4 + 1024;
   static constexpr int kFixed = kQBufs * kQBytes + kRaw + kBufs * kPBuf + kSmall + 1024;
   static constexpr int kRoom = (kPerSm == 1 ? 227 : 113) * 1024;
   static constexpr int kFit = (kRoom - kFixed) / (2 * kTile);
@@ -158,17 +180,21 @@ struct Shape {
   static constexpr int kSum = kTop + 4 * NH * 4;                // [KG][4 warps][NHW]
   static constexpr int kRef = kSum + 4 * NH * 4;                // [KG][4 warps][NHW]
   static constexpr int kAlpha = kRef + 4 * NH * 4;              // [KG][4 warps][NHW]
-  static constexpr int kItems = kAlpha + 4 * NH * 4;            // [kItemBufs] Item
+  static constexpr int kShift = kAlpha + 4 * NH * 4;            // [KG][4 warps][NHW]
+  static constexpr int kMarks = kShift + 4 * NH * 4;            // [KG][4 warps] integers
+  static constexpr int kItems = kMarks + KG * 16;               // [kItemBufs] Item
   static constexpr int kTicket = kItems + kItemBufs * 64;
   static constexpr int kBar = kTicket + 16;
   static constexpr int kBars =
       4 * kStages + 2 * SB + 2 * kBufs + kScaleStages + 2 * kQBufs + 6 + 2 * kItemBufs + 2;
   static constexpr int kTmemSlot = kBar + kBars * 8;
   static constexpr int kBytes = kTmemSlot + 16 + 1024;
-  static_assert(kItemBufs * 64 + kBars * 8 + 32 <= 1024 && kBytes <= kRoom && kStages >= 2,
+  static_assert(KG * 16 + kItemBufs * 64 + kBars * 8 + 32 <= 1024 && kBytes <= kRoom &&
+                    kStages >= 2,
                 "shared memory overflow");
   static constexpr int kColO = SB * NS;
-  static constexpr int kTmemCols = pow2_at_least(SB * NS + NO);
+  static constexpr int kColFar = kColO + NO;  // O^T of the V rows added apart
+  static constexpr int kTmemCols = pow2_at_least(kColFar + NH);
   static_assert(kTmemCols <= 512 / kPerSm, "tensor memory overflow");
   static constexpr int kSwizzle = D == 128 ? 2 : 4;  // descriptor code of the D-byte swizzle
 };
@@ -883,7 +909,9 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
     float* tops = reinterpret_cast<float*>(smem + L::kTop) + kg * 4 * NHW;
     float* sums = reinterpret_cast<float*>(smem + L::kSum) + kg * 4 * NHW;
     float* refs = reinterpret_cast<float*>(smem + L::kRef) + at;      // minus the references
-    float* alphas = reinterpret_cast<float*>(smem + L::kAlpha) + at;  // this warp's copies
+    int* marks = reinterpret_cast<int*>(smem + L::kMarks) + kg * 4;
+    float* alphas = reinterpret_cast<float*>(smem + L::kAlpha) + at;  // (this warp's copies)
+    float* shifts = reinterpret_cast<float*>(smem + L::kShift) + at;
     int kt = 0, sc = 0;
     uint32_t sc_phase = 0;
     bool ok = true;
@@ -939,12 +967,15 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
         continue;
       }
       // Rows past the item's get weights of zero by their reference.
-      float nm = hb + row < it.rows ? -kNoRef : -CUDART_INF_F;
+      float nm = hb + row < it.rows ? 0.f : -CUDART_INF_F;
+      bool unset = hb + row < it.rows;  // nm is of no weight yet
       if (lane < NHW) refs[row] = nm;
       __syncwarp();
       Pair l_part[NHW / 2];
 #pragma unroll
       for (int g = 0; g < NHW / 2; ++g) l_part[g] = pair(0.f, 0.f);
+      int ref_v = kNoScale;  // E
+      bool far = false;      // rows were added apart
       for (int i = 0; i < it.n_tiles; ++i, ++kt) {
         const int key0 = it.t_begin + i * kKeys;
         const int nvalid = min(kKeys, it.t_end - key0);
@@ -969,18 +1000,23 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
           sc_phase ^= 1;
         }
         const float ks = scale_value(scales[0]);
-        const uint32_t vbits = scales[kKeys];
+        uint32_t vb = scales[kKeys];
+        if (i == 0) {
+          // E: the tile's largest scale, looked for by every warp (with a NaN in it, or
+          // drafts that may not count, looked at again below).
+          uint2 four = *reinterpret_cast<const uint2*>(scales - t + kKeys + lane * 4);
+          const int n = nvalid - lane * 4;  // of the four, in the context
+          four.x &= (n > 1 ? 0xffffff80u : n > 0 ? 0xff80u : 0u);
+          four.y &= (n > 3 ? 0xffffff80u : n > 2 ? 0xff80u : 0u);
+          const uint32_t two = __vmaxu2(four.x, four.y);
+          const int most = (int)__reduce_max_sync(0xffffffffu, max(two & 0xff80u, two >> 16));
+          if (most >= 0x80 && most < 0x7f80) ref_v = reference_above(most, 0);
+        }
         Pair y[NHW / 2];
         load_parts<kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, y);
         tc_fence_before();
         arrive_warp(&s_free[sb]);
 
-        // What this key's V scale does: y = x + lv, l gets p * 2^-lv.
-        const int ev = (int)(vbits >> 7) - 127;
-        const bool tiny = ev < kMinVExponent;
-        const int lv = max(ev, kMinVExponent);
-        float lvf = vbits > 0x7f80u ? CUDART_NAN_F : (float)lv;
-        const float inv_v = pow2(-min(lv, 126));
         uint32_t seen = valid ? 0xffffffffu : 0u;
         const bool tail = p.tree_masks != nullptr && key0 + nvalid > it.base;
         const int st = kt % S;
@@ -1012,12 +1048,20 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
           }
           if constexpr (L::KG > 1) named_barrier_sync(1 + L::KG, 128 * L::KG);  // both have read
           if (nan) {
-            lvf = CUDART_NAN_F;
+            vb = kNanScale;
             if (kg == 0)
 #pragma unroll 2
               for (int c = 0; c < D / 16; ++c) v_row[c] = make_uint4(0, 0, 0, 0);
           }
         }
+        // What this key's V scale does: y = x + lv, l gets p * 2^-lv.  Scales out of
+        // the band, NaN among them, are looked after below.
+        vb = valid ? vb & 0xff80u : ref_v + kBelow * 128;
+        const uint32_t in_band = vb - ref_v;
+        const bool odd = in_band > kBand;
+        const float lvf = fmaf(__uint_as_float(0x4b000000u + in_band), 1.f / 128,  // 2^23 + in_band
+                               -(65536.f + kBelow));
+        float inv_v = __uint_as_float(((127u + kBelow) << 23) - (in_band << 16));
         const Pair ks2 = pair(ks, ks), lv2 = pair(lvf, lvf);
 #pragma unroll
         for (int g = 0; g < NHW / 2; ++g) y[g] = fma2(y[g], mul2(pair_at(factors, g), ks2), lv2);
@@ -1036,33 +1080,79 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
           e[g] = both(add2(y[g], pair_at(refs, g)));
           top = fmax3(top, e[g].x, e[g].y);
         }
-        if (group_any(kg, top > kExceed)) {
+        if (group_any(kg, top > kExceed || unset || odd)) {
+          bool low = false, apart = false;  // this key, some of the tile's are added apart
+          const bool again = i == 0 && tail;
+          if (__builtin_expect(group_any(kg, odd || again), 0)) {
+            const bool v_nan = vb >= 0x7f80u;
+            const int of_warp =
+                __reduce_max_sync(0xffffffffu, seen != 0 && !v_nan ? (int)vb : 0);
+            if (lane == 0) marks[warp & 3] = of_warp;
+            named_barrier_sync(1 + kg, 128);
+            const int largest = max(max(marks[0], marks[1]), max(marks[2], marks[3]));
+            if (largest >= 0x80 && (again || ref_v == kNoScale || largest > ref_v + kBand)) {
+              // E moves, and the O^T so far with it.
+              const int old = ref_v;
+              ref_v = reference_above(largest, 0);
+              if (i > 0 && old != kNoScale) {
+                const int up = (ref_v - old) / 128;
+                const float shrink = up > 126 ? 0.f : pow2(-up);
+                ok = ok && mbar_wait(&p_free[(kt - 1) % PB], ((kt - 1) / PB) & 1, p.status);
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < (far ? kParts + 1 : kParts); ++c) {
+                  const uint32_t addr =
+                      tmem + L::kColO + (c < kParts ? c * NH : L::NO) + hb + lane_base;
+                  float o[NHW];
+                  tmem_load_small<NHW>(addr, o);
+#pragma unroll
+                  for (int g = 0; g < NHW; ++g) o[g] *= shrink;
+                  tmem_store_small<NHW>(addr, o);
+                }
+                tc_fence_before();
+              }
+            }
+            const int at = (int)vb - ref_v;
+            const int lv = min(max(at >> 7, 0), kAbove + kBelow) - kBelow;
+            const float by = v_nan ? CUDART_NAN_F : (float)lv - lvf;
+            inv_v = pow2(-lv);
+#pragma unroll
+            for (int g = 0; g < NHW / 2; ++g) {  // (-infinity: not seen)
+              if (e[g].x > -CUDART_INF_F) e[g].x += by;
+              if (e[g].y > -CUDART_INF_F) e[g].y += by;
+            }
+            low = seen != 0 && !v_nan && at < 0;
+            apart = group_any(kg, low);
+          }
           // The tile's maxima per row, then the rows whose reference moves:
           // lane r of each warp settles row r.
           float mine = 0.f;
 #pragma unroll
           for (int g = 0; g < NHW / 2; ++g) {
-            const float2 v = both(y[g]);
-            const float a = warp_max(v.x), b = warp_max(v.y);
+            const float a = warp_max(e[g].x), b = warp_max(e[g].y);
             if (row / 2 == g) mine = row & 1 ? b : a;
           }
           if (lane < NHW) tops[(warp & 3) * NHW + row] = mine;
           named_barrier_sync(1 + kg, 128);
           const float mt = fmax3(fmaxf(tops[row], tops[NHW + row]), tops[2 * NHW + row],
                                  tops[3 * NHW + row]);
-          const bool moves = mt + nm > kPlace;  // (all that have grown, now that some must)
-          const float alpha = moves ? ex2(kPlace - mt - nm) : 1.f;
-          if (moves) nm = kPlace - mt;
+          // (All that have grown, now that some must.)
+          const bool moves = mt > (unset ? -CUDART_INF_F : kPlace);
+          const float shift = moves ? kPlace - mt : 0.f;
+          nm += shift;
           if (lane < NHW) {
             refs[row] = nm;
-            alphas[row] = alpha;
+            shifts[row] = shift;
+            alphas[row] = unset ? 0.f : ex2(shift);  // (an unset row has no weights yet)
           }
+          unset = unset && mt == -CUDART_INF_F;
           const bool moved = __any_sync(0xffffffffu, moves);  // (orders the stores, too)
           __syncwarp();
 #pragma unroll
           for (int g = 0; g < NHW / 2; ++g) {
             l_part[g] = mul2(l_part[g], pair_at(alphas, g));
-            e[g] = both(add2(y[g], pair_at(refs, g)));
+            e[g] = both(add2(pair(e[g].x, e[g].y), pair_at(shifts, g)));
           }
           if (i > 0 && moved) {
             // O^T holds this item's tiles so far: rescaled once their MMAs are
@@ -1071,8 +1161,9 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kParts; ++c) {
-              const uint32_t addr = tmem + L::kColO + c * NH + hb + lane_base;
+            for (int c = 0; c < (far ? kParts + 1 : kParts); ++c) {
+              const uint32_t addr =
+                  tmem + L::kColO + (c < kParts ? c * NH : L::NO) + hb + lane_base;
               float o[NHW];
               tmem_load_small<NHW>(addr, o);
 #pragma unroll
@@ -1080,6 +1171,73 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
               tmem_store_small<NHW>(addr, o);
             }
             tc_fence_before();
+          }
+          if (__builtin_expect(apart, 0)) {
+            // Four keys at a time, the next of each warp: its weights into `tops`,
+            // then every thread adds its dimension of the four rows.  Rows of zeros
+            // are left out.  The sums get these weights here, the product none.
+            ok = ok && mbar_wait(&v_full[st], (kt / S) & 1, p.status);
+            named_barrier_sync(1 + kg, 128);  // the maxima have been read
+            const unsigned char* v_tile = sV + st * L::kTile;
+            uint32_t some = 0;
+            if (low && vb >= 0x80u) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                const uint4 w = reinterpret_cast<const uint4*>(v_tile + t * D)[(c + t) % (D / 16)];
+                some |= (w.x | w.y | w.z | w.w) & 0x7f7f7f7fu;
+              }
+            }
+            const int down = ((int)vb - ref_v) / 128;  // (below 0 where it is used)
+            const float v_rel = down < -126 ? 0.f : pow2(min(down, 0));
+            uint32_t todo = __ballot_sync(0xffffffffu, some != 0);
+#pragma unroll 1
+            for (;;) {
+              const int src = __ffs(todo) - 1;
+              if (lane == max(src, 0)) {
+                marks[warp & 3] = src < 0 ? -1 : t;
+                float* to = tops + (warp & 3) * NHW;
+#pragma unroll
+                for (int g = 0; g < NHW / 2; ++g) {
+                  to[2 * g] = ex2(e[g].x) * v_rel;
+                  to[2 * g + 1] = ex2(e[g].y) * v_rel;
+                }
+              }
+              __syncwarp();
+              if (!group_any(kg, src >= 0)) break;
+              float code[4];
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const int key = marks[w];
+                code[w] = key < 0 || !has_d ? 0.f : decode2(v_tile[swizzled<D>(key, d)]).x;
+              }
+#pragma unroll 1
+              for (int g = 0; g < NHW; g += 4) {
+                const uint32_t addr = tmem + L::kColFar + hb + g + lane_base;
+                float o[4] = {0.f, 0.f, 0.f, 0.f};
+                if (far) tmem_load_small<4>(addr, o);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  if (marks[w] < 0) continue;  // (its weights are none)
+                  const float4 x = *reinterpret_cast<const float4*>(tops + w * NHW + g);
+                  o[0] = fmaf(x.x, code[w], o[0]);
+                  o[1] = fmaf(x.y, code[w], o[1]);
+                  o[2] = fmaf(x.z, code[w], o[2]);
+                  o[3] = fmaf(x.w, code[w], o[3]);
+                }
+                tmem_store_small<4>(addr, o);
+              }
+              far = true;
+              todo &= todo - 1;
+              named_barrier_sync(1 + kg, 128);  // read, before the next are written
+            }
+            if (low) {
+#pragma unroll
+              for (int g = 0; g < NHW / 2; ++g) {
+                l_part[g] = fma2(pair(ex2(e[g].x), ex2(e[g].y)), pair(inv_v, inv_v), l_part[g]);
+                e[g] = make_float2(-CUDART_INF_F, -CUDART_INF_F);
+              }
+            }
+            __syncwarp();
           }
         }
         // The weights of this key: rounded to fp16, then split in three.  The
@@ -1094,10 +1252,6 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
           e[g] = make_float2(ex2(e[g].x), ex2(e[g].y));
           l_part[g] = fma2(pair(e[g].x, e[g].y), inv2, l_part[g]);
           h[g] = Cvt<__half>::from_float2(e[g].x, e[g].y);
-        }
-        if (tiny) {
-#pragma unroll
-          for (int g = 0; g < NHW / 2; ++g) h[g] = 0u;
         }
         uint32_t part[kParts][NHW / 4];
 #pragma unroll
@@ -1162,14 +1316,23 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
       if (lane < NHW) alphas[row] = l == 0.f ? 0.f : __fdividef(1.f, l);
       __syncwarp();
       constexpr int kOut = NHW < 8 ? NHW : 8;
+      // 2^E
+      const float v_scale = ref_v == kNoScale ? 1.f : pow2((ref_v >> 7) - 127 + kBelow);
 #pragma unroll 1
       for (int g = 0; g < NHW && g < there; g += kOut) {
         Pair o[kOut / 2];
         load_parts<kParts, NH, kOut>(tmem + L::kColO + hb + g + lane_base, o);
+        if (far) {
+          float x[kOut];
+          tmem_load_small<kOut>(tmem + L::kColFar + hb + g + lane_base, x);
+#pragma unroll
+          for (int u = 0; u < kOut / 2; ++u) o[u] = add2(o[u], pair(x[2 * u], x[2 * u + 1]));
+        }
 #pragma unroll
         for (int u = 0; u < kOut; ++u) {
           const float2 v = both(o[u / 2]);
-          const float inv = alphas[g + u], x = inv == 0.f ? 0.f : (u & 1 ? v.y : v.x) * inv;
+          const float inv = alphas[g + u],
+                      x = inv == 0.f ? 0.f : (u & 1 ? v.y : v.x) * inv * v_scale;
           if (!ok || !has_d || g + u >= there) continue;
           if (it.nparts_seq == 1)
             static_cast<T*>(p.out)[(size_t)rows[g + u] * D + d] = static_cast<T>(x);
@@ -1180,7 +1343,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
       tc_fence_before();
       if (ok && it.nparts_seq > 1 && t < NHW && t < there) {
         const size_t r = (size_t)rows[t] * p.num_parts + it.part;
-        p.ws_m[r] = -nm;
+        p.ws_m[r] = l == 0.f ? kNoRef : -nm;
         p.ws_l[r] = l;
       }
       arrive_warp(&m_free[mb]);  // the item's rows are read
@@ -1253,18 +1416,25 @@ __global__ void __launch_bounds__(128) attn_fp8_reduce_kernel(const AttnFp8Param
   float M = lane < np ? m0 : -CUDART_INF_F;
   for (int i = lane + 32; i < np; i += 32) M = fmaxf(M, __ldcg(mrow + i));
   M = warp_max(M);
-  float sum = 0.f, acc[E];
+  auto weight = [&](int i) {
+    if (i >= np) return 0.f;
+    const float l = i < 32 ? l0 : __ldcg(lrow + i), m = i < 32 ? m0 : __ldcg(mrow + i);
+    return l == 0.f ? 0.f : l * exp2f(m - M);
+  };
+  // (The sum first: a weight of more than 1 times an output may pass the range.)
+  float sum = 0.f;
+  for (int i = lane; i < np; i += 32) sum += weight(i);
+#pragma unroll
+  for (int mk = 16; mk >= 1; mk >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mk);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int base = 0; base < np; base += 32) {
-    const int i = base + lane;
-    const float l = base == 0 ? l0 : (i < np ? __ldcg(lrow + i) : 0.f);
-    const float m = base == 0 ? m0 : (i < np ? __ldcg(mrow + i) : 0.f);
-    const float mine = i >= np || l == 0.f ? 0.f : l * exp2f(m - M);
+    const float mine = weight(base + lane) * inv;
     const int n = min(32, np - base);
     auto add = [&](int k, const float2* o) {
       const float w = __shfl_sync(0xffffffffu, mine, k);
-      sum += w;
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
         acc[2 * e] = fmaf(w, o[e].x, acc[2 * e]);
@@ -1282,11 +1452,9 @@ __global__ void __launch_bounds__(128) attn_fp8_reduce_kernel(const AttnFp8Param
       add(k, o);
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * E);
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e)
-    out[e] = Cvt<T>::from_float2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  for (int e = 0; e < E / 2; ++e) out[e] = Cvt<T>::from_float2(acc[2 * e], acc[2 * e + 1]);
 }
 
 // The cache's rows of D codes: boxes of a block's rows of one head, D-byte

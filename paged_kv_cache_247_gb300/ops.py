@@ -723,8 +723,10 @@ def paged_attn_decode_fp8(out, q, k_cache, v_cache, k_scales, v_scales, block_ta
     """:func:`paged_attn_decode` over a cache held in 8 bits
     (:func:`kv_append_fp8`).  ``partition_size``: 0 or a multiple of 128;
     ``workspace`` (any CUDA tensor of at least :func:`decode_fp8_workspace_size`
-    bytes) is allocated here with torch if omitted and needed.  Writes ``out``
-    ([S, Hq, D]) and returns it."""
+    bytes) is allocated here with torch if omitted and needed.  Sums are 32-bit;
+    softmax weights have 11 bits, and those below 2^-31 of their row's largest
+    (2^-24 where V rows differ in size) may be lost.  Writes ``out`` ([S, Hq, D])
+    and returns it."""
     dev, (S, Hq, Hkv, D, B, NB) = _fp8_attn(out, q, k_cache, v_cache, k_scales, v_scales,
                                             block_tables, context_lens, workspace)
     if q.shape[0] != S:

@@ -1,26 +1,29 @@
 """Attention over a cache held in 8 bits where the types' ranges are used: query
-elements far below the largest of their row, many weights far below the largest.
-Cases are those of test_gpu_fp8.
+elements far below the largest of their row, many weights far below the largest,
+V rows whose sizes differ by any power of two.  Cases are those of test_gpu_fp8.
 
 Tolerance.  As there, |err| <= eps / 2 |out| + (2 dx + 2^-17 + 2^-11) sum_t p_t |v_t|,
 but each position's lost weight by itself, and the fp32 sums' roundings with the
 length: of O^T, which takes up 32 positions at a time, at most 2^-23 each, and of the
 weights, 128 of them side by side, 2^-24:
   (n / 32) 2^-23 + (n / 128) 2^-24 <= n 2^-27
-of sum_t p_t |v_t|.  A weight times its V row's scale is rounded to fp16 where the
-largest such product stands at 2^6 or more: its own half step is 2^-25, so that a
-position loses at most 2^-31 of the largest product over its own scale:
-  lost_t = min(p_t, 2^-31 max_s p_s 2^e_s / 2^e_t).
+of sum_t p_t |v_t|.  A weight times its V row's scale is rounded to fp16, whose own
+half step is 2^-25, where the largest such product has come to 2^6 or more: 2^-31 of
+it.  The scales that enter the product lie within 2^-6 and 2 of their reference, so
+that a position loses at most 2^(7 - 31) of the largest weight, 2^-31 where all rows
+have the same scale, and between, where they differ by 2^k, 2^(k + 1) <= 2^(2 k) times that:
+  lost_t = min(p_t, 2^(min(7, 2 k) - 31) max_s p_s).
 """
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import oracle
 import paged_kv_cache_247_gb300 as pkv
-from test_gpu_fp8 import Case, _clean_status, _gen  # noqa: F401 (an autouse fixture)
+from test_gpu_fp8 import Case, _clean_status, _gen, _random_masks  # noqa: F401 (an autouse fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -60,9 +63,10 @@ def reference(c, held=0.0):
         dx = abs(c.scale) * torch.where(seen, a, 0.0).amax(-1, keepdim=True)
         p = torch.softmax(x, -1).nan_to_num(0.0)                              # (nothing seen: zeros)
         o, size = p @ v[:, None], p @ v[:, None].abs()
-        e2 = scales[:, None].transpose(-1, -2)                                # [H, 1, 1, n]
-        most = (p * e2).amax(-1, keepdim=True) / e2
-        lost = torch.minimum(p, 2.0 ** -31 * most) @ v[:, None].abs()
+        e = torch.where((v != 0).any(-1), torch.log2(scales[..., 0]), math.nan)  # (rows of zeros lose nothing)
+        e = e[~e.isnan()]
+        k = float(e.max() - e.min()) if len(e) else 0.0
+        lost = torch.minimum(p, 2.0 ** (min(7.0, 2 * k) - 31) * p.amax(-1, keepdim=True)) @ v[:, None].abs()
         b = torch.finfo(c.dt).eps / 2 * o.abs() + (2 * dx + 2.0 ** -17 + 2.0 ** -11 + n * 2.0 ** -27) * size + lost
         b += 2.0 ** -25 if c.dt == torch.float16 else 2.0 ** -134              # half a subnormal step
         out[lo:hi] = o.permute(2, 0, 1, 3).reshape(L, hq, c.D)
@@ -138,3 +142,115 @@ def test_a_flat_tail_of_weights(cuda_device, dtype, gap, rows, D):
     c.v[0, 0, 0] = 0.9
     c.v = c.v.to(c.dt)
     check(c, partition_size=-(-n // 128) * 128)
+
+
+# ---- V rows ------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("rows,D", [(4, 128), (12, 64), (32, 128), (64, 64)])
+@pytest.mark.parametrize("at", [0, 20000, 32767])
+@pytest.mark.parametrize("dtype,top", [("fp16", 1.0), ("fp16", 64.0), ("bf16", 400.0), ("fp16", 6e4),
+                                       ("bf16", 1e6), ("bf16", 2.0 ** 100)])
+def test_one_large_element_of_v(cuda_device, dtype, top, at, rows, D):
+    """One position of great weight has a V row with a single large element, the
+    other positions' weights add up to as much: every other dimension is theirs."""
+    n = 32768
+    c = case(dtype, rows, D, [n])
+    heavy(c, n, at, 15)
+    c.v = 0.5 + 0.6 * (torch.rand((n, 1, D), generator=_gen(2), device="cuda") - 0.5)
+    c.v[at, 0, 0] = top
+    c.v = c.v.to(c.dt)
+    check(c, partition_size=n)
+
+
+SIZES = [("fp16", -14, 12), ("bf16", -14, 12), ("bf16", -60, 55), ("bf16", -120, -30), ("bf16", 20, 115)]
+
+
+@pytest.mark.parametrize("rows,D", [(1, 128), (8, 64), (16, 128), (27, 64), (64, 128)])
+@pytest.mark.parametrize("dtype,lo,hi", SIZES)
+def test_v_rows_of_every_size(cuda_device, dtype, lo, hi, rows, D):
+    """V rows of any two sizes, zero rows among them, each row in an eighth of the
+    dimensions, so that every dimension sums rows of other sizes."""
+    lens = [700, 130, 1, 257]
+    n = sum(lens)
+    c = case(dtype, rows, D, lens, seed=rows)
+    e = torch.randint(lo, hi + 1, (n, 1, 1), generator=_gen(5), device="cuda").double()
+    own = (torch.arange(D, device="cuda") % 8)[None, None] == torch.randint(0, 8, (n, 1, 1), generator=_gen(6),
+                                                                           device="cuda")
+    v = torch.randn((n, 1, D), generator=_gen(7), device="cuda", dtype=torch.float64) * torch.exp2(e) * own
+    v[::9] = 0
+    c.v = v.to(c.dt)
+    check(c)
+    check(c, partition_size=128)
+
+
+@pytest.mark.parametrize("dtype,lo,hi", SIZES)
+def test_v_rows_of_every_size_under_trees(cuda_device, dtype, lo, hi):
+    lens, drafts = [300, 64, 129, 40], [16, 64, 9, 3]
+    c = Case(3, dtype, 4, 2, 64, 16, lens, drafts, _random_masks(np.random.default_rng(2), drafts))
+    e = torch.randint(lo, hi + 1, (sum(lens), 2, 1), generator=_gen(5), device="cuda").double()
+    own = torch.rand((sum(lens), 2, 64), generator=_gen(8), device="cuda") < 0.2
+    c.v = (torch.randn((sum(lens), 2, 64), generator=_gen(7), device="cuda", dtype=torch.float64) * torch.exp2(e)
+           * own).to(c.dt)
+    check(c)
+    check(c, partition_size=128)
+
+
+@pytest.mark.parametrize("rows,D", [(4, 128), (16, 64), (48, 128)])
+@pytest.mark.parametrize("size", [-126, -100, -70, -62, 60, 75, 110])
+def test_v_rows_of_one_size_beside_zeros(cuda_device, size, rows, D):
+    """Half of the positions hold zeros, the others rows of one size."""
+    c = case("bf16", rows, D, [300, 128, 5])
+    c.v = torch.randn((433, 1, D), generator=_gen(4), device="cuda", dtype=torch.float64) * 2.0 ** size
+    c.v[::2] = 0
+    c.v = c.v.to(c.dt)
+    check(c)
+    check(c, partition_size=128)
+
+
+def test_tiles_of_zeros_before_and_after(cuda_device):
+    """Whole tiles of zero rows at either end, and a cache of nothing else."""
+    c = case("bf16", 8, 128, [640, 384, 256])
+    c.v[:256] = 0
+    c.v[640 + 128:1024] = 0
+    c.v[1024:] = 0
+    got = check(c)
+    assert not got[2].any()
+    check(c, partition_size=128)
+
+
+def test_partitions_of_the_largest_values(cuda_device):
+    """Partial outputs near the end of bf16's range, joined without passing it."""
+    c = case("bf16", 8, 64, [1500])
+    c.v = (torch.randn((1500, 1, 64), generator=_gen(4), device="cuda", dtype=torch.float64) * 2.0 ** 124).to(c.dt)
+    c.k *= 0.01
+    got = check(c, partition_size=128)
+    assert torch.isfinite(got).all()
+
+
+def test_a_huge_row_that_some_queries_do_not_see(cuda_device):
+    """A drafted V row far above the rest: queries that do not see it get what
+    the rest gives, those that do get theirs."""
+    for D, rows, up in ((64, 4, 90), (128, 2, 110)):
+        lens, drafts = [200, 60], [12, 5]
+        masks = [(1 << j) | 1 for j in range(12)] + [1 << j for j in range(5)]
+        c = Case(4, "bf16", rows, 1, D, 16, lens, drafts, masks)
+        c.v = c.v.double()
+        c.v[188 + 6] *= 2.0 ** up
+        c.v[200 + 57] *= 2.0 ** up
+        c.v = c.v.to(c.dt)
+        check(c)
+        check(c, partition_size=128)
+
+
+def test_a_scale_of_zero_gives_the_mean(cuda_device):
+    """Logits that are all zero: every output is the mean of the V rows."""
+    c = Case(21, "fp16", 4, 2, 64, 16, [130, 64, 3])
+    c.scale = 0.0
+    got = check(c)
+    values = torch.from_numpy(oracle.e4m3_values()).cuda()
+    at = c.slots[:130]
+    v = values[c.caches[1].view(torch.uint8)[at // 16, :, at % 16].long()] * c.caches[3][at // 16, :, at % 16].double()
+    mean, size = v.mean(0), v.abs().mean(0)
+    for h in range(4):
+        assert ((got[0, h] - mean[h // 2]).abs() <= 2.0 ** -10 * size[h // 2] + 2.0 ** -25).all()
