@@ -1149,6 +1149,7 @@ pkv_status_t attn_fp8_impl(void* out, const void* q, int total_queries, const in
   p.block_size = block_size;
   p.num_blocks = num_blocks;
   p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax is evaluated with exp2
+  p.sms = device_sms();
   p.chunks = plan.chunks;
   p.partition_size = plan.partition;
   p.num_parts = (int)plan.parts;

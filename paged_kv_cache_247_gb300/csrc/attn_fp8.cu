@@ -54,8 +54,8 @@
 // query head of the group and one of the sequence's queries.  Two CTAs per SM (one
 // from 33 rows on) go through the items; their rings, barriers and tensor memory
 // flow from item to item, and an SM whose items are short takes more of them:
-// the launch has a CTA per item, and a running one takes over those that have
-// not started.  Warps:
+// the launch has a CTA per item, and where the device does not hold all of them a
+// running one takes over those that have not started.  Warps:
 //
 //   key warpgroups (one; two and four, each with 16 rows, for more than 16 and 32):
 //              thread t has key t of the tile: scales, logits, weights, and at
@@ -577,7 +577,7 @@ __device__ __forceinline__ float split_row(uint4 x, int row, int c, unsigned cha
 template <typename T, int NH, int D>
 __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
     attn_fp8_kernel(const AttnFp8Params p, const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap vmap, int num_items) {
+                    const __grid_constant__ CUtensorMap vmap, int num_items, bool takes) {
   using L = Shape<NH, D>;
   constexpr int S = L::kStages, SB = L::SB, PB = kBufs, SC = L::kScaleStages, NHW = L::NHW,
                 QB = L::kQBufs;
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
     int j = blockIdx.x, n = 0, asked = 0;
     bool ok = true;
     while (ok && j >= 0) {
-      if (lane == 0) {
+      if (takes && lane == 0) {
         mbar_arrive_expect_tx(ticket, 16);
         take_cta(answer, ticket);
       }
@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
                                             w % kWords] = make_uint4(0, 0, 0, 0);
         }
       }
+      if (!takes) break;
       if (!ok || !wait_warp(ticket, asked & 1, p.status)) {
         mbar_drain(ticket, asked & 1);  // the answer lands before the CTA leaves
         ok = false;
@@ -1498,8 +1499,11 @@ cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CU
   }
   const int items = p.num_seqs * p.num_kv_heads * p.num_parts * p.chunks;
   const int ctas = std::min(items, kMostCtas);
+  // Where the device holds all CTAs at once, none takes over another's: the first to
+  // run would take those that are about to start, and leave their SMs idle.
+  const bool takes = ctas > p.sms * L::kPerSm;
   err = launch_overlapped(attn_fp8_kernel<T, NH, D>, dim3(ctas), dim3(L::kThreads), L::kBytes,
-                          stream, p, km, vm, items);
+                          stream, p, km, vm, items, takes);
   if (err != cudaSuccess || p.num_parts <= 1) return err;
   const long long rows = (long long)p.total_queries * p.num_q_heads;
   return launch_overlapped(attn_fp8_reduce_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)),

@@ -340,6 +340,7 @@ struct AttnFp8Params {
   int block_size;
   int num_blocks;
   float qscale;  // scale * log2(e)
+  int sms;             // of the device
   int chunks;          // work items of up to kFp8Rows rows per (sequence, KV head, partition)
   int partition_size;  // multiple of 128
   int num_parts;       // ceil(max_context_len / partition_size), >= 1
