@@ -1026,39 +1026,49 @@ struct Fp8Plan {
 };
 
 // Tiles per partition for `units` (sequence, KV head, chunk of rows) triples of
-// `rows` query rows each over contexts of `tiles` tiles: the split whose rounds of
-// items are done soonest on the CTAs the device holds (two per SM up to 32 rows,
-// else one).  An item costs its tiles and some more; a round that leaves CTAs out
-// is faster, down to `alone`; a split call pays for its partial outputs, written
-// and read again, and a launch.  Measured over all splits of a context (us, the
-// chosen one first): 4 x 8,192 positions, 8 heads of 64 rows, 16 tiles 41, 8 tiles
-// 47, 64 94; 1 x 32,768, 8 heads of 4 rows, 16 tiles 29, 64 57, 256 186; 32 x
-// 4,096, 8 heads of 64 rows, unsplit 108, 16 tiles 125; 64 x 8,192, 8 heads of 4
-// rows, unsplit 158, 32 tiles 171; 32 x 4,096, 4 heads of 16 rows, unsplit 45, 16
-// tiles 53.
-long long fp8_partition_tiles(double units, double rows, int head_dim, long long tiles) {
-  const bool wide = rows > 32;
-  const double slots = (wide ? 1.0 : 2.0) * device_sms();
-  const double alone = wide ? 0.75 : rows > 8 && rows <= 16 ? 0.45 : 0.6;
-  const double item = rows > 16 ? 2.5 : 1.0;
-  const double tile_us = head_dim == 128 ? 1.5 : (rows > 16 ? 1.2 : 0.8);
-  const double part_us = units * std::min(rows, (double)pkv::kFp8Rows) * head_dim * 8.0 / 6.8e6;
-  double best_cost = 0.0;
-  long long best = tiles;
+// `rows` query rows each over contexts of `tiles` tiles: the split that a model of
+// the call's time, in us, finds shortest on the CTAs that the device holds (two
+// per SM up to 32 rows, else one):
+//   * an item takes its tiles and two more (its start and its output), 1.5 us each,
+//     in as many rounds as the items fill; a round that leaves CTAs out is shorter,
+//     to 0.8 of a full one at the least (the rest have HBM and their SM to themselves);
+//   * a split call takes 3 us for the launch that joins the partial outputs, their
+//     bytes, written and read, and 0.2 us a partition (a warp goes through a row's
+//     partitions one after another).
+// The five numbers are a fit to all splits of 456 calls (1-512 units of 1-64 rows,
+// head_dim 64 and 128, contexts of 1,024-65,536): what the model chooses takes
+// 1.02 times the fastest in the mean (1.15 at most), no split 1.9 times; constants by
+// classes of rows and no time per partition: 1.06 and 1.75.  For example (us, the
+// chosen one first): 4 x 16,384 positions, 8 heads of 64 rows, 32 tiles 64, 15 tiles
+// 70, unsplit 178; 1 x 65,536, one head of 4 rows, 9 tiles 25, 3 tiles 39, unsplit 364.
+// Above 16 partitions the search takes steps of a sixteenth, and the numbers that fill
+// one, two and three rounds (66 evaluations at most; all of them choose no better).
+long long fp8_partition_tiles(long long units, long long rows, int head_dim, long long tiles) {
+  constexpr double kTileUs = 1.5, kItemTiles = 2.0, kLeast = 0.8, kJoinUs = 3.0, kPartUs = 0.2;
+  const long long slots = (rows > 32 ? 1 : 2) * (long long)device_sms();
+  const double part_us =
+      kPartUs + (double)units * (double)std::min<long long>(rows, pkv::kFp8Rows) * head_dim * 8.0 / 6.8e6;
   // more than about three rounds of items never pays: the search stops there
-  const long long most = std::min(tiles, (long long)(3.0 * slots / units) + 1);
-  for (long long parts = 1; parts <= most; ++parts) {
-    const long long pt = (tiles + parts - 1) / parts;
-    if ((tiles + pt - 1) / pt != parts) continue;  // the same partition as fewer parts
-    const double items = units * (double)parts, rounds = floor(items / slots);
-    const double rest = items - rounds * slots;
-    const double cost = ((double)tiles / (double)parts + item) *
-                            (rounds + (rest > 0.0 ? fmax(rest / slots, alone) : 0.0)) +
-                        (parts > 1 ? (3.0 + (double)parts * part_us) / tile_us : 0.0);
-    if (parts == 1 || cost < best_cost) {
-      best_cost = cost;
+  const long long most = std::min(tiles, 3 * slots / units + 1);
+  double best_us = 0.0;
+  long long best = tiles;
+  for (long long parts = 1; parts <= most;) {
+    const long long pt = (tiles + parts - 1) / parts, real = (tiles + pt - 1) / pt;
+    const long long items = units * real, rest = items % slots;
+    const double rounds = (double)(items / slots) + (rest ? fmax((double)rest / slots, kLeast) : 0.0);
+    const double us = kTileUs * ((double)pt + kItemTiles) * rounds +
+                      (real > 1 ? kJoinUs + (double)real * part_us : 0.0);
+    if (parts == 1 || us < best_us) {
+      best_us = us;
       best = pt;
     }
+    // (more parts than these with the same partition are the same split)
+    long long next = std::max(parts + 1 + parts / 16, real + 1);
+    for (long long k = 1; k <= 3; ++k) {
+      const long long full = k * slots / units;
+      if (parts < full && full < next) next = full;
+    }
+    parts = next;
   }
   return best;
 }
@@ -1081,7 +1091,7 @@ bool fp8_plan(int total_queries, int max_query_len, int num_seqs, int num_q_head
     constexpr int kQuantum = pkv::kTcPartitionQuantum;
     const long long tiles = std::max(1, (max_context_len + kQuantum - 1) / kQuantum);
     plan->partition =
-        (int)(fp8_partition_tiles((double)units, (double)rows, head_dim, tiles) * kQuantum);
+        (int)(fp8_partition_tiles(units, rows, head_dim, tiles) * kQuantum);
   }
   plan->parts = num_parts_for(max_context_len, plan->partition);
   return plan->parts <= 0x7fffffffLL / units;
