@@ -14,6 +14,7 @@
 // and three ahead 68 and 60, four CTAs per SM instead of three 68.)
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -169,7 +170,37 @@ __global__ void __launch_bounds__(kThreads, 3)
       float sum = both(sq).x + both(sq).y;
 #pragma unroll
       for (int mk = kUpr / 2; mk >= 1; mk >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mk);
-      const float r = rsqrtf(sum * (1.f / D) + p.eps);
+      float mean = sum * (1.f / D) + p.eps;
+      // bf16 reaches squares that 32 bits do not hold: such a row is scaled by a power
+      // of two first, eps with it.
+      const bool held = mean >= 0x1p-100f && mean <= 0x1p+120f;
+      if (std::is_same<T, __nv_bfloat16>::value && __any_sync(0xffffffffu, !held)) {
+        float top = sqrtf(p.eps);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 u = both(x[j]), v = both(y[j]);
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y))));
+        }
+#pragma unroll
+        for (int mk = kUpr / 2; mk >= 1; mk >>= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, mk));
+        // 2^-e of top = 1.m 2^e, within what a normal number holds; 1 for a row that is held
+        const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+        const float by = held ? 1.f : __uint_as_float((254u - e) << 23);
+        const Pair by2 = pair(by, by);
+        sq = pair(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] = mul2(x[j], by2);
+          y[j] = mul2(y[j], by2);
+          sq = fma2(x[j], x[j], fma2(y[j], y[j], sq));
+        }
+        sum = both(sq).x + both(sq).y;
+#pragma unroll
+        for (int mk = kUpr / 2; mk >= 1; mk >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mk);
+        mean = sum * (1.f / D) + p.eps * by * by;
+      }
+      const float r = rsqrtf(mean);
       const Pair r2 = pair(r, r);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
