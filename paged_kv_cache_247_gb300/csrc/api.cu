@@ -1012,7 +1012,7 @@ pkv_status_t pkv_qk_norm_rope(void* q_out, int64_t q_out_stride, void* k_out, in
   p.interleaved = interleaved != 0;
   p.eps = eps;
   p.factor = attn_factor;
-  const cudaError_t err = pkv::launch_qk_norm_rope(p, num_tokens, head_dim, dtype,
+  const cudaError_t err = pkv::launch_qk_norm_rope(p, num_tokens, head_dim, dtype, device_sms(),
                                                    reinterpret_cast<cudaStream_t>(stream));
   return err != cudaSuccess ? cuda_fail(err) : PKV_OK;
 }

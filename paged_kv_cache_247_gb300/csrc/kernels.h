@@ -309,7 +309,7 @@ struct NormRopeParams {
 };
 
 cudaError_t launch_qk_norm_rope(const NormRopeParams& p, int num_tokens, int head_dim, int dtype,
-                                cudaStream_t stream);
+                                int sms, cudaStream_t stream);
 
 // Attention over an 8-bit cache.  query_start == nullptr: one query per
 // sequence, the whole context seen.  Otherwise the last positions of each

@@ -255,11 +255,11 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const NormRopeParams& p, int num_tokens, cudaStream_t stream) {
+cudaError_t launch_typed(const NormRopeParams& p, int num_tokens, int sms, cudaStream_t stream) {
   // Eight tokens per CTA share its sines and cosines evenly (four: 63 us instead of
   // 58 at 16,384 tokens); fewer where that would leave SMs without a CTA.
   int tokens = kTokens;
-  while (tokens > 1 && num_tokens < 2 * 152 * tokens) tokens /= 2;
+  while (tokens > 1 && num_tokens < 2 * sms * tokens) tokens /= 2;
   const dim3 grid((num_tokens + tokens - 1) / tokens), block(kThreads);
   if (p.interleaved)
     return launch_overlapped(qk_norm_rope_kernel<T, D, kInterleaved>, grid, block, 0, stream, p,
@@ -274,12 +274,12 @@ cudaError_t launch_typed(const NormRopeParams& p, int num_tokens, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const NormRopeParams& p, int num_tokens, int head_dim, int dtype,
-                                cudaStream_t stream) {
+                                int sms, cudaStream_t stream) {
   if (dtype == PKV_F16)
-    return head_dim == 64 ? launch_typed<__half, 64>(p, num_tokens, stream)
-                          : launch_typed<__half, 128>(p, num_tokens, stream);
-  return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(p, num_tokens, stream)
-                        : launch_typed<__nv_bfloat16, 128>(p, num_tokens, stream);
+    return head_dim == 64 ? launch_typed<__half, 64>(p, num_tokens, sms, stream)
+                          : launch_typed<__half, 128>(p, num_tokens, sms, stream);
+  return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(p, num_tokens, sms, stream)
+                        : launch_typed<__nv_bfloat16, 128>(p, num_tokens, sms, stream);
 }
 
 }  // namespace pkv
