@@ -543,8 +543,11 @@ pkv_status_t pkv_kv_compact(
  *   e the smallest integer >= -126 with max |element of the row| <= 448 * 2^e.
  * The division by a power of two is exact, so each element is rounded once, to
  * nearest even, and a row gives the same bits wherever it is written; read back
- * and appended again it keeps its values.  A row with a NaN or an infinity is
- * held as NaN as a whole (scale NaN, codes 0).
+ * and appended again it keeps its values.  (Elements that round above their type:
+ * an fp16 one from 63,488 on is held as 65,536, a bf16 one from 1.9375 2^127 on as 2^128,
+ * and is infinity where it is read in that type, in an output of the attention calls,
+ * too, that comes to it; appended again, its row is NaN.)  A row with a NaN or an
+ * infinity is held as NaN as a whole (scale NaN, codes 0).
  *
  * The attention calls read scales as powers of two (or NaN): one of V that comes
  * from elsewhere and is none counts as the power of two below it, an infinity as NaN.
@@ -581,8 +584,8 @@ pkv_status_t pkv_kv_append_fp8(
 /* Read blocks back into 16 bits: for each pair i, block src_dst_pairs[2i] of
  * the 8-bit caches, every row of it, into block src_dst_pairs[2i + 1] of k_out
  * and v_out [num_out_blocks, num_kv_heads, block_size, head_dim].  bf16 holds
- * the products exactly (down to its smallest normal number), fp16 rounds them
- * once.  A source may be read into several blocks; destinations must be
+ * the products exactly (from its smallest normal number to its largest), fp16
+ * rounds them once, to infinity from 65,520 on.  A source may be read into several blocks; destinations must be
  * distinct.  Ids outside the pools skip the pair and flag PKV_DEV_BAD_BLOCK_ID.
  * Errors as pkv_kv_append_fp8. */
 pkv_status_t pkv_block_read_fp8(

@@ -556,8 +556,9 @@ def kv_append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping):
     codes in ``k_cache`` / ``v_cache`` ([NB, Hkv, B, D]) and one scale in
     ``k_scales`` / ``v_scales`` (bfloat16 [NB, Hkv, B, 1]), the smallest power
     of two that leaves no element above 448, so that ``cache.float() *
-    scales.float()`` are the rows, each element rounded once.  A row with a NaN
-    or an infinity is NaN as a whole."""
+    scales.float()`` are the rows, each element rounded once (a float16 one from
+    63,488 on to 65,536, which float16 itself does not hold).  A row with a NaN or an
+    infinity is NaN as a whole."""
     if not isinstance(k, torch.Tensor) or k.dtype not in _DTYPE_CODE or k.dim() != 3:
         raise ValueError("k must be float16 or bfloat16 with 3 dimensions")
     dtype, shape = k.dtype, k.shape
@@ -579,8 +580,10 @@ def block_read_fp8(k_out, v_out, k_cache, v_cache, k_scales, v_scales, src_dst_p
     """Read blocks of a cache held in 8 bits back into 16 bits: block ``src`` of
     the caches into block ``dst`` of ``k_out`` and ``v_out`` (float16 or
     bfloat16 [blocks, Hkv, B, D]) for each pair of ``src_dst_pairs`` (int64
-    [P, 2] CUDA tensor; destinations distinct).  :func:`paged_attn_prefill`
-    attends over them through a table of the destinations."""
+    [P, 2] CUDA tensor; destinations distinct).  bfloat16 holds the values
+    exactly; float16 rounds them once, what is held as 65,520 and more to infinity.
+    :func:`paged_attn_prefill` attends over them through a table of the
+    destinations."""
     _cuda(k_out, "k_out", ndim=4)
     dtype = k_out.dtype
     if dtype not in _DTYPE_CODE:
