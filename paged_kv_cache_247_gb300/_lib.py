@@ -22,7 +22,6 @@ STATUS = {
     3: "PKV_ERR_WORKSPACE_TOO_SMALL", 4: "PKV_ERR_OUT_OF_BLOCKS", 5: "PKV_ERR_CUDA",
     6: "PKV_ERR_UNKNOWN_SEQ", 7: "PKV_ERR_SEQ_EXISTS", 8: "PKV_ERR_TABLE_TOO_SMALL",
 }
-PKV_ERR_WORKSPACE_TOO_SMALL = 3
 PKV_F16, PKV_BF16 = 0, 1
 DEV_BAD_BLOCK_ID, DEV_BAD_CONTEXT_LEN, DEV_BAD_SLOT, DEV_WAIT_TIMEOUT = 1, 2, 4, 8
 DEV_BAD_KEEP = 16

@@ -6,6 +6,7 @@ happens in the library's kernels; nothing here computes a result.
 """
 
 import ctypes
+import functools
 
 import numpy as np
 import torch
@@ -702,20 +703,29 @@ def _fp8_attn(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, contex
     return dev, (S, Hq, Hkv, D, B, NB)
 
 
+@functools.lru_cache(maxsize=256)
+def _fp8_workspace(dev, *sizes):
+    """Bytes of scratch for a call of these sizes on device ``dev``, the current one
+    (the layers of a step ask for the same; 0 for sizes that the call refuses)."""
+    n = _lib.load().pkv_tree_fp8_workspace_size(*sizes)
+    return 0 if n == _SIZE_T_MAX else n
+
+
 def _launch_fp8_attn(name, dev, q, workspace, sizes, *args):
-    """_launch with the workspace last.  Without one the call is made as it is,
-    which is all there is to it unless the context is split; then it comes back
-    at once, before anything runs, and is made again with one of torch's."""
+    """_launch with the workspace last, one of torch's where the call needs one and
+    gets none."""
     fn = getattr(_lib.load(), name)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _launch_fp8_attn(name, dev, q, workspace, sizes, *args)
     stream = torch._C._cuda_getCurrentRawStream(dev)
     if workspace is None:
+        needed = _fp8_workspace(dev, *sizes)
+        if needed:
+            workspace = q.new_empty(needed >> 1)
+    if workspace is None:
         st = fn(*args, None, 0, stream)
-        if st == _lib.PKV_ERR_WORKSPACE_TOO_SMALL:
-            workspace = q.new_empty(tree_fp8_workspace_size(*sizes) >> 1)
-    if workspace is not None:
+    else:
         st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
     if st:
         _lib.check(st, name)
