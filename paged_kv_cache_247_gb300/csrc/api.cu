@@ -1032,19 +1032,23 @@ struct Fp8Plan {
 //   * an item takes its tiles and two more (its start and its output), 1.5 us each,
 //     in as many rounds as the items fill; a round that leaves CTAs out is shorter,
 //     to 0.8 of a full one at the least (the rest have HBM and their SM to themselves);
-//   * a split call takes 3 us for the launch that joins the partial outputs, their
+//   * a split call takes 7 us for the launch that joins the partial outputs, their
 //     bytes, written and read, and 0.2 us a partition (a warp goes through a row's
 //     partitions one after another).
-// The five numbers are a fit to all splits of 456 calls (1-512 units of 1-64 rows,
-// head_dim 64 and 128, contexts of 1,024-65,536): what the model chooses takes
-// 1.02 times the fastest in the mean (1.15 at most), no split 1.9 times; constants by
-// classes of rows and no time per partition: 1.06 and 1.75.  For example (us, the
+// The numbers are a fit to all splits of 456 calls (1-512 units of 1-64 rows, head_dim
+// 64 and 128, contexts of 1,024-65,536), but for the 7: on the device 3 fit, but
+// a split costs the host a launch more and, where the caller brings no workspace, that
+// (four chains of drafts over up to 600 positions, split, 28 us a call for 14).
+// With 3, what the model chooses takes 1.02 times the fastest on the device in the
+// mean (1.15 at most), no split 1.9 times; with 7 it leaves contexts of 1,024 whole
+// (1.11 there), longer ones as with 3.  Constants by classes of rows and no time per
+// partition: 1.06 and 1.75.  For example (us, the
 // chosen one first): 4 x 16,384 positions, 8 heads of 64 rows, 32 tiles 64, 15 tiles
 // 70, unsplit 178; 1 x 65,536, one head of 4 rows, 9 tiles 25, 3 tiles 39, unsplit 364.
 // Above 16 partitions the search takes steps of a sixteenth, and the numbers that fill
 // one, two and three rounds (66 evaluations at most; all of them choose no better).
 long long fp8_partition_tiles(long long units, long long rows, int head_dim, long long tiles) {
-  constexpr double kTileUs = 1.5, kItemTiles = 2.0, kLeast = 0.8, kJoinUs = 3.0, kPartUs = 0.2;
+  constexpr double kTileUs = 1.5, kItemTiles = 2.0, kLeast = 0.8, kJoinUs = 7.0, kPartUs = 0.2;
   const long long slots = (rows > 32 ? 1 : 2) * (long long)device_sms();
   const double part_us =
       kPartUs + (double)units * (double)std::min<long long>(rows, pkv::kFp8Rows) * head_dim * 8.0 / 6.8e6;
