@@ -80,9 +80,11 @@
 //   two CTAs per SM, items taken as they come, seldom code
 //     kept short (met for the first time it runs at the
 //     latency of its fetch)                                   164     76     165
-//   weights in e5m2, one arrival per warp                     159     73     154
+//   weights in e5m2, one arrival per warp                     170     83     154
 //   two CTAs per SM with two key warpgroups each              156     70     125
 //   four key warpgroups: each tile once for 64 rows           161     69     100
+//   three parts of bf16 queries, weights to 2^-31 of the
+//     largest, V rows of any sizes                            161     70     109
 
 #include <math_constants.h>
 
@@ -116,16 +118,17 @@ constexpr int kAbove = 1, kBelow = 6;
 constexpr int kBand = (kAbove + kBelow) * 128;
 constexpr int kNoScale = 0x10000;  // before any: no scale's bits are in its band
 
-// E from the bits of a scale that is to be 2^up below it (down to 2^-126: a band that
-// leaves out a scale of zero).
-__device__ __forceinline__ int reference_above(int bits, int up) {
-  return max(bits + (up - kBelow) * 128, 0x80);
-}
+// E of the scale with the given bits (no lower than 2^-120: a band that leaves out a
+// scale of zero).
+__device__ __forceinline__ int reference_of(int bits) { return max(bits - kBelow * 128, 0x80); }
 
-// Registers with several key warpgroups.  Two: 256 threads of 88 and 256 of 40, out
-// of 512 of 64; four: 512 of 96 and 256 of 40, out of 768 of 80.
-constexpr int kFewRegs = 40;
-constexpr int key_regs(int warpgroups) { return warpgroups == 2 ? 88 : 96; }
+// Registers with several key warpgroups.  Two: 256 threads of 96 and 256 of 32, out
+// of 512 of 64 (88 and 40: 32 x 4,096, 8 heads of 32 rows 77.9 us for 71.6, L2
+// flushed).  Four: 512 of 96 and 256 of 40, out of 768 of 80 (104 and 32: the same
+// for 64 rows, and items of three tiles, whose starts the other warps' spills
+// delay, 40 x 5,422, 5 heads of 34 rows 220 us for 200).
+constexpr int kKeyRegs = 96;
+constexpr int few_regs(int warpgroups) { return warpgroups == 2 ? 32 : 40; }
 
 constexpr int up16(int x) { return (x + 15) / 16 * 16; }
 constexpr int pow2_at_least(int x, int p = 32) { return p >= x ? p : pow2_at_least(x, 2 * p); }
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
   Item it;
   // (Said in each branch: where they meet, the compiler counts on the least.)
   auto few_registers = [] {
-    if constexpr (L::KG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if constexpr (L::KG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(few_regs(L::KG)));
   };
 
   if (warp > L::kReaders) {
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
     mbar_drain(d, 0);
     __syncwarp();
   } else {
-    if constexpr (L::KG > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(key_regs(L::KG)));
+    if constexpr (L::KG > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kKeyRegs));
     // ----------------------------------------------------- key warpgroups
     // Code that runs once per item or seldom is kept short (loops that stay
     // loops): straight-line code met for the first time runs at the latency of
@@ -1011,7 +1014,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
           four.y &= (n > 3 ? 0xffffff80u : n > 2 ? 0xff80u : 0u);
           const uint32_t two = __vmaxu2(four.x, four.y);
           const int most = (int)__reduce_max_sync(0xffffffffu, max(two & 0xff80u, two >> 16));
-          if (most >= 0x80 && most < 0x7f80) ref_v = reference_above(most, 0);
+          if (most >= 0x80 && most < 0x7f80) ref_v = reference_of(most);
         }
         Pair y[NHW / 2];
         load_parts<kQParts, NH, NHW>(tmem + sb * L::NS + hb + lane_base, y);
@@ -1057,12 +1060,13 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
         }
         // What this key's V scale does: y = x + lv, l gets p * 2^-lv.  Scales out of
         // the band, NaN among them, are looked after below.
-        vb = valid ? vb & 0xff80u : ref_v + kBelow * 128;
+        vb &= 0xff80u;
+        if (nvalid < kKeys && !valid) vb = ref_v + kBelow * 128;
         const uint32_t in_band = vb - ref_v;
         const bool odd = in_band > kBand;
         const float lvf = fmaf(__uint_as_float(0x4b000000u + in_band), 1.f / 128,  // 2^23 + in_band
                                -(65536.f + kBelow));
-        float inv_v = __uint_as_float(((127u + kBelow) << 23) - (in_band << 16));
+        int lv_bits = in_band;  // (lv + kBelow) * 128
         const Pair ks2 = pair(ks, ks), lv2 = pair(lvf, lvf);
 #pragma unroll
         for (int g = 0; g < NHW / 2; ++g) y[g] = fma2(y[g], mul2(pair_at(factors, g), ks2), lv2);
@@ -1083,6 +1087,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
         }
         if (group_any(kg, top > kExceed || unset || odd)) {
           bool low = false, apart = false;  // this key, some of the tile's are added apart
+          float shrink = 1.f;
           const bool again = i == 0 && tail;
           if (__builtin_expect(group_any(kg, odd || again), 0)) {
             const bool v_nan = vb >= 0x7f80u;
@@ -1092,32 +1097,15 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
             named_barrier_sync(1 + kg, 128);
             const int largest = max(max(marks[0], marks[1]), max(marks[2], marks[3]));
             if (largest >= 0x80 && (again || ref_v == kNoScale || largest > ref_v + kBand)) {
-              // E moves, and the O^T so far with it.
+              // E moves, and the O^T so far with it (below).
               const int old = ref_v;
-              ref_v = reference_above(largest, 0);
-              if (i > 0 && old != kNoScale) {
-                const int up = (ref_v - old) / 128;
-                const float shrink = up > 126 ? 0.f : pow2(-up);
-                ok = ok && mbar_wait(&p_free[(kt - 1) % PB], ((kt - 1) / PB) & 1, p.status);
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < (far ? kParts + 1 : kParts); ++c) {
-                  const uint32_t addr =
-                      tmem + L::kColO + (c < kParts ? c * NH : L::NO) + hb + lane_base;
-                  float o[NHW];
-                  tmem_load_small<NHW>(addr, o);
-#pragma unroll
-                  for (int g = 0; g < NHW; ++g) o[g] *= shrink;
-                  tmem_store_small<NHW>(addr, o);
-                }
-                tc_fence_before();
-              }
+              ref_v = reference_of(largest);
+              if (i > 0) shrink = old == kNoScale || ref_v - old > 126 * 128 ? 0.f : pow2((old - ref_v) / 128);
             }
             const int at = (int)vb - ref_v;
             const int lv = min(max(at >> 7, 0), kAbove + kBelow) - kBelow;
             const float by = v_nan ? CUDART_NAN_F : (float)lv - lvf;
-            inv_v = pow2(-lv);
+            lv_bits = (lv + kBelow) * 128;
 #pragma unroll
             for (int g = 0; g < NHW / 2; ++g) {  // (-infinity: not seen)
               if (e[g].x > -CUDART_INF_F) e[g].x += by;
@@ -1155,7 +1143,11 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
             l_part[g] = mul2(l_part[g], pair_at(alphas, g));
             e[g] = both(add2(pair(e[g].x, e[g].y), pair_at(shifts, g)));
           }
-          if (i > 0 && moved) {
+          if (__builtin_expect(shrink != 1.f, 0)) {
+            if (lane < NHW) alphas[row] *= shrink;
+            __syncwarp();
+          }
+          if (i > 0 && (moved || shrink != 1.f)) {
             // O^T holds this item's tiles so far: rescaled once their MMAs are
             // done (P buffer of the previous tile released).
             ok = ok && mbar_wait(&p_free[(kt - 1) % PB], ((kt - 1) / PB) & 1, p.status);
@@ -1233,8 +1225,9 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
             }
             if (low) {
 #pragma unroll
-              for (int g = 0; g < NHW / 2; ++g) {
-                l_part[g] = fma2(pair(ex2(e[g].x), ex2(e[g].y)), pair(inv_v, inv_v), l_part[g]);
+              for (int g = 0; g < NHW / 2; ++g) {  // (lv = -kBelow)
+                l_part[g] = fma2(pair(ex2(e[g].x), ex2(e[g].y)),
+                                 pair(pow2(kBelow), pow2(kBelow)), l_part[g]);
                 e[g] = make_float2(-CUDART_INF_F, -CUDART_INF_F);
               }
             }
@@ -1246,6 +1239,7 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
         // (Nothing to wait for in the first PB: their phase before the first counts
         // as completed.)
         const bool p_here = mbar_test_wait(&p_free[pb], p_phase ^ 1);
+        const float inv_v = __uint_as_float(((127u + kBelow) << 23) - ((uint32_t)lv_bits << 16));
         const Pair inv2 = pair(inv_v, inv_v);
         uint32_t h[NHW / 2];
 #pragma unroll
@@ -1319,16 +1313,22 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
       constexpr int kOut = NHW < 8 ? NHW : 8;
       // 2^E
       const float v_scale = ref_v == kNoScale ? 1.f : pow2((ref_v >> 7) - 127 + kBelow);
+      if (__builtin_expect(far, 0)) {  // the rows added apart, into the first part
+#pragma unroll 1
+        for (int g = 0; g < NHW; g += 4) {
+          const uint32_t addr = tmem + L::kColO + hb + g + lane_base;
+          float o[4], x[4];
+          tmem_load_small<4>(addr, o);
+          tmem_load_small<4>(addr + L::NO, x);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[u] += x[u];
+          tmem_store_small<4>(addr, o);
+        }
+      }
 #pragma unroll 1
       for (int g = 0; g < NHW && g < there; g += kOut) {
         Pair o[kOut / 2];
         load_parts<kParts, NH, kOut>(tmem + L::kColO + hb + g + lane_base, o);
-        if (far) {
-          float x[kOut];
-          tmem_load_small<kOut>(tmem + L::kColFar + hb + g + lane_base, x);
-#pragma unroll
-          for (int u = 0; u < kOut / 2; ++u) o[u] = add2(o[u], pair(x[2 * u], x[2 * u + 1]));
-        }
 #pragma unroll
         for (int u = 0; u < kOut; ++u) {
           const float2 v = both(o[u / 2]);
@@ -1490,9 +1490,9 @@ cudaError_t launch_shape(const AttnFp8Params& p, const CUtensorMap& km, const CU
       cudaFuncAttributes attr;
       err = cudaFuncGetAttributes(&attr, attn_fp8_kernel<T, NH, D>);
       if (err != cudaSuccess) return err;
-      if (attr.numRegs < kFewRegs ||
+      if (attr.numRegs < few_regs(L::KG) ||
           (attr.numRegs + 7) / 8 * 8 * L::kThreads <
-              128 * L::KG * key_regs(L::KG) + (L::kThreads - 128 * L::KG) * kFewRegs)
+              128 * L::KG * kKeyRegs + (L::kThreads - 128 * L::KG) * few_regs(L::KG))
         return cudaErrorInvalidConfiguration;
     }
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
