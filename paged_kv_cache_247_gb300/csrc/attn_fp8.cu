@@ -42,9 +42,9 @@
 // of the item's first tile, and moves to a later tile's if that is more than twice
 // as large; the O^T so far shrinks by as much.  Rows below 2^-6 of it are added
 // apart, to an O^T of their own, in fp32 with their whole weights, and rows of zeros
-// not at all.  That takes 1.5 us a tile (3.4 with four warpgroups); where one token's V
-// is small in each context, a call takes 0 to 5 % more.  That the code is there
-// costs trees 4 % and decode nothing.  What is below 2^-126 of the largest row that
+// not at all.  That takes 0.6 us a tile for 4 rows, 3.4 for 64; where one token's V
+// is small in each context, a call takes 0 to 6 % more.  That the code is there
+// costs 64 rows 3 % and 4 nothing.  What is below 2^-126 of the largest row that
 // some query of the item sees may be lost.
 //
 // Orientation, pipeline and roles follow the 16-bit decode kernel: keys are the
@@ -69,10 +69,10 @@
 //   S, O issuers     four (D = 64: two, four) MMAs per tile
 //
 // Up to 8 rows the time is the cache's bytes: 64 x 8,192 positions, 8 heads of 128
-// with 4 rows 161 us, 6,780 GB/s; 64 contexts of 16-2,048, 40 heads of one row 69 us,
-// 5,470 GB/s, where the ends of items show.  More rows are bound by the key warps:
-// 32 x 4,096, 8 heads of 64 rows 100 us, 2,790 GB/s, issue slots 56 % used where an
-// SM works: 24 instructions a row and key warp for each tile, 4 of them the split in
+// with 4 rows 161 us, 6,780 GB/s; 64 contexts of 16-2,048, 40 heads of one row 70 us,
+// 5,370 GB/s, where the ends of items show.  More rows are bound by the key warps:
+// 32 x 4,096, 8 heads of 64 rows 109 us, 2,560 GB/s, issue slots 56 % used where an
+// SM works: 26 instructions a row and key warp for each tile, 4 of them the split in
 // three.  What it took, at those three cases (us):
 //   CUDA cores                                              2,406    349   3,998
 //   this form, one CTA per SM, items dealt out beforehand     201    127     392

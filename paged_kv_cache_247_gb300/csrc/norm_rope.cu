@@ -8,7 +8,7 @@
 // The mean and the products are 32-bit, the angle is formed and reduced to one
 // turn in 64 bits, and each element is rounded once, at the end.  Bound by HBM:
 // (Hq + Hkv) D elements read and as many written per token: 16,384 tokens of 32 + 8
-// heads of 128 with three axes 58.5 us, 5,740 GB/s.  (A CTA per token, sines and
+// heads of 128 with three axes 59.5 us, 5,640 GB/s.  (A CTA per token, sines and
 // cosines read from shared memory for every head: 104; kept in registers, the next
 // turn's rows in registers, too: 70; four turns ahead in shared memory: 58; two
 // and three ahead 68 and 60, four CTAs per SM instead of three 68.)
