@@ -13,6 +13,7 @@ it.  The scales that enter the product lie within 2^-6 and 2 of their reference,
 that a position loses at most 2^(7 - 31) of the largest weight, 2^-31 where all rows
 have the same scale, and between, where they differ by 2^k, 2^(k + 1) <= 2^(2 k) times that:
   lost_t = min(p_t, 2^(min(7, 2 k) - 31) max_s p_s).
+What is rounded last is the output with these errors in it: (1 + eps / 2) times them.
 """
 
 import math
@@ -67,7 +68,8 @@ def reference(c, held=0.0):
         e = e[~e.isnan()]
         k = float(e.max() - e.min()) if len(e) else 0.0
         lost = torch.minimum(p, 2.0 ** (min(7.0, 2 * k) - 31) * p.amax(-1, keepdim=True)) @ v[:, None].abs()
-        b = torch.finfo(c.dt).eps / 2 * o.abs() + (2 * dx + 2.0 ** -17 + 2.0 ** -11 + n * 2.0 ** -27) * size + lost
+        half = torch.finfo(c.dt).eps / 2
+        b = half * o.abs() + (1 + half) * ((2 * dx + 2.0 ** -17 + 2.0 ** -11 + n * 2.0 ** -27) * size + lost)
         b += 2.0 ** -25 if c.dt == torch.float16 else 2.0 ** -134              # half a subnormal step
         out[lo:hi] = o.permute(2, 0, 1, 3).reshape(L, hq, c.D)
         bound[lo:hi] = b.permute(2, 0, 1, 3).reshape(L, hq, c.D)
