@@ -1096,7 +1096,8 @@ __global__ void __launch_bounds__(Shape<NH, D>::kThreads, Shape<NH, D>::kPerSm)
             if (lane == 0) marks[warp & 3] = of_warp;
             named_barrier_sync(1 + kg, 128);
             const int largest = max(max(marks[0], marks[1]), max(marks[2], marks[3]));
-            if (largest >= 0x80 && (again || ref_v == kNoScale || largest > ref_v + kBand)) {
+            if (again) ref_v = kNoScale;  // (it may be of drafts that no row sees)
+            if (largest >= 0x80 && (ref_v == kNoScale || largest > ref_v + kBand)) {
               // E moves, and the O^T so far with it (below).
               const int old = ref_v;
               ref_v = reference_of(largest);
